@@ -25,7 +25,8 @@ EXPORTS = ("bq_quantize_blockwise", "bq_dequantize_blockwise", "bq_quantize_nest
            "bq_dequantize_nested", "bq_dequant_q32", "bq_iq2xs_quantize", "bq_iq2xs_dequantize",
            "bq_iq1s_quantize", "bq_iq1s_dequantize", "bq_nested_workspace_bytes", "bq_status_string",
            "bq_debug_nearest_codes", "bq_last_hip_error", "bq_linear_blockwise", "bq_gemm_blockwise",
-           "bq_debug_time_next_kernel", "bq_quantize_nested_noalloc")
+           "bq_debug_time_next_kernel", "bq_quantize_nested_noalloc", "bq_kv_write", "bq_kv_read",
+           "bq_kv_attention_workspace_bytes", "bq_kv_attention")
 
 
 class BQError(RuntimeError):
@@ -47,6 +48,19 @@ class bq_nested_stats(ctypes.Structure):
                 ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
 
 
+class bq_kv_cache(ctypes.Structure):
+    _fields_ = [("k_packed", ctypes.c_void_p), ("k_absmax", ctypes.c_void_p), ("v_packed", ctypes.c_void_p),
+                ("v_absmax", ctypes.c_void_p), ("table", ctypes.POINTER(bq_code_table)),
+                ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("blocksize", ctypes.c_int32)]
+
+
+class bq_kv_batch(ctypes.Structure):
+    _fields_ = [("q_start", ctypes.c_void_p), ("kv_len", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
+                ("table_stride", ctypes.c_int64), ("tokens", ctypes.c_int64), ("num_seqs", ctypes.c_int32),
+                ("max_q_len", ctypes.c_int32), ("max_kv_len", ctypes.c_int32)]
+
+
 def _load() -> ctypes.CDLL:
     if not os.path.exists(LIB_PATH):
         raise ImportError("libbq.so is not built (run: python dequantization_block_absmax_amd/build.py)")
@@ -61,6 +75,7 @@ def _load() -> ctypes.CDLL:
     vp, i64, i32, st = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_int
     tp = ctypes.POINTER(bq_code_table)
     sp = ctypes.POINTER(bq_nested_stats)
+    cp, bp, f32 = ctypes.POINTER(bq_kv_cache), ctypes.POINTER(bq_kv_batch), ctypes.c_float
     sig = {
         "bq_quantize_blockwise": [vp, st, i64, i32, tp, vp, vp, vp],
         "bq_dequantize_blockwise": [vp, st, i64, i32, tp, vp, vp, vp],
@@ -74,6 +89,9 @@ def _load() -> ctypes.CDLL:
         "bq_iq1s_dequantize": [vp, vp, i64, i64, st, vp, vp],
         "bq_linear_blockwise": [vp, st, i64, i64, i64, i32, tp, vp, vp, vp, vp],
         "bq_gemm_blockwise": [vp, st, i64, i64, i64, i32, tp, vp, vp, vp, vp],
+        "bq_kv_write": [cp, st, vp, vp, i64, i64, i64, vp, vp],
+        "bq_kv_read": [cp, st, vp, vp, i64, i64, i64, vp, vp],
+        "bq_kv_attention": [cp, bp, st, vp, i64, i32, f32, i32, i32, vp, i64, vp, vp, ctypes.c_size_t, vp],
     }
     for name, args in sig.items():
         f = getattr(lib, name)
@@ -81,6 +99,8 @@ def _load() -> ctypes.CDLL:
         f.restype = st
     lib.bq_nested_workspace_bytes.argtypes = [i64, i32, i32]
     lib.bq_nested_workspace_bytes.restype = ctypes.c_size_t
+    lib.bq_kv_attention_workspace_bytes.argtypes = [cp, bp, st, i32]
+    lib.bq_kv_attention_workspace_bytes.restype = ctypes.c_size_t
     lib.bq_debug_nearest_codes.argtypes = [tp, vp, i64, vp, vp, vp]
     lib.bq_debug_nearest_codes.restype = st
     lib.bq_debug_time_next_kernel.argtypes = [vp, vp]
@@ -159,6 +179,30 @@ def nested_stats(qabsmax, absmax2, mean, table, blocksize2: int = 256, workspace
     return s
 
 
+def kv_cache(k_packed, k_absmax, v_packed, v_absmax, table, num_pages: int, page_size: int, kv_heads: int,
+             head_dim: int, blocksize: int) -> bq_kv_cache:
+    """A bq_kv_cache over the caller's device buffers (the caller keeps them alive)."""
+    t = table if isinstance(table, bq_code_table) or table is None else code_table(table)
+    c = bq_kv_cache(_addr(k_packed), _addr(k_absmax), _addr(v_packed), _addr(v_absmax),
+                    ctypes.pointer(t) if t is not None else None, int(num_pages), int(page_size), int(kv_heads),
+                    int(head_dim), int(blocksize))
+    c._keep = t
+    return c
+
+
+def kv_batch(q_start, kv_len, page_table, tokens: int, max_q_len: int, max_kv_len: int, num_seqs: int | None = None,
+             table_stride: int | None = None) -> bq_kv_batch:
+    """A bq_kv_batch over the caller's device buffers; the number of sequences and the page table's
+    stride are read off the tensors where not given."""
+    if num_seqs is None:
+        num_seqs = kv_len.numel()
+    if table_stride is None:
+        # a table of one row may carry any stride: its length is what the row holds
+        table_stride = page_table.stride(0) if page_table.shape[0] > 1 else page_table.shape[1]
+    return bq_kv_batch(_addr(q_start), _addr(kv_len), _addr(page_table), int(table_stride), int(tokens),
+                       int(num_seqs), int(max_q_len), int(max_kv_len))
+
+
 # ---- entry points (same names as the C ABI; each returns the bq_status) -----------------
 
 def bq_quantize_blockwise(inp, dtype, n: int, blocksize: int, table, absmax, packed, stream=None) -> int:
@@ -227,6 +271,38 @@ def bq_gemm_blockwise(x, dtype, M: int, K: int, N: int, blocksize: int, table, a
                       stream=None) -> int:
     return _lib.bq_gemm_blockwise(_addr(x), dtype_code(dtype), int(M), int(K), int(N), int(blocksize),
                                   _table_ptr(table), _addr(absmax), _addr(packed), _addr(y), _stream(stream))
+
+
+def _struct_ptr(s):
+    return ctypes.pointer(s) if s is not None else None
+
+
+def bq_kv_write(cache: bq_kv_cache | None, dtype, k, v, tokens: int, k_stride: int, v_stride: int, slots,
+                stream=None) -> int:
+    return _lib.bq_kv_write(_struct_ptr(cache), dtype_code(dtype), _addr(k), _addr(v), int(tokens), int(k_stride),
+                            int(v_stride), _addr(slots), _stream(stream))
+
+
+def bq_kv_read(cache: bq_kv_cache | None, dtype, k, v, tokens: int, k_stride: int, v_stride: int, slots,
+               stream=None) -> int:
+    return _lib.bq_kv_read(_struct_ptr(cache), dtype_code(dtype), _addr(k), _addr(v), int(tokens), int(k_stride),
+                           int(v_stride), _addr(slots), _stream(stream))
+
+
+def bq_kv_attention_workspace_bytes(cache: bq_kv_cache | None, batch: bq_kv_batch | None, dtype, heads: int) -> int:
+    return int(_lib.bq_kv_attention_workspace_bytes(_struct_ptr(cache), _struct_ptr(batch), dtype_code(dtype),
+                                                    int(heads)))
+
+
+def bq_kv_attention(cache: bq_kv_cache | None, batch: bq_kv_batch | None, dtype, q, q_stride: int, heads: int,
+                    scale: float, causal: int, window: int, out, out_stride: int, lse=None, workspace=None,
+                    workspace_bytes: int | None = None, stream=None) -> int:
+    if workspace_bytes is None:
+        workspace_bytes = 0 if workspace is None or isinstance(workspace, int) else \
+            workspace.numel() * workspace.element_size()
+    return _lib.bq_kv_attention(_struct_ptr(cache), _struct_ptr(batch), dtype_code(dtype), _addr(q), int(q_stride),
+                                int(heads), float(scale), int(causal), int(window), _addr(out), int(out_stride),
+                                _addr(lse), _addr(workspace), int(workspace_bytes), _stream(stream))
 
 
 def bq_nested_workspace_bytes(n: int, blocksize: int, blocksize2: int = 256) -> int:

@@ -8,6 +8,7 @@
 // upload measured in "Cache device-side constants in dequant kernels", ComfyUI-GGUF PR 472,
 // "Problem", and the graph-capture limitation in PR 2052, "Limitations").
 #include <hip/hip_runtime_api.h>
+#include <math.h>
 #include <string.h>
 
 #include <mutex>
@@ -121,12 +122,12 @@ const char* bq_status_string(bq_status s) {
     case BQ_OK: return "ok";
     case BQ_ERR_NULL: return "a required pointer is NULL";
     case BQ_ERR_DTYPE: return "unknown dtype";
-    case BQ_ERR_SIZE: return "invalid element count";
+    case BQ_ERR_SIZE: return "invalid count, length or stride";
     case BQ_ERR_BLOCKSIZE: return "block size must be a power of two in [32, 4096]";
     case BQ_ERR_TABLE: return "invalid code table";
     case BQ_ERR_ALIGNMENT: return "misaligned device pointer";
-    case BQ_ERR_FORMAT: return "unknown block format or row length";
-    case BQ_ERR_WORKSPACE: return "nested workspace missing or too small";
+    case BQ_ERR_FORMAT: return "unknown block format, row length, page size or head size";
+    case BQ_ERR_WORKSPACE: return "workspace missing or too small";
     case BQ_ERR_HIP: return "HIP launch failed";
   }
   return "unknown status";
@@ -372,6 +373,160 @@ bq_status bq_iq2xs_dequantize(const uint8_t* blocks, const uint8_t* grid, int64_
   if (blocks == nullptr || grid == nullptr || out == nullptr) return BQ_ERR_NULL;
   if (!aligned(blocks, 2) || !aligned(grid, 8) || !aligned(out, 16)) return BQ_ERR_ALIGNMENT;
   return hip_status(bq::launch_iq2xs_dequantize(blocks, grid, n, dtype, out, stream));
+}
+
+static int log2_of(int32_t v) {
+  int l = 0;
+  while ((1 << l) < v) ++l;
+  return l;
+}
+
+// Shape, block size and table of a cache (its pointers are looked at by check_cache_pointers).
+static bq_status check_cache(const bq_kv_cache* c, bq::PreparedTable* t, bq::KvCacheArgs* out) {
+  if (c == nullptr) return BQ_ERR_NULL;
+  if (c->num_pages < 1 || c->kv_heads < 1) return BQ_ERR_SIZE;
+  if (c->page_size < 16 || c->page_size > 4096 || (c->page_size & (c->page_size - 1)) != 0) return BQ_ERR_FORMAT;
+  if (c->head_dim < 32 || c->head_dim > 256 || c->head_dim % 32 != 0) return BQ_ERR_FORMAT;
+  if (!valid_blocksize(c->blocksize) || c->head_dim % c->blocksize != 0) return BQ_ERR_BLOCKSIZE;
+  // at most 2^12 * 8 blocks per page and head; two steps, so that no product overflows
+  const int64_t per_page = (int64_t)c->page_size * (c->head_dim / c->blocksize);
+  if ((int64_t)c->num_pages * c->kv_heads > INT32_MAX / per_page) return BQ_ERR_SIZE;
+  const bq_status st = check_table(c->table, t);
+  if (st != BQ_OK) return st;
+  *out = {{c->k_packed, c->v_packed}, {c->k_absmax, c->v_absmax}, c->num_pages, log2_of(c->page_size),
+          c->kv_heads, c->head_dim, log2_of(c->blocksize)};
+  return BQ_OK;
+}
+
+static bq_status check_cache_pointers(const bq_kv_cache* c) {
+  if (c->k_packed == nullptr || c->k_absmax == nullptr || c->v_packed == nullptr || c->v_absmax == nullptr)
+    return BQ_ERR_NULL;
+  if (!aligned(c->k_packed, 16) || !aligned(c->k_absmax, 16) || !aligned(c->v_packed, 16) || !aligned(c->v_absmax, 16))
+    return BQ_ERR_ALIGNMENT;
+  return BQ_OK;
+}
+
+// What bq_kv_write and bq_kv_read check alike (*done: nothing to enqueue).
+static bq_status check_kv_rows(const bq_kv_cache* cache, bq_dtype dtype, const void* k, const void* v, int64_t tokens,
+                               int64_t k_stride, int64_t v_stride, const int64_t* slots, bq::PreparedTable* t,
+                               bq::KvCacheArgs* ca) {
+  if (!valid_dtype(dtype)) return BQ_ERR_DTYPE;
+  const bq_status st = check_cache(cache, t, ca);
+  if (st != BQ_OK) return st;
+  if ((int64_t)cache->kv_heads * cache->head_dim >= (int64_t)1 << 34) return BQ_ERR_SIZE;
+  const int64_t row = (int64_t)cache->kv_heads * cache->head_dim;
+  if (tokens < 0 || tokens > (((int64_t)1 << 34) - 1) / row) return BQ_ERR_SIZE;
+  const int64_t size = dtype == BQ_F32 ? 4 : 2;
+  // the last row's byte offset fits 62 bits
+  const int64_t most = tokens > 1 ? ((int64_t)1 << 60) / tokens : (int64_t)1 << 60;
+  if (k_stride < row || v_stride < row || k_stride > most || v_stride > most) return BQ_ERR_SIZE;
+  if (tokens == 0) return BQ_OK;
+  const bq_status pt = check_cache_pointers(cache);
+  if (pt == BQ_ERR_NULL || k == nullptr || v == nullptr || slots == nullptr) return BQ_ERR_NULL;
+  if (pt != BQ_OK || !aligned(k, 16) || !aligned(v, 16) || !aligned(slots, 8) || (k_stride * size) % 16 != 0 ||
+      (v_stride * size) % 16 != 0)
+    return BQ_ERR_ALIGNMENT;
+  return BQ_OK;
+}
+
+bq_status bq_kv_write(const bq_kv_cache* cache, bq_dtype dtype, const void* k, const void* v, int64_t tokens,
+                      int64_t k_stride, int64_t v_stride, const int64_t* slots, hipStream_t stream) {
+  Tables t;
+  bq::KvCacheArgs ca;
+  const bq_status st = check_kv_rows(cache, dtype, k, v, tokens, k_stride, v_stride, slots, &t.data, &ca);
+  if (st != BQ_OK || tokens == 0) return st;
+  return hip_status(bq::launch_kv_write(ca, dtype, k, v, tokens, k_stride, v_stride, slots, t.data, stream));
+}
+
+bq_status bq_kv_read(const bq_kv_cache* cache, bq_dtype dtype, void* k, void* v, int64_t tokens, int64_t k_stride,
+                     int64_t v_stride, const int64_t* slots, hipStream_t stream) {
+  Tables t;
+  bq::KvCacheArgs ca;
+  const bq_status st = check_kv_rows(cache, dtype, k, v, tokens, k_stride, v_stride, slots, &t.data, &ca);
+  if (st != BQ_OK || tokens == 0) return st;
+  bq::DequantArgs a;
+  memset(&a, 0, sizeof(a));
+  memcpy(a.c, t.data.c, sizeof(float) * t.data.K);
+  a.K = t.data.K;
+  return hip_status(bq::launch_kv_read(ca, dtype, k, v, tokens, k_stride, v_stride, slots, a, stream));
+}
+
+// Shape of an attention call; fills everything of `a` but the data pointers.
+static bq_status check_attention_shape(const bq_kv_cache* cache, const bq_kv_batch* b, bq_dtype dtype, int32_t heads,
+                                       bq::PreparedTable* t, bq::KvAttendArgs* a) {
+  if (dtype != BQ_F16 && dtype != BQ_BF16) return BQ_ERR_DTYPE;
+  memset(a, 0, sizeof(*a));
+  const bq_status st = check_cache(cache, t, &a->cache);
+  if (st != BQ_OK) return st;
+  if (cache->head_dim != 64 && cache->head_dim != 128 && cache->head_dim != 256) return BQ_ERR_FORMAT;
+  if (b == nullptr) return BQ_ERR_NULL;
+  if (heads < 1 || heads % cache->kv_heads != 0 || heads > (1 << 20)) return BQ_ERR_SIZE;
+  if (b->num_seqs < 0 || b->num_seqs > 65535 || b->tokens < 0 || b->tokens > INT32_MAX || b->table_stride < 0 ||
+      b->table_stride > INT32_MAX || b->max_q_len < 0 || b->max_kv_len < 0)
+    return BQ_ERR_SIZE;
+  a->table_stride = b->table_stride;
+  a->tokens = b->tokens;
+  a->num_seqs = b->num_seqs;
+  a->max_q_len = b->max_q_len;
+  if (a->max_q_len > a->tokens) a->max_q_len = (int32_t)a->tokens;
+  // keys the page table can hold at all
+  const int64_t held = b->table_stride * cache->page_size;
+  a->max_kv_len = held < b->max_kv_len ? (int32_t)held : b->max_kv_len;
+  a->heads = heads;
+  return BQ_OK;
+}
+
+size_t bq_kv_attention_workspace_bytes(const bq_kv_cache* cache, const bq_kv_batch* batch, bq_dtype dtype,
+                                       int32_t heads) {
+  Tables t;
+  bq::KvAttendArgs a;
+  if (check_attention_shape(cache, batch, dtype, heads, &t.data, &a) != BQ_OK) return 0;
+  if (a.tokens == 0 || a.num_seqs == 0 || a.max_q_len == 0) return 0;
+  return bq::kv_attend_workspace(a, t.data.K);
+}
+
+bq_status bq_kv_attention(const bq_kv_cache* cache, const bq_kv_batch* batch, bq_dtype dtype, const void* q,
+                          int64_t q_stride, int32_t heads, float scale, int32_t causal, int32_t window, void* out,
+                          int64_t out_stride, float* lse, void* workspace, size_t workspace_bytes,
+                          hipStream_t stream) {
+  Tables t;
+  bq::KvAttendArgs a;
+  const bq_status st = check_attention_shape(cache, batch, dtype, heads, &t.data, &a);
+  if (st != BQ_OK) return st;
+  const int64_t row = (int64_t)heads * cache->head_dim;
+  const int64_t most = (int64_t)1 << 29;  // rows number less than 2^31: byte offsets fit 62 bits
+  if (q_stride < row || out_stride < row || q_stride > most || out_stride > most || window < 0 || !isfinite(scale))
+    return BQ_ERR_SIZE;
+  if (a.tokens == 0 || a.num_seqs == 0 || a.max_q_len == 0) return BQ_OK;
+  const bq_status pt = check_cache_pointers(cache);
+  if (pt == BQ_ERR_NULL || q == nullptr || out == nullptr || batch->q_start == nullptr || batch->kv_len == nullptr ||
+      batch->page_table == nullptr)
+    return BQ_ERR_NULL;
+  if (pt != BQ_OK || !aligned(q, 16) || !aligned(out, 16) || q_stride % 8 != 0 || out_stride % 8 != 0 ||
+      !aligned(batch->q_start, 4) || !aligned(batch->kv_len, 4) || !aligned(batch->page_table, 4) || !aligned(lse, 4))
+    return BQ_ERR_ALIGNMENT;
+  const size_t need = bq::kv_attend_workspace(a, t.data.K);
+  if (need > 0) {
+    if (workspace == nullptr || workspace_bytes < need) return BQ_ERR_WORKSPACE;
+    if (!aligned(workspace, 256)) return BQ_ERR_ALIGNMENT;
+  }
+  a.q_start = batch->q_start;
+  a.kv_len = batch->kv_len;
+  a.page_table = batch->page_table;
+  a.q = q;
+  a.q_stride = q_stride;
+  a.out = out;
+  a.out_stride = out_stride;
+  a.lse = lse;
+  a.causal = causal != 0;
+  a.window = window;
+  a.scale = scale;
+  a.workspace = workspace;
+  bq::DequantArgs da;
+  memset(&da, 0, sizeof(da));
+  memcpy(da.c, t.data.c, sizeof(float) * t.data.K);
+  da.K = t.data.K;
+  return hip_status(bq::launch_kv_attend(a, dtype, da, stream));
 }
 
 }  // extern "C"

@@ -57,16 +57,17 @@ typedef enum {
   BQ_OK = 0,
   BQ_ERR_NULL = 1,      /* a required pointer is NULL */
   BQ_ERR_DTYPE = 2,     /* dtype is not a bq_dtype */
-  BQ_ERR_SIZE = 3,      /* n < 0, more than INT32_MAX blocks, n not a whole number of rows, or a
+  BQ_ERR_SIZE = 3,      /* a count, length or stride out of its range: n < 0, more than INT32_MAX blocks, n not a whole number of rows, or a
                            launch of more than 2^32 - 1 threads, refused before any work is
                            enqueued (quantize and 4-bit dequantize from 2^37 elements, 8-bit
                            dequantize from 2^36) */
   BQ_ERR_BLOCKSIZE = 4, /* blocksize not a power of two in [32, 4096] */
   BQ_ERR_TABLE = 5,     /* code table: size, order, range or spacing (see bq_code_table) */
   BQ_ERR_ALIGNMENT = 6, /* a device pointer is not aligned as required */
-  BQ_ERR_FORMAT = 7,    /* unknown bq_q32_format, or row_len not a multiple of 32 (of 256 for
-                           the IQ2_XS- and IQ1_S-style calls) */
-  BQ_ERR_WORKSPACE = 8, /* nested workspace missing or smaller than bq_nested_workspace_bytes */
+  BQ_ERR_FORMAT = 7,    /* unknown bq_q32_format, row_len not a multiple of 32 (of 256 for
+                           the IQ2_XS- and IQ1_S-style calls), or page_size or head_dim of a cache */
+  BQ_ERR_WORKSPACE = 8, /* workspace missing or smaller than bq_nested_workspace_bytes or
+                           bq_kv_attention_workspace_bytes */
   BQ_ERR_HIP = 9        /* the HIP runtime rejected a launch */
 } bq_status;
 
@@ -308,6 +309,99 @@ bq_status bq_iq1s_quantize(const void* in, bq_dtype dtype, int64_t n, int64_t ro
  * Errors: as bq_iq1s_quantize. */
 bq_status bq_iq1s_dequantize(const uint8_t* blocks, const int8_t* grid, int64_t n, int64_t row_len,
                              bq_dtype dtype, void* out, hipStream_t stream);
+
+/* ---- A paged key/value cache in blockwise codes --------------------------------------------
+ *
+ * The cache of a served transformer: a pool of pages of `page_size` tokens each, for keys and for
+ * values.  Element (page, head, slot, d) of a pool is flat element
+ *     ((page * kv_heads + head) * page_size + slot) * head_dim + d
+ * of an array held exactly as bq_quantize_blockwise holds it (packed codes and block maxima; B
+ * divides head_dim, so a block holds elements of one token's head): bq_dequantize_blockwise
+ * expands a whole pool.  Token slot s of the cache is slot s % page_size of page s / page_size.
+ * Which pages belong to which sequence is the caller's affair (see bq_kv_batch). */
+typedef struct {
+  uint8_t* k_packed;  /* [device] codes of num_pages * kv_heads * page_size * head_dim keys, 16-byte aligned */
+  float* k_absmax;    /* [device] their block maxima, 16-byte aligned */
+  uint8_t* v_packed;  /* [device] the values' codes, 16-byte aligned */
+  float* v_absmax;    /* [device] the values' block maxima, 16-byte aligned */
+  const bq_code_table* table; /* [host] 16 or 256 entries, for keys and values */
+  int32_t num_pages;
+  int32_t page_size;  /* tokens per page: a power of two from 16 to 4096 */
+  int32_t kv_heads;
+  int32_t head_dim;   /* a multiple of 32 from 32 to 256 (bq_kv_attention: 64, 128 or 256) */
+  int32_t blocksize;  /* a power of two from 32 that divides head_dim */
+} bq_kv_cache;
+
+/* Quantizes the keys and values of `tokens` new tokens into the cache, by the absmax, normalize and
+ * nearest rules above (the codes and maxima are those of bq_quantize_blockwise, bit for bit).
+ *   k, v       [device] tokens rows of kv_heads * head_dim elements of `dtype`, 16-byte aligned.
+ *   k_stride, v_stride
+ *              elements from one token's row to the next, at least kv_heads * head_dim, a multiple of
+ *              16 bytes (the rows may be parts of a fused projection's output).
+ *   slots      [device] one cache slot per token, 8-byte aligned.  A token whose slot is outside
+ *              [0, num_pages * page_size) is not written.  Slots must differ: of two tokens with one
+ *              slot, either may be kept, in parts.
+ * Errors: BQ_ERR_DTYPE; BQ_ERR_SIZE (tokens negative or tokens * kv_heads * head_dim >= 2^34, a pool of
+ * more than INT32_MAX blocks, num_pages or kv_heads below 1, a stride too short); BQ_ERR_FORMAT
+ * (page_size or head_dim); BQ_ERR_BLOCKSIZE; BQ_ERR_TABLE; BQ_ERR_NULL; BQ_ERR_ALIGNMENT; BQ_ERR_HIP.
+ * tokens == 0 enqueues nothing. */
+bq_status bq_kv_write(const bq_kv_cache* cache, bq_dtype dtype, const void* k, const void* v, int64_t tokens,
+                      int64_t k_stride, int64_t v_stride, const int64_t* slots, hipStream_t stream);
+
+/* Reads the keys and values of `tokens` cache slots back, each element RN(fl32(c[q] * a)) as
+ * bq_dequantize_blockwise gives it; a token whose slot is outside the pool reads as zeros.
+ *   k, v       [device] out: tokens rows of kv_heads * head_dim elements of `dtype`, 16-byte aligned, with
+ *              strides as in bq_kv_write.
+ *   slots      [device] one cache slot per token, 8-byte aligned, in any order, repeats allowed.
+ * Errors: as bq_kv_write. */
+bq_status bq_kv_read(const bq_kv_cache* cache, bq_dtype dtype, void* k, void* v, int64_t tokens, int64_t k_stride,
+                     int64_t v_stride, const int64_t* slots, hipStream_t stream);
+
+/* The sequences of one attention call.  Sequence s brings the new tokens q_start[s] ..
+ * q_start[s + 1] - 1 (rows of q and out) and has kv_len[s] tokens in the cache, its new ones included:
+ * key j is in slot j % page_size of page page_table[s * table_stride + j / page_size].  New token i of
+ * n stands at position kv_len[s] - n + i. */
+typedef struct {
+  const int32_t* q_start;    /* [device] num_seqs + 1 ascending row numbers */
+  const int32_t* kv_len;     /* [device] num_seqs; read as at most max_kv_len and table_stride * page_size */
+  const int32_t* page_table; /* [device] num_seqs rows; a page outside the pool hides its keys */
+  int64_t table_stride;      /* entries from one row to the next */
+  int64_t tokens;            /* rows of q and out; rows outside every sequence are left as they are */
+  int32_t num_seqs;          /* at most 65535 */
+  int32_t max_q_len;         /* no sequence brings more new tokens (later ones are left out) */
+  int32_t max_kv_len;        /* no sequence has more keys (later ones are left out) */
+} bq_kv_batch;
+
+/* Bytes of workspace bq_kv_attention needs for this call's shape (the batch's pointers are not
+ * read); 0 if an argument is not valid.  It depends on the device's number of compute units. */
+size_t bq_kv_attention_workspace_bytes(const bq_kv_cache* cache, const bq_kv_batch* batch, bq_dtype dtype,
+                                       int32_t heads);
+
+/* Attention of new tokens over the cache, for single tokens (decoding), a few (drafts) and long
+ * pieces of a prompt alike:
+ *     out[i] = sum_j p_ij v_j,   p_ij = softmax over j of scale * (q_i . k_j),
+ * query head h over key/value head h / (heads / kv_heads), keys and values being the cached
+ * fl32(c[q] * a).  Row i at position t sees the keys j <= t if `causal` is nonzero, else all kv_len;
+ * of these, if window > 0, those with j > t - window.  Cached values of keys it does not see do not
+ * matter (they may be NaN).  A row that sees no key gives zeros, and -infinity in lse.
+ *   dtype      BQ_F16 or BQ_BF16: the type of q and out.
+ *   q          [device] tokens rows of heads * head_dim elements, 16-byte aligned; q_stride elements
+ *              from row to row (at least heads * head_dim, a multiple of 8).
+ *   heads      a positive multiple of kv_heads.
+ *   out        [device] out: rows as in q, with out_stride.
+ *   lse        [device] out, or NULL: tokens x heads binary32, the natural logarithm of
+ *              sum_j exp(scale * (q_i . k_j)).
+ *   workspace  [device] bq_kv_attention_workspace_bytes bytes, 256-byte aligned (NULL if that is 0).
+ * Products are summed in binary32; see k_attn.hip for what is rounded to 16 bits on the way.
+ * Results are the same on every call on one device.  Block maxima of keys that are seen must be
+ * finite and at most 2^100.
+ * Errors: BQ_ERR_DTYPE; BQ_ERR_SIZE (a negative count or length, num_seqs > 65535, heads, a stride,
+ * window < 0, a scale that is not finite, or a launch of more than 2^32 - 1 threads); BQ_ERR_WORKSPACE;
+ * otherwise as bq_kv_write.  tokens, num_seqs or max_q_len of 0 enqueue nothing. */
+bq_status bq_kv_attention(const bq_kv_cache* cache, const bq_kv_batch* batch, bq_dtype dtype, const void* q,
+                          int64_t q_stride, int32_t heads, float scale, int32_t causal, int32_t window, void* out,
+                          int64_t out_stride, float* lse, void* workspace, size_t workspace_bytes,
+                          hipStream_t stream);
 
 /* The hipError_t (as int) of the most recent launch that failed on the calling thread with
  * BQ_ERR_HIP, or 0 if none has. */
