@@ -1,0 +1,96 @@
+// bq_attn.h -- device helpers shared by the attention kernels (k_attn.hip, k_attn_merge.hip).
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include "bq_internal.h"
+
+namespace bq {
+
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
+typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+
+// 2^x and log2 x by the hardware instructions (about one unit in the last place; results below the
+// normal range are zero).
+__device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
+__device__ __forceinline__ float log2_hw(float x) { return __builtin_amdgcn_logf(x); }
+
+// Maximum and sum over the four 16-lane rows of a wave (lanes l, l ^ 16, l ^ 32, l ^ 48), in every lane.
+__device__ __forceinline__ float rows_max(float v) {
+  u32x2 s = __builtin_amdgcn_permlane32_swap(f32_bits(v), f32_bits(v), false, false);
+  v = fmaxf(bits_f32(s.x), bits_f32(s.y));
+  s = __builtin_amdgcn_permlane16_swap(f32_bits(v), f32_bits(v), false, false);
+  return fmaxf(bits_f32(s.x), bits_f32(s.y));
+}
+
+__device__ __forceinline__ float rows_sum(float v) {
+  u32x2 s = __builtin_amdgcn_permlane32_swap(f32_bits(v), f32_bits(v), false, false);
+  v = bits_f32(s.x) + bits_f32(s.y);
+  s = __builtin_amdgcn_permlane16_swap(f32_bits(v), f32_bits(v), false, false);
+  return bits_f32(s.x) + bits_f32(s.y);
+}
+
+// Two binary32 values as a pair of 16-bit ones (round to nearest even), the first in the low half.
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const f32x2 v = {lo, hi};
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, f16x2));
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const f32x2 v = {lo, hi};
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
+}
+
+__device__ __forceinline__ uint32_t pack16(float lo, float hi, bool bf16) {
+  return bf16 ? pack_bf16(lo, hi) : pack_f16(lo, hi);
+}
+
+// A sequence's rows and keys, clamped to what the call allows.
+struct Sequence {
+  int q0, nq;  // first row of q, new tokens
+  int kv;      // keys
+};
+
+__device__ __forceinline__ Sequence sequence(const KvAttendArgs& aa, int seq) {
+  Sequence s;
+  const int first = max(aa.q_start[seq], 0);
+  const int last = (int)min((int64_t)aa.q_start[seq + 1], aa.tokens);
+  s.q0 = first;
+  // positions count all new tokens; rows past max_q_len are left out by the grid
+  s.nq = max(last - first, 0);
+  s.kv = max(min(aa.kv_len[seq], aa.max_kv_len), 0);
+  return s;
+}
+
+// Keys [lo, hi) that the new token i of the sequence sees.
+__device__ __forceinline__ int first_key(const KvAttendArgs& aa, const Sequence& s, int i) {
+  const int pos = s.kv - s.nq + i;
+  return aa.window > 0 && pos >= aa.window ? pos - aa.window + 1 : 0;
+}
+
+__device__ __forceinline__ int end_key(const KvAttendArgs& aa, const Sequence& s, int i) {
+  return aa.causal ? max(min(s.kv, s.kv - s.nq + i + 1), 0) : s.kv;
+}
+
+// Partial results of a row over one split of its keys, relative to the reference exponent m:
+// sum of weights l and the weighted sum of values (head_dim binary32), kept in the workspace.
+struct Partial {
+  float m, l;
+};
+
+constexpr int kMaxSplits = 64;
+
+// Natural logarithm of l 2^m: the integer part of log2 l joins m before the sum is rounded.
+__device__ __forceinline__ float log_sum(float m, float l) {
+  if (!(l > 0.0f)) return l == 0.0f ? -INFINITY : l;
+  const int e = __builtin_amdgcn_frexp_expf(l);
+  return ((m + (float)e) + log2_hw(__builtin_amdgcn_frexp_mantf(l))) * 0.693147180559945309f;
+}
+
+}  // namespace bq

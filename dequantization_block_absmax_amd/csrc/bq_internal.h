@@ -195,6 +195,8 @@ struct KvAttendArgs {
 // Bytes of workspace the launch needs (no device is touched beyond its CU count).
 size_t kv_attend_workspace(const KvAttendArgs& a, int table_size);
 int launch_kv_attend(const KvAttendArgs& a, int dtype, const DequantArgs& da, void* stream);
+// Joins the partial results of nsplit splits of the keys (k_attn_merge.hip).
+int launch_kv_merge(const KvAttendArgs& a, int dtype, int nsplit, void* stream);
 
 // The library-owned scratch of bq_quantize_nested_noalloc (k_scratch.hip): kScratchBytes per
 // device, 256-byte aligned.  scratch_buffer sets *ptr to the current device's copy (its device

@@ -120,3 +120,18 @@ def test_attention_validation():
         assert attend(**kw) == bq.BQ_ERR_ALIGNMENT, kw
     for kw in (dict(q_start=FAKE + 2), dict(kv_len=FAKE + 1), dict(page_table=FAKE + 3)):
         assert attend(b=batch(**kw)) == bq.BQ_ERR_ALIGNMENT, kw
+
+
+def test_attention_workspace():
+    """A long context over few rows is split, which needs a workspace; invalid or empty calls need none."""
+    def size(c=None, b=None, dtype=bq.BQ_BF16, heads=16):
+        return bq.bq_kv_attention_workspace_bytes(cache() if c is None else c, batch() if b is None else b, dtype, heads)
+
+    assert size(dtype=bq.BQ_F32) == 0 and size(heads=3) == 0 and size(cache(page_size=7)) == 0
+    assert size(b=batch(num_seqs=0)) == 0
+    long = batch(num_seqs=1, tokens=1, max_kv_len=100000, table_stride=7000)
+    need = size(b=long)
+    assert need > 0 and need == size(b=long)
+    assert attend(b=long, workspace_bytes=need - 1) == bq.BQ_ERR_WORKSPACE
+    assert attend(b=long, workspace=None) == bq.BQ_ERR_WORKSPACE
+    assert attend(b=long, workspace=FAKE + 128) == bq.BQ_ERR_ALIGNMENT
