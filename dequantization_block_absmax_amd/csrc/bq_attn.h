@@ -59,12 +59,12 @@ struct Sequence {
 
 __device__ __forceinline__ Sequence sequence(const KvAttendArgs& aa, int seq) {
   Sequence s;
-  const int first = max(aa.q_start[seq], 0);
-  const int last = (int)min((int64_t)aa.q_start[seq + 1], aa.tokens);
+  const int first = max(__builtin_amdgcn_readfirstlane(aa.q_start[seq]), 0);
+  const int last = (int)min((int64_t)__builtin_amdgcn_readfirstlane(aa.q_start[seq + 1]), aa.tokens);
   s.q0 = first;
   // positions count all new tokens; rows past max_q_len are left out by the grid
   s.nq = max(last - first, 0);
-  s.kv = max(min(aa.kv_len[seq], aa.max_kv_len), 0);
+  s.kv = max(min(__builtin_amdgcn_readfirstlane(aa.kv_len[seq]), aa.max_kv_len), 0);
   return s;
 }
 

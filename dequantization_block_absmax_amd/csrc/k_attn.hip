@@ -31,6 +31,8 @@
 // halves of their bytes (spread) so that each holds some d's of every block.
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 #include "bq_attn.h"
 #include "bq_internal.h"
 #include "bq_launch.h"
@@ -38,29 +40,39 @@
 namespace bq {
 namespace {
 
-constexpr int kWaves = 4;
 constexpr int kGroup = 32;        // keys per wave and step
-constexpr int kCopies = 32;       // copies of the LDS table, one per bank: no lookup waits for another
+constexpr int kCopies = 64;       // copies of the LDS table, one per bank: no lookup waits for another
 constexpr float kSlack = 6.0f;    // weights may grow by 2^6 before the sums are rescaled
 
 template <int D, int NB, int KB>
 struct Shape {
+  static constexpr int kB = D / NB;             // block size
   static constexpr int kRow = D * KB / 8;       // bytes of a key's codes
   static constexpr int kLane = kRow / 16;       // bytes of a value's codes per lane: 2, 4, 8 or 16
   static constexpr int kWords = kLane < 4 ? 1 : kLane / 4;
   static constexpr int kSteps = D / 32;         // products of 32 d
+  static constexpr int kStepWords = KB / 4;     // words of a key's codes per lane and step: 1 or 2
   static constexpr int kTiles = D / 16;         // tiles of 16 d of the result
   static constexpr int kPerLane = D / 16;       // d's per lane
   static constexpr int kPerBlock = kPerLane / NB;
+  static constexpr int kMaxima = NB > 2 ? NB / 2 : 1;  // block maxima of a group that a lane loads
 };
 
-// One group of 32 keys as a lane loads it.
+// What a lane holds of one group of 32 keys: of the keys and of the values.  The group's 32 NB block
+// maxima are spread over the wave, in order, and go through LDS when they are used (held where they
+// are used they would take 16 NB registers).
 template <int D, int NB, int KB>
-struct Group {
+struct Keys {
   using S = Shape<D, NB, KB>;
-  uint32_t k[2][S::kSteps][KB == 4 ? 1 : 2];
-  uint32_t v[8][S::kWords];
-  float ka[2][4][NB], va[2][4][NB];
+  uint32_t code[2][S::kSteps * S::kStepWords];
+  float a[S::kMaxima];
+};
+
+template <int D, int NB, int KB>
+struct Values {
+  using S = Shape<D, NB, KB>;
+  uint32_t code[8][S::kWords];
+  float a[S::kMaxima];
 };
 
 // Where the pages of a group of 32 keys lie; a page outside the pool reads page 0 and hides its keys.
@@ -68,21 +80,54 @@ struct Pages {
   int id[2];
 };
 
-template <int KB>
-__device__ __forceinline__ uint32_t table_at(const char* lut, uint32_t byte_times_128, uint32_t lane4) {
-  return *reinterpret_cast<const uint32_t*>(lut + (byte_times_128 | lane4));
+typedef const __attribute__((address_space(1))) uint8_t* Global;
+
+// Keeps a uniform address in scalar registers, apart from the lane's offset: loads then take a scalar
+// base and a 32-bit offset (the compiler would else keep base plus offset of every array in vector
+// registers through the loop).
+__device__ __forceinline__ Global scalar_base(const void* p) {
+  uint64_t a = (uint64_t)(uintptr_t)p;
+  asm("" : "+s"(a));
+  return (Global)(uintptr_t)a;
 }
 
-// Table entry of byte b of a word: 4-bit codes, the binary16 pair (low nibble, high nibble); 8-bit codes, the
-// binary16 entry in the low half.
-template <int KB>
-__device__ __forceinline__ uint32_t lookup(const char* lut, uint32_t w, int b, uint32_t lane4) {
-  const uint32_t at = b == 0 ? w << 7 : w >> (8 * b - 7);
-  return table_at<KB>(lut, at & 0x7f80u, lane4);
+// The N words at src (N = 1, 2, 4 or 8, aligned to min(N, 4) words).
+template <int N>
+__device__ __forceinline__ void load_words(uint32_t* w, Global src) {
+  if constexpr (N == 1) {
+    w[0] = *(const __attribute__((address_space(1))) uint32_t*)src;
+  } else if constexpr (N == 2) {
+    const u32x2 t = *(const __attribute__((address_space(1))) u32x2*)src;
+    w[0] = t.x;
+    w[1] = t.y;
+  } else {
+#pragma unroll
+    for (int k = 0; k < N / 4; ++k) {
+      const u32x4 t = *(const __attribute__((address_space(1))) u32x4*)(src + 16 * k);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) w[4 * k + e] = t[e];
+    }
+  }
 }
 
-// Two 8-bit codes' entries as a pair.
-__device__ __forceinline__ uint32_t join(uint32_t lo, uint32_t hi) { return __builtin_amdgcn_perm(hi, lo, 0x05040100u); }
+// LDS offset of the lane's copy of the entry for byte b of w: byte << 8 | 4 * lane, one permute
+// (lane4 = 4 * lane).
+__device__ __forceinline__ uint32_t entry_of(uint32_t w, int b, uint32_t lane4) {
+  return __builtin_amdgcn_perm(w, lane4, 0x0c0c0000u | (uint32_t)(4 + b) << 8);
+}
+
+// Two consecutive operands of a product: 4-bit codes, the pair at byte b of w (low nibble's entry in the
+// low half); 8-bit codes, the entries of byte b of w and byte b2 of w2.
+template <int KB>
+__device__ __forceinline__ uint32_t operand_pair(const char* lut, uint32_t w, int b, uint32_t w2, int b2, uint32_t lane4) {
+  if constexpr (KB == 4) {
+    return *reinterpret_cast<const uint32_t*>(lut + entry_of(w, b, lane4));
+  } else {
+    const f16x2 v = {*reinterpret_cast<const _Float16*>(lut + entry_of(w, b, lane4)),
+                     *reinterpret_cast<const _Float16*>(lut + entry_of(w2, b2, lane4))};
+    return __builtin_bit_cast(uint32_t, v);
+  }
+}
 
 // Exchange between lanes m and p of a row of 16: of the lane's bytes in w (two halves), the lane with
 // `upper` false keeps its first half and takes the partner's first half as its second; the other
@@ -96,8 +141,9 @@ __device__ __forceinline__ uint32_t partner(uint32_t v) {
   if constexpr (DPP == kXor4) {
     const int even = __builtin_amdgcn_update_dpp(0, (int)v, 0x12C, 0xF, 0x5, false);
     return (uint32_t)__builtin_amdgcn_update_dpp(even, (int)v, 0x124, 0xF, 0xA, false);
-  } else
+  } else {
     return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, DPP, 0xF, 0xF, false);
+  }
 }
 
 template <int DPP>
@@ -181,15 +227,36 @@ struct Spread {
   }
 };
 
+// Keeps loads where they are written, before and after.
+__device__ __forceinline__ void load_fence() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+// Waves per workgroup and per SIMD: what the registers of each form allow without spilling (the table
+// and sums in LDS leave room for two workgroups of eight waves).
+template <int D, int NB, int RT>
+struct Occupancy {
+  static constexpr int kWaves = D == 256 && NB == 8 ? 4 : 8;
+  static constexpr int kPerSimd = D == 256 && NB == 8 ? 1 : RT * D <= 128 && NB <= 2 ? 4 : 2;
+};
+
 template <int D, int NB, int KB, int RT>
-__global__ __launch_bounds__(64 * kWaves, RT* D > 128 ? 1 : 2) void attend_kernel(KvAttendArgs aa, DequantArgs da,
-                                                                                   int nsplit, int bf16) {
+__global__ __launch_bounds__((64 * Occupancy<D, NB, RT>::kWaves), (Occupancy<D, NB, RT>::kPerSimd)) void attend_kernel(
+    KvAttendArgs aa, DequantArgs da, int nsplit, int bf16) {
+  constexpr int W = Occupancy<D, NB, RT>::kWaves;
   using S = Shape<D, NB, KB>;
+  constexpr int kThreads = 64 * W;
   constexpr int kRows = 16 * RT;
   constexpr int kPitch = D + 4;  // of a row of partial sums in LDS
-  constexpr int kLut = 256 * kCopies * 4, kSums = kWaves * 16 * kPitch * 4;
-  __shared__ __attribute__((aligned(16))) char s_mem[kLut > kSums ? kLut : kSums];
-  __shared__ Partial s_part[kWaves][kRows];
+  constexpr int kLut = 256 * kCopies * 4;
+  constexpr int kQueries = RT * S::kSteps * 64 * 16;     // in the order the lanes read them
+  constexpr int kMaxima = 32 * NB * 4;                   // one side of a wave's group
+  constexpr int kLoop = kLut + kQueries + 2 * W * kMaxima, kSums = W * 16 * kPitch * 4;
+  // table, queries and block maxima; after the keys, the waves' sums
+  __shared__ __attribute__((aligned(16))) char s_mem[kLoop > kSums ? kLoop : kSums];
+  __shared__ Partial s_part[W][kRows];
+  __shared__ float s_scale[kRows];
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -202,67 +269,17 @@ __global__ __launch_bounds__(64 * kWaves, RT* D > 128 ? 1 : 2) void attend_kerne
   const int nrows = min(sq.nq, aa.max_q_len) * group;  // rows of the sequence for this key/value head
   if (tile * kRows >= nrows) return;
 
-  // Table: entry b in copy c at (b * kCopies + c) * 4; a lane reads copy lane % 32.
-  {
-    const float lo = da.c[KB == 4 ? tid & 15 : tid], hi = da.c[KB == 4 ? tid >> 4 : tid];
-    const uint32_t e = pack_f16(lo, hi);
-    const u32x4 e4 = {e, e, e, e};
-#pragma unroll
-    for (int i = 0; i < kCopies / 4; ++i)  // in turn over the banks
-      *reinterpret_cast<u32x4*>(s_mem + tid * (kCopies * 4) + ((i + tid) & (kCopies / 4 - 1)) * 16) = e4;
-  }
-  const uint32_t lane4 = (lane & (kCopies - 1)) * 4;
-
-  // Rows of this lane (column m of the products), their keys and queries.
-  int lo[RT], hi[RT];
-  float scale[RT];
-  f16x8 q[RT][S::kSteps];
-#pragma unroll
-  for (int t = 0; t < RT; ++t) {
-    const int r = tile * kRows + t * 16 + m;
-    const bool live = r < nrows;
-    const int i = live ? r / group : 0;
-    const int head = kvh * group + (live ? r - i * group : 0);
-    lo[t] = live ? first_key(aa, sq, i) : 0;
-    hi[t] = live ? end_key(aa, sq, i) : 0;
-    const char* src = static_cast<const char*>(aa.q) + ((int64_t)(sq.q0 + i) * aa.q_stride + (int64_t)head * D) * 2;
-    float x[S::kSteps][8];
-    uint32_t top = 0;
-#pragma unroll
-    for (int s = 0; s < S::kSteps; ++s) {
-      const u32x4 w = *reinterpret_cast<const u32x4*>(src + (32 * s + 8 * g) * 2);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const uint32_t h = (w[e >> 1] >> (16 * (e & 1))) & 0xffffu;
-        x[s][e] = bf16 ? bits_f32(h << 16) : (float)__builtin_bit_cast(_Float16, (uint16_t)h);
-        top = max(top, f32_bits(x[s][e]) & 0x7fffffffu);
-      }
-    }
-    const float tf = rows_max(bits_f32(top < 0x7f800000u ? top : 0u));
-    const int ex = tf > 0.0f ? __builtin_amdgcn_frexp_expf(tf) : 0;  // |q| < 2^ex
-#pragma unroll
-    for (int s = 0; s < S::kSteps; ++s) {
-      u32x4 w;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float a = __builtin_ldexpf(x[s][2 * k], -ex), b = __builtin_ldexpf(x[s][2 * k + 1], -ex);
-        // 4-bit codes: the first element of a byte is its high nibble, the high half of the table's pair
-        w[k] = KB == 4 ? pack_f16(b, a) : pack_f16(a, b);
-      }
-      q[t][s] = __builtin_bit_cast(f16x8, w);
-    }
-    scale[t] = __builtin_ldexpf(aa.scale * 1.44269504088896341f, ex);
-  }
-
-  // Keys of the tile's rows together, this split's groups of 32 of them, and this wave's.
+  // Keys of the tile's rows together, this split's groups of 32 of them, and this wave's: groups
+  // wave, wave + W, ... of the split.
   const int last_row = min(tile * kRows + kRows, nrows) - 1;
   const int i_first = tile * kRows / group, i_last = last_row / group;
-  const int begin = first_key(aa, sq, i_first) & ~(kGroup - 1);
+  const int first = first_key(aa, sq, i_first), begin = first & ~(kGroup - 1);
   const int end = end_key(aa, sq, i_last);
   const int lo_all = first_key(aa, sq, i_last), hi_all = end_key(aa, sq, i_first);  // seen by every row
   const int groups = end > begin ? (end - begin + kGroup - 1) / kGroup : 0;
   const int per = (groups + nsplit - 1) / nsplit;
   const int g_end = min((split + 1) * per, groups);
+  int gi = split * per + wave;
 
   const int lps = aa.cache.log2_page;
   // read through scalar loads: the numbers are the same for the whole wave, and waiting for them
@@ -270,95 +287,183 @@ __global__ __launch_bounds__(64 * kWaves, RT* D > 128 ? 1 : 2) void attend_kerne
   typedef const __attribute__((address_space(4))) int32_t* ScalarTable;
   const ScalarTable pages = (ScalarTable)(uintptr_t)(aa.page_table + (int64_t)seq * aa.table_stride);
   const int last_page = sq.kv > 0 ? (sq.kv - 1) >> lps : 0;
-  auto find = [&](int gi) {
+  auto find = [&](int i) {
     Pages p;
 #pragma unroll
-    for (int u = 0; u < 2; ++u) p.id[u] = pages[min((begin + gi * kGroup + 16 * u) >> lps, last_page)];
+    for (int u = 0; u < 2; ++u) p.id[u] = pages[min((begin + i * kGroup + 16 * u) >> lps, last_page)];
     return p;
   };
-  const uint32_t k_at = m * S::kRow + g * (KB == 4 ? 4 : 8);
-  const uint32_t v_at = 4 * g * S::kRow + m * S::kLane;
-  const uint32_t a_at = 4 * g * NB * 4;
-  auto load = [&](int gi, const Pages& p, Group<D, NB, KB>& x) {
+  auto listed = [&](int id) { return (uint32_t)id < (uint32_t)aa.cache.num_pages; };
+  auto row_of = [&](int i, const Pages& p, int u) {  // the pool's row (page, head, slot) of the half group
+    const int j = begin + i * kGroup + 16 * u;
+    return (((int64_t)(listed(p.id[u]) ? p.id[u] : 0) * aa.cache.kv_heads + kvh) << lps) + (j & ((1 << lps) - 1));
+  };
+  // The maxima of the group's first 16 keys, then of the others: lane l takes the l-th few.
+  auto load_maxima = [&](int i, const Pages& p, int side, float* a) {
+    constexpr int half = NB == 1 ? 16 : 32;  // lanes of 16 keys (NB = 1: the wave's upper half repeats the lower)
+    const Global src0 = scalar_base(aa.cache.absmax[side] + row_of(i, p, 0) * NB);
+    const Global src1 = scalar_base(aa.cache.absmax[side] + row_of(i, p, 1) * NB);
+    load_words<S::kMaxima>(reinterpret_cast<uint32_t*>(a),
+                           (lane & half ? src1 : src0) + (uint32_t)((lane & (half - 1)) * S::kMaxima * 4));
+  };
+  float* const s_maxima = reinterpret_cast<float*>(s_mem + kLut + kQueries) + wave * 2 * (kMaxima / 4);
+  auto put_maxima = [&](int side, const float* a) {
+    float* dst = s_maxima + side * (kMaxima / 4) + (NB == 1 ? lane & 31 : lane) * S::kMaxima;
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int j = begin + gi * kGroup + 16 * u;
-      const uint32_t id = (uint32_t)p.id[u] < (uint32_t)aa.cache.num_pages ? p.id[u] : 0;
-      const int64_t row = (((int64_t)id * aa.cache.kv_heads + kvh) << lps) + (j & ((1 << lps) - 1));
-      const uint8_t* kp = aa.cache.packed[0] + row * S::kRow;
-      const uint8_t* vp = aa.cache.packed[1] + row * S::kRow;
+    for (int k = 0; k < S::kMaxima; ++k) dst[k] = a[k];
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+  };
+  // of the lane's keys 4g .. 4g+3 of the half group u, block by block
+  auto get_maxima = [&](int side, int u, float (&a)[4][NB]) {
+    const float* src = s_maxima + side * (kMaxima / 4) + (16 * u + 4 * g) * NB;
 #pragma unroll
-      for (int s = 0; s < S::kSteps; ++s) {
-        if constexpr (KB == 4) {
-          x.k[u][s][0] = *reinterpret_cast<const uint32_t*>(kp + k_at + 16 * s);
-        } else {
-          const u32x2 w = *reinterpret_cast<const u32x2*>(kp + k_at + 32 * s);
-          x.k[u][s][0] = w.x;
-          x.k[u][s][1] = w.y;
-        }
-      }
-      const float* kap = aa.cache.absmax[0] + row * NB;
-      const float* vap = aa.cache.absmax[1] + row * NB;
+    for (int k = 0; k < NB; ++k) {
+      const f32x4 v = *reinterpret_cast<const f32x4*>(src + 4 * k);
 #pragma unroll
-      for (int i = 0; i < NB; ++i) {
-        const f32x4 ka = *reinterpret_cast<const f32x4*>(reinterpret_cast<const char*>(kap) + a_at + 16 * i);
-        const f32x4 va = *reinterpret_cast<const f32x4*>(reinterpret_cast<const char*>(vap) + a_at + 16 * i);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          x.ka[u][(4 * i + e) / NB][(4 * i + e) % NB] = ka[e];
-          x.va[u][(4 * i + e) / NB][(4 * i + e) % NB] = va[e];
-        }
-      }
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const uint8_t* src = vp + v_at + r * S::kRow;
-        uint32_t* w = x.v[4 * u + r];
-        if constexpr (S::kLane == 2) {
-          w[0] = *reinterpret_cast<const uint16_t*>(src);
-        } else if constexpr (S::kLane == 4) {
-          w[0] = *reinterpret_cast<const uint32_t*>(src);
-        } else if constexpr (S::kLane == 8) {
-          const u32x2 t = *reinterpret_cast<const u32x2*>(src);
-          w[0] = t.x;
-          w[1] = t.y;
-        } else {
-          const u32x4 t = *reinterpret_cast<const u32x4*>(src);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) w[e] = t[e];
-        }
-      }
+      for (int e = 0; e < 4; ++e) a[(4 * k + e) / NB][(4 * k + e) % NB] = v[e];
     }
   };
+  // A lane takes a quarter of each block's codes of key m: d = b * B + g * B / 4 + 0 .. B / 4 - 1.
+  constexpr int kQuarter = S::kB / 4 * KB / 8;  // bytes
+  auto load_keys = [&](int i, const Pages& p, Keys<D, NB, KB>& x) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int64_t row = row_of(i, p, u);
+      const Global src = scalar_base(aa.cache.packed[0] + row * S::kRow);
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+        load_words<kQuarter / 4>(&x.code[u][b * (kQuarter / 4)], src + (uint32_t)(m * S::kRow + g * kQuarter) + b * 4 * kQuarter);
+    }
+    load_maxima(i, p, 0, x.a);
+  };
+  // A lane takes bytes m * kLane .. of the codes of keys 4g .. 4g+3 of each 16.
+  auto load_values = [&](int i, const Pages& p, Values<D, NB, KB>& x) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int64_t row = row_of(i, p, u);
+      const Global src = scalar_base(aa.cache.packed[1] + row * S::kRow) + (uint32_t)(4 * g * S::kRow + m * S::kLane);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        if constexpr (S::kLane == 2) x.code[4 * u + r][0] = *(const __attribute__((address_space(1))) uint16_t*)(src + r * S::kRow);
+        else load_words<S::kWords>(x.code[4 * u + r], src + r * S::kRow);
+      }
+    }
+    load_maxima(i, p, 1, x.a);
+  };
+
+  Keys<D, NB, KB> xk;
+  Values<D, NB, KB> xv;
+  Pages now = {{0, 0}}, next = {{0, 0}};
+  if (gi < g_end) {  // the first group is on its way while the table and the queries are set up
+    now = find(gi);
+    next = find(min(gi + W, groups - 1));
+    load_keys(gi, now, xk);
+    load_values(gi, now, xv);
+  }
+
+  // Table: entry b in copy c at (b * kCopies + c) * 4; a lane reads copy `lane`.
+  if (tid < 256) {
+    const float lo = da.c[KB == 4 ? tid & 15 : tid], hi = da.c[KB == 4 ? tid >> 4 : tid];
+    const uint32_t e = pack_f16(lo, hi);
+    const u32x4 e4 = {e, e, e, e};
+#pragma unroll
+    for (int i = 0; i < kCopies / 4; ++i)  // in turn over the banks
+      *reinterpret_cast<u32x4*>(s_mem + tid * (kCopies * 4) + ((i + tid) & (kCopies / 4 - 1)) * 16) = e4;
+  }
+  const uint32_t lane4 = lane * 4;
+
+  // Queries: wave t sets up the 16 rows of tile t, as the products' operands and a scale per row.
+  f16x8* const s_q = reinterpret_cast<f16x8*>(s_mem + kLut);
+  if (wave < RT) {
+    const int r = tile * kRows + wave * 16 + m;
+    const int i = r < nrows ? r / group : 0;
+    const int head = kvh * group + (r < nrows ? r - i * group : 0);
+    const char* src = static_cast<const char*>(aa.q) + ((int64_t)(sq.q0 + i) * aa.q_stride + (int64_t)head * D) * 2;
+    u32x4 w[S::kSteps];
+#pragma unroll
+    for (int s = 0; s < S::kSteps; ++s) {
+      constexpr int per_block = S::kSteps / NB;
+      const int d = s / per_block * S::kB + g * (S::kB / 4) + s % per_block * 8;
+      w[s] = *reinterpret_cast<const u32x4*>(src + d * 2);
+    }
+    float x[S::kSteps][8];
+    if (bf16) {
+#pragma unroll
+      for (int s = 0; s < S::kSteps; ++s)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[s][e] = bits_f32(e & 1 ? w[s][e >> 1] & 0xffff0000u : w[s][e >> 1] << 16);
+    } else {
+#pragma unroll
+      for (int s = 0; s < S::kSteps; ++s)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[s][e] = (float)__builtin_bit_cast(f16x8, w[s])[e];
+    }
+    uint32_t top = 0;
+#pragma unroll
+    for (int s = 0; s < S::kSteps; ++s)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) top = max(top, f32_bits(x[s][e]) & 0x7fffffffu);
+    const float tf = rows_max(bits_f32(top < 0x7f800000u ? top : 0u));
+    const int ex = tf > 0.0f ? __builtin_amdgcn_frexp_expf(tf) : 0;  // |q| < 2^ex
+#pragma unroll
+    for (int s = 0; s < S::kSteps; ++s) {
+      u32x4 o;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float a = __builtin_ldexpf(x[s][2 * k], -ex), b = __builtin_ldexpf(x[s][2 * k + 1], -ex);
+        // 4-bit codes: the first element of a byte is its high nibble, the high half of the table's pair
+        o[k] = KB == 4 ? pack_f16(b, a) : pack_f16(a, b);
+      }
+      s_q[(wave * S::kSteps + s) * 64 + lane] = __builtin_bit_cast(f16x8, o);
+    }
+    if (g == 0) s_scale[wave * 16 + m] = __builtin_ldexpf(aa.scale * 1.44269504088896341f, ex);
+  }
+  __syncthreads();  // table and queries are in place
+
+  // Rows of this lane (column m of the products): the keys they see, their scales.
+  int lo[RT], hi[RT];
+  float scale[RT];
+#pragma unroll
+  for (int t = 0; t < RT; ++t) {
+    const int r = tile * kRows + t * 16 + m;
+    const int i = r / group;
+    lo[t] = r < nrows ? first_key(aa, sq, i) : 0;
+    hi[t] = r < nrows ? end_key(aa, sq, i) : 0;
+    scale[t] = s_scale[t * 16 + m];
+  }
 
   const Spread<D, NB, KB> spread(m);
-  float ref[RT], safe[RT], sum[RT];  // reference M, M where it is finite, sum of weights (this lane's keys)
+  float ref[RT], sum[RT];  // reference M, sum of weights (this lane's keys)
   f32x4 acc[RT][S::kTiles];
 #pragma unroll
   for (int t = 0; t < RT; ++t) {
     ref[t] = -INFINITY;
-    safe[t] = sum[t] = 0.0f;
+    sum[t] = 0.0f;
 #pragma unroll
     for (int i = 0; i < S::kTiles; ++i) acc[t][i] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
   }
 
-  auto step = [&](int gi, const Pages& p, Group<D, NB, KB>& x) {
-    const int j0 = begin + gi * kGroup;
-    // scores, in the log2 domain
-    float s[RT][2][4];
+  // Scores of the group, in the log2 domain: the lane's keys 4g .. 4g+3 of each 16.
+  float s[RT][2][4];
+  auto scores = [&](const Keys<D, NB, KB>& x) {
+    put_maxima(0, x.a);
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
+      float ka[4][NB];
+      get_maxima(0, u, ka);
       f32x4 z[RT];
 #pragma unroll
       for (int k = 0; k < S::kSteps; ++k) {
         u32x4 w;
-        if constexpr (KB == 4) {
 #pragma unroll
-          for (int b = 0; b < 4; ++b) w[b] = lookup<4>(s_mem, x.k[u][k][0], b, lane4);
-        } else {
-#pragma unroll
-          for (int b = 0; b < 4; ++b)
-            w[b] = join(lookup<8>(s_mem, x.k[u][k][b >> 1], 2 * (b & 1), lane4),
-                        lookup<8>(s_mem, x.k[u][k][b >> 1], 2 * (b & 1) + 1, lane4));
+        for (int b = 0; b < 4; ++b) {
+          if constexpr (KB == 4) w[b] = operand_pair<4>(s_mem, x.code[u][k], b, 0, 0, lane4);
+          else {
+            const uint32_t c = x.code[u][2 * k + (b >> 1)];
+            w[b] = operand_pair<8>(s_mem, c, 2 * (b & 1), c, 2 * (b & 1) + 1, lane4);
+          }
         }
         const f16x8 a = __builtin_bit_cast(f16x8, w);
         constexpr int per_block = S::kSteps / NB;
@@ -366,11 +471,11 @@ __global__ __launch_bounds__(64 * kWaves, RT* D > 128 ? 1 : 2) void attend_kerne
 #pragma unroll
         for (int t = 0; t < RT; ++t) {
           if (k % per_block == 0) z[t] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
-          z[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, q[t][k], z[t], 0, 0, 0);
+          z[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, s_q[(t * S::kSteps + k) * 64 + lane], z[t], 0, 0, 0);
           if (k % per_block == per_block - 1) {
 #pragma unroll
             for (int r = 0; r < 4; ++r)
-              s[t][u][r] = b == 0 ? z[t][r] * x.ka[u][r][b] : fmaf(z[t][r], x.ka[u][r][b], s[t][u][r]);
+              s[t][u][r] = b == 0 ? z[t][r] * ka[r][b] : fmaf(z[t][r], ka[r][b], s[t][u][r]);
             // The scaled score is rounded here, once, and not inside fused multiply-adds below: the key
             // that sets the reference then has the weight 2^-E exactly.
             if (k == S::kSteps - 1) {
@@ -381,81 +486,80 @@ __global__ __launch_bounds__(64 * kWaves, RT* D > 128 ? 1 : 2) void attend_kerne
         }
       }
     }
-    // exponents of the tokens' largest value maximum (between 2^-100 and 2^100; zero counts as 2^-100)
+  };
+
+  // Weights of the lane's 8 keys, block by block, as pairs of binary16.
+  uint32_t w[RT][NB][4];
+  auto weights = [&](int j0, const Pages& p, const Values<D, NB, KB>& x) {
+    float va[2][4][NB];
+    put_maxima(1, x.a);
+    get_maxima(1, 0, va[0]);
+    get_maxima(1, 1, va[1]);
+    if (!(j0 >= lo_all && j0 + kGroup <= hi_all && listed(p.id[0]) && listed(p.id[1]))) {  // uniform
+      // Some row does not see some key.  Keys that no row of the tile sees may have any maxima: zeros.
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int j = j0 + 16 * u + 4 * g + r;
+          const bool none = j < first || j >= end || !listed(p.id[u]);
+#pragma unroll
+          for (int b = 0; b < NB; ++b) va[u][r][b] = none ? 0.0f : va[u][r][b];
+#pragma unroll
+          for (int t = 0; t < RT; ++t) s[t][u][r] = none || j < lo[t] || j >= hi[t] ? -INFINITY : s[t][u][r];
+        }
+    }
+    // exponents of the keys' largest value maximum (at least -99; a of zero counts as 2^-100)
     float ev[2][4];
 #pragma unroll
     for (int u = 0; u < 2; ++u)
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        float a = fabsf(x.va[u][r][0]);
+        float a = 0x1p-100f;
 #pragma unroll
-        for (int b = 1; b < NB; ++b) a = fmaxf(a, fabsf(x.va[u][r][b]));
-        ev[u][r] = (float)__builtin_amdgcn_frexp_expf(fminf(fmaxf(a, 0x1p-100f), 0x1p100f));
+        for (int b = 0; b < NB; ++b) a = fmaxf(a, fabsf(va[u][r][b]));
+        ev[u][r] = (float)__builtin_amdgcn_frexp_expf(a);
       }
-    const bool listed0 = (uint32_t)p.id[0] < (uint32_t)aa.cache.num_pages;
-    const bool listed1 = (uint32_t)p.id[1] < (uint32_t)aa.cache.num_pages;
-    const bool masked = !(j0 >= lo_all && j0 + kGroup <= hi_all && listed0 && listed1);  // uniform
-    uint32_t w[RT][NB][4];  // weights of the lane's 8 keys
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
-      uint32_t hide = 0;
-      if (masked) {
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const int j = j0 + 16 * u + 4 * g + r;
-            const bool out = j < lo[t] || j >= hi[t] || !(u == 0 ? listed0 : listed1);
-            hide |= out ? 1u << (4 * u + r) : 0u;
-            if (out) s[t][u][r] = 0.0f;
-          }
-      }
       float top = -INFINITY;
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const float v = s[t][u][r] + ev[u][r];
-          top = fmaxf(top, masked && (hide >> (4 * u + r) & 1) ? -INFINITY : v);
-        }
+        for (int r = 0; r < 4; ++r) top = fmaxf(top, s[t][u][r] + ev[u][r]);
       if (__any(top > ref[t] + kSlack)) {  // rare after the first groups: raise the reference
         const float up = fmaxf(ref[t], rows_max(top));
         const float f = ref[t] == -INFINITY ? 0.0f : exp2_hw(ref[t] - up);
         ref[t] = up;
-        safe[t] = up == -INFINITY ? 0.0f : up;
         sum[t] *= f;
 #pragma unroll
         for (int i = 0; i < S::kTiles; ++i)
 #pragma unroll
           for (int r = 0; r < 4; ++r) acc[t][i][r] *= f;
       }
-      float pw[NB][8];
+      const float safe = fmaxf(ref[t], -0x1p120f);  // no key yet: -infinity - safe is still -infinity
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int e = 4 * u + r;
-          const bool out = masked && (hide >> e & 1);
-          const float p2 = out ? 0.0f : exp2_hw(s[t][u][r] - safe[t]);
-          sum[t] += p2;
+        for (int r = 0; r < 4; r += 2) {
+          const float p0 = exp2_hw(s[t][u][r] - safe), p1 = exp2_hw(s[t][u][r + 1] - safe);
+          sum[t] += p0 + p1;
 #pragma unroll
-          for (int b = 0; b < NB; ++b) pw[b][e] = out ? 0.0f : p2 * x.va[u][r][b];
+          for (int b = 0; b < NB; ++b) w[t][b][2 * u + r / 2] = pack_f16(p0 * va[u][r][b], p1 * va[u][r + 1][b]);
         }
-#pragma unroll
-      for (int b = 0; b < NB; ++b)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) w[t][b][k] = pack_f16(pw[b][2 * k], pw[b][2 * k + 1]);
     }
-    // sums of values
+  };
+
+  auto add_values = [&](Values<D, NB, KB>& x) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) spread.apply(x.v[e]);
+    for (int e = 0; e < 8; ++e) spread.apply(x.code[e]);
 #pragma unroll
     for (int wd = 0; wd < S::kWords; ++wd) {
       uint32_t pair[4][2];  // 4-bit: both keys' codes of a pair in one byte (even and odd d's)
       if constexpr (KB == 4) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const uint32_t x0 = x.v[2 * k][wd], x1 = x.v[2 * k + 1][wd];
+          const uint32_t x0 = x.code[2 * k][wd], x1 = x.code[2 * k + 1][wd];
           pair[k][0] = ((x0 >> 4) & 0x0f0f0f0fu) | (x1 & 0xf0f0f0f0u);
           pair[k][1] = (x0 & 0x0f0f0f0fu) | ((x1 << 4) & 0xf0f0f0f0u);
         }
@@ -469,9 +573,8 @@ __global__ __launch_bounds__(64 * kWaves, RT* D > 128 ? 1 : 2) void attend_kerne
           u32x4 a;
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            if constexpr (KB == 4) a[k] = lookup<4>(s_mem, pair[k][h], by, lane4);
-            else
-              a[k] = join(lookup<8>(s_mem, x.v[2 * k][wd], by, lane4), lookup<8>(s_mem, x.v[2 * k + 1][wd], by, lane4));
+            if constexpr (KB == 4) a[k] = operand_pair<4>(s_mem, pair[k][h], by, 0, 0, lane4);
+            else a[k] = operand_pair<8>(s_mem, x.code[2 * k][wd], by, x.code[2 * k + 1][wd], by, lane4);
           }
           const int i = (4 * wd + by) * kPer + h;  // tile: place i of the lane's d's
           const int b = i / S::kPerBlock;
@@ -484,28 +587,27 @@ __global__ __launch_bounds__(64 * kWaves, RT* D > 128 ? 1 : 2) void attend_kerne
     }
   };
 
-  __syncthreads();  // the table is in place
-  // Groups wave, wave + 4, ... of the split: the next group's loads, and the page numbers of the one
-  // after it, are issued before the current group is worked on.
-  int gi = split * per + wave;
+  // A group's keys are used before its values: the next group's keys are loaded into the same
+  // registers in between, its values at the end, and the page numbers come one group further ahead.
   if (gi < g_end) {
-    Group<D, NB, KB> x0, x1;
-    Pages p0 = find(gi), p1 = find(min(gi + kWaves, groups - 1));
-    load(gi, p0, x0);
-    for (;;) {
-      const Pages p2 = find(min(gi + 2 * kWaves, groups - 1));
-      load(min(gi + kWaves, groups - 1), p1, x1);
-      step(gi, p0, x0);
-      gi += kWaves;
-      if (gi >= g_end) break;
-      const Pages p3 = find(min(gi + 2 * kWaves, groups - 1));
-      load(min(gi + kWaves, groups - 1), p2, x0);
-      step(gi, p1, x1);
-      gi += kWaves;
-      if (gi >= g_end) break;
-      p0 = p2;
-      p1 = p3;
+    while (gi + W < g_end) {
+      const Pages later = find(min(gi + 2 * W, groups - 1));
+      scores(xk);
+      load_fence();
+      load_keys(gi + W, next, xk);
+      load_fence();
+      weights(begin + gi * kGroup, now, xv);
+      add_values(xv);
+      load_fence();
+      load_values(gi + W, next, xv);
+      load_fence();
+      now = next;
+      next = later;
+      gi += W;
     }
+    scores(xk);
+    weights(begin + gi * kGroup, now, xv);
+    add_values(xv);
   }
 
   // Join the waves: common reference, then their scaled sums in wave order.
@@ -520,7 +622,7 @@ __global__ __launch_bounds__(64 * kWaves, RT* D > 128 ? 1 : 2) void attend_kerne
   for (int t = 0; t < RT; ++t) {
     float top = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) top = fmaxf(top, s_part[w][t * 16 + m].m);
+    for (int v = 0; v < W; ++v) top = fmaxf(top, s_part[v][t * 16 + m].m);
     const float f = ref[t] == -INFINITY ? 0.0f : exp2_hw(ref[t] - top);
 #pragma unroll
     for (int i = 0; i < S::kTiles; ++i)
@@ -530,43 +632,39 @@ __global__ __launch_bounds__(64 * kWaves, RT* D > 128 ? 1 : 2) void attend_kerne
         s_sum[(wave * 16 + m) * kPitch + d] = acc[t][i][r] * f;
       }
     __syncthreads();
-    // 16 threads to a row, each some groups of 4 d
-    const int row = tid >> 4;
-    const int r = tile * kRows + t * 16 + row;
-    if (r < nrows) {
+#pragma unroll
+    for (int c0 = 0; c0 < 16 * D / 4; c0 += kThreads) {  // groups of 4 d of the 16 rows
+      const int c = c0 + tid;
+      const int row = c / (D / 4), d = c % (D / 4) * 4;
+      const int r = tile * kRows + t * 16 + row;
+      if ((16 * D / 4) % kThreads != 0 && c >= 16 * D / 4) break;
+      if (r >= nrows) continue;
       const int i = r / group, head = kvh * group + (r - i * group);
       const int64_t token = sq.q0 + i;
       float m_all = -INFINITY, l_all = 0.0f;
 #pragma unroll
-      for (int w = 0; w < kWaves; ++w) m_all = fmaxf(m_all, s_part[w][t * 16 + row].m);
+      for (int v = 0; v < W; ++v) m_all = fmaxf(m_all, s_part[v][t * 16 + row].m);
 #pragma unroll
-      for (int w = 0; w < kWaves; ++w) {
-        const Partial p = s_part[w][t * 16 + row];
+      for (int v = 0; v < W; ++v) {
+        const Partial p = s_part[v][t * 16 + row];
         l_all += p.m == -INFINITY ? 0.0f : p.l * exp2_hw(p.m - m_all);
       }
-      const float inv = l_all > 0.0f ? 1.0f / l_all : (l_all == 0.0f ? 0.0f : l_all);
-      const int64_t part = ((token * aa.heads + head) * nsplit + split);
-      float* wsum = static_cast<float*>(aa.workspace) + part * D;
-      Partial* wpart = reinterpret_cast<Partial*>(static_cast<float*>(aa.workspace) + aa.tokens * aa.heads * nsplit * D) + part;
+      f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-      for (int c = 0; c < D / 64; ++c) {
-        const int d = (tid & 15) * 4 + 64 * c;
-        f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int w = 0; w < kWaves; ++w) v += *reinterpret_cast<const f32x4*>(&s_sum[(w * 16 + row) * kPitch + d]);
-        if (nsplit == 1) {
-          const u32x2 o = {pack16(v[0] * inv, v[1] * inv, bf16), pack16(v[2] * inv, v[3] * inv, bf16)};
-          *reinterpret_cast<u32x2*>(static_cast<char*>(aa.out) + (token * aa.out_stride + (int64_t)head * D + d) * 2) = o;
-        } else {
-          *reinterpret_cast<f32x4*>(wsum + d) = v;
-        }
-      }
-      if ((tid & 15) == 0) {
-        if (nsplit > 1) *wpart = {m_all, l_all};
-        else if (aa.lse != nullptr) aa.lse[token * aa.heads + head] = log_sum(m_all, l_all);
+      for (int v = 0; v < W; ++v) o += *reinterpret_cast<const f32x4*>(&s_sum[(v * 16 + row) * kPitch + d]);
+      if (nsplit == 1) {
+        const float inv = l_all > 0.0f ? 1.0f / l_all : (l_all == 0.0f ? 0.0f : l_all);
+        const u32x2 o16 = {pack16(o[0] * inv, o[1] * inv, bf16), pack16(o[2] * inv, o[3] * inv, bf16)};
+        *reinterpret_cast<u32x2*>(static_cast<char*>(aa.out) + (token * aa.out_stride + (int64_t)head * D + d) * 2) = o16;
+        if (d == 0 && aa.lse != nullptr) aa.lse[token * aa.heads + head] = log_sum(m_all, l_all);
+      } else {
+        const int64_t part = (token * aa.heads + head) * nsplit + split;
+        float* wsum = static_cast<float*>(aa.workspace);
+        *reinterpret_cast<f32x4*>(wsum + part * D + d) = o;
+        if (d == 0) reinterpret_cast<Partial*>(wsum + aa.tokens * aa.heads * nsplit * D)[part] = {m_all, l_all};
       }
     }
-    __syncthreads();
+    if (t + 1 < RT) __syncthreads();
   }
 }
 
@@ -580,7 +678,7 @@ struct Plan {
 static Plan make_plan(const KvAttendArgs& a) {
   Plan p;
   const int64_t rows = (int64_t)a.max_q_len * (a.heads / a.cache.kv_heads);
-  p.rt = rows > 16 ? 2 : 1;
+  p.rt = rows > 16 && a.cache.head_dim <= 128 ? 2 : 1;
   p.tiles = (int)((rows + 16 * p.rt - 1) / (16 * p.rt));
   const int64_t base = (int64_t)p.tiles * a.cache.kv_heads * a.num_seqs;
   const int64_t cus = cu_count();
@@ -590,8 +688,8 @@ static Plan make_plan(const KvAttendArgs& a) {
     n = n < most ? n : most;
     return n < 1 ? 1 : n > kMaxSplits ? kMaxSplits : n;
   };
-  int64_t n = splits(8 * cus, 256);
-  if (n * base < 2 * cus) n = splits(2 * cus, 128);
+  int64_t n = splits(8 * cus, 512);
+  if (n * base < 2 * cus) n = splits(2 * cus, 256);
   p.nsplit = (int)n;
   return p;
 }
@@ -607,14 +705,15 @@ namespace {
 template <int D, int NB, int KB, int RT>
 hipError_t launch_rows(const KvAttendArgs& a, const Plan& p, int dtype, const DequantArgs& da, hipStream_t s) {
   const dim3 grid((unsigned)p.nsplit, (unsigned)(p.tiles * a.cache.kv_heads), (unsigned)a.num_seqs);
-  return launch_kernel(attend_kernel<D, NB, KB, RT>, grid, dim3(64 * kWaves), s, a, da, p.nsplit, dtype == BF16);
+  return launch_kernel(attend_kernel<D, NB, KB, RT>, grid, dim3(64 * Occupancy<D, NB, RT>::kWaves), s, a, da, p.nsplit, dtype == BF16);
 }
 
 template <int D, int NB>
 hipError_t launch_blocks(const KvAttendArgs& a, const Plan& p, int dtype, const DequantArgs& da, hipStream_t s) {
-  if (da.K == 16)
-    return p.rt == 1 ? launch_rows<D, NB, 4, 1>(a, p, dtype, da, s) : launch_rows<D, NB, 4, 2>(a, p, dtype, da, s);
-  return p.rt == 1 ? launch_rows<D, NB, 8, 1>(a, p, dtype, da, s) : launch_rows<D, NB, 8, 2>(a, p, dtype, da, s);
+  if constexpr (D <= 128) {
+    if (p.rt == 2) return da.K == 16 ? launch_rows<D, NB, 4, 2>(a, p, dtype, da, s) : launch_rows<D, NB, 8, 2>(a, p, dtype, da, s);
+  }
+  return da.K == 16 ? launch_rows<D, NB, 4, 1>(a, p, dtype, da, s) : launch_rows<D, NB, 8, 1>(a, p, dtype, da, s);
 }
 
 }  // namespace

@@ -1,8 +1,7 @@
 // k_attn_merge.hip -- joins the partial results of the splits of an attention call.
 //
 // A row's splits hold (M_s, l_s) and sums o_s relative to their own reference exponent M_s; with
-// M = max_s M_s:  o = sum_s 2^(M_s - M) o_s / sum_s 2^(M_s - M) l_s, in split order.  One wave per row:
-// lane s works out split s's factor, then the lanes take head_dim.  Bound by latency: a call's
+// M = max_s M_s:  o = sum_s 2^(M_s - M) o_s / sum_s 2^(M_s - M) l_s, in a fixed order.  Bound by latency: a call's
 // partial sums are a small part of its cache.
 #include <hip/hip_runtime.h>
 
@@ -13,13 +12,16 @@
 namespace bq {
 namespace {
 
+// One workgroup per row: wave w takes splits w, w + 4, ..., lane by lane over head_dim.
 constexpr int kWaves = 4;
 
 template <int D>
 __global__ __launch_bounds__(64 * kWaves) void merge_kernel(KvAttendArgs aa, int nsplit, int bf16) {
-  const int lane = threadIdx.x & 63;
+  __shared__ float s_sum[kWaves][D];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const Sequence sq = sequence(aa, blockIdx.y);
-  const int64_t row = (int64_t)blockIdx.x * kWaves + (threadIdx.x >> 6);
+  const int64_t row = blockIdx.x;
   if (row >= (int64_t)min(sq.nq, aa.max_q_len) * aa.heads) return;
   const int64_t at = (int64_t)sq.q0 * aa.heads + row;  // token * heads + head
   const float* sums = static_cast<const float*>(aa.workspace) + at * nsplit * D;
@@ -27,6 +29,11 @@ __global__ __launch_bounds__(64 * kWaves) void merge_kernel(KvAttendArgs aa, int
       reinterpret_cast<const Partial*>(static_cast<const float*>(aa.workspace) + aa.tokens * aa.heads * nsplit * D) +
       at * nsplit;
   const Partial mine = lane < nsplit ? parts[lane] : Partial{-INFINITY, 0.0f};
+  constexpr int kPer = D / 64;
+  float v[kPer];
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) v[k] = 0.0f;
+  // splits past the last repeat it with weight zero, so that four loads are in flight without a condition
   float top = mine.m;
 #pragma unroll
   for (int x = 1; x < 64; x <<= 1) top = fmaxf(top, __shfl_xor(top, x));
@@ -34,35 +41,44 @@ __global__ __launch_bounds__(64 * kWaves) void merge_kernel(KvAttendArgs aa, int
   float l = f * mine.l;
 #pragma unroll
   for (int x = 1; x < 64; x <<= 1) l += __shfl_xor(l, x);
-
-  constexpr int kPer = D / 64;
-  float v[kPer];
+  for (int s0 = wave; s0 < nsplit; s0 += 4 * kWaves) {
+    float x[4][kPer];
 #pragma unroll
-  for (int k = 0; k < kPer; ++k) v[k] = 0.0f;
-#pragma unroll 4
-  for (int s = 0; s < nsplit; ++s) {
-    const float fs = bits_f32(__builtin_amdgcn_readlane(f32_bits(f), s));
-    const float* src = sums + (int64_t)s * D + lane * kPer;
+    for (int i = 0; i < 4; ++i) {
+      const float* src = sums + (int64_t)min(s0 + i * kWaves, nsplit - 1) * D + lane * kPer;
 #pragma unroll
-    for (int k = 0; k < kPer; ++k) v[k] = fmaf(fs, src[k], v[k]);
+      for (int k = 0; k < kPer; ++k) x[i][k] = src[k];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int s = s0 + i * kWaves;
+      const float fs = s < nsplit ? bits_f32(__builtin_amdgcn_readlane(f32_bits(f), min(s, 63))) : 0.0f;
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) v[k] = fmaf(fs, x[i][k], v[k]);
+    }
   }
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) s_sum[wave][lane * kPer + k] = v[k];
+  __syncthreads();
   const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
   const int64_t token = at / aa.heads, head = at - token * aa.heads;
-  uint16_t* out = static_cast<uint16_t*>(aa.out) + token * aa.out_stride + head * D + lane * kPer;
-  if constexpr (kPer == 1) {
-    *out = (uint16_t)pack16(v[0] * inv, 0.0f, bf16);
-  } else {
+  if (tid < D / 2) {
+    const int d = 2 * tid;
+    float o[2];
 #pragma unroll
-    for (int k = 0; k < kPer; k += 2) reinterpret_cast<uint32_t*>(out)[k / 2] = pack16(v[k] * inv, v[k + 1] * inv, bf16);
+    for (int k = 0; k < 2; ++k)
+      o[k] = ((s_sum[0][d + k] + s_sum[1][d + k]) + (s_sum[2][d + k] + s_sum[3][d + k])) * inv;
+    uint16_t* out = static_cast<uint16_t*>(aa.out) + token * aa.out_stride + head * D;
+    *reinterpret_cast<uint32_t*>(out + d) = pack16(o[0], o[1], bf16);
   }
-  if (aa.lse != nullptr && lane == 0) aa.lse[at] = log_sum(top, l);
+  if (aa.lse != nullptr && tid == 0) aa.lse[at] = log_sum(top, l);
 }
 
 }  // namespace
 
 int launch_kv_merge(const KvAttendArgs& a, int dtype, int nsplit, void* stream) {
   hipStream_t s = static_cast<hipStream_t>(stream);
-  const dim3 grid((unsigned)(((int64_t)a.max_q_len * a.heads + kWaves - 1) / kWaves), (unsigned)a.num_seqs);
+  const dim3 grid((unsigned)((int64_t)a.max_q_len * a.heads), (unsigned)a.num_seqs);
   const dim3 block(64 * kWaves);
   const int bf16 = dtype == BF16;
   if (a.cache.head_dim == 64) return (int)launch_kernel(merge_kernel<64>, grid, block, s, a, nsplit, bf16);
