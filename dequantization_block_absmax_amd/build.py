@@ -26,7 +26,7 @@ DEVICE = ["--offload-arch=" + ARCH, "-Xclang", "-target-feature", "-Xclang", "-p
 
 SOURCES = ["bq_api.cpp", "bq_table.cpp", "k_quant.hip", "k_dequant.hip", "k_nested.hip", "k_q32.hip",
            "k_linear.hip", "k_gemm.hip", "k_scratch.hip", "k_iq2xs.hip",
-           "k_iq1s.hip", "k_kv.hip", "k_attn.hip", "k_attn_merge.hip"]
+           "k_iq1s.hip", "k_kv.hip", "k_attn.hip", "k_attn_merge.hip", "k_attn_chunk.hip"]
 
 
 def _cmd(src: str, obj: str) -> list[str]:

@@ -36,6 +36,10 @@ __device__ __forceinline__ float rows_sum(float v) {
   return bits_f32(s.x) + bits_f32(s.y);
 }
 
+// Cached values enter the matrix cores multiplied by a power of two that puts the largest just below
+// 2^kTopBit, so that binary16 (down to 2^-14 in full precision) keeps 11 bits of small ones too.
+constexpr int kTopBit = 14;
+
 // Two binary32 values as a pair of 16-bit ones (round to nearest even), the first in the low half.
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   const f32x2 v = {lo, hi};
@@ -85,6 +89,20 @@ struct Partial {
 };
 
 constexpr int kMaxSplits = 64;
+
+// Which sequences a launch takes.  A call whose sequences may bring many rows to a key/value head goes
+// through two sets of kernels: those of k_attn_chunk.hip for sequences with more than kFewRows rows (any, if
+// it is the only one), and the splitting kernel of k_attn.hip for the others.
+enum Rows : int { kAllRows = 0, kFewOnly = 1, kManyRows = 2 };
+constexpr int kFewRows = 32;
+
+__device__ __forceinline__ bool many_rows(int nq, int group, int num_seqs) {
+  return num_seqs == 1 || (int64_t)nq * group > kFewRows;
+}
+
+__device__ __forceinline__ bool takes(int rows, int nq, int group, int num_seqs) {
+  return rows == kAllRows || many_rows(nq, group, num_seqs) == (rows == kManyRows);
+}
 
 // Natural logarithm of l 2^m: the integer part of log2 l joins m before the sum is rounded.
 __device__ __forceinline__ float log_sum(float m, float l) {

@@ -195,8 +195,21 @@ struct KvAttendArgs {
 // Bytes of workspace the launch needs (no device is touched beyond its CU count).
 size_t kv_attend_workspace(const KvAttendArgs& a, int table_size);
 int launch_kv_attend(const KvAttendArgs& a, int dtype, const DequantArgs& da, void* stream);
-// Joins the partial results of nsplit splits of the keys (k_attn_merge.hip).
-int launch_kv_merge(const KvAttendArgs& a, int dtype, int nsplit, void* stream);
+// Joins the partial results of splits of the keys (k_attn_merge.hip): [0] those of sequences with few
+// rows, [1] with many; nsplit <= 1: nothing to join.  Not both: every sequence is of `kind`.
+struct MergeArgs {
+  const float* partial[2];
+  int nsplit[2];
+  int both, kind;
+};
+int launch_kv_merge(const KvAttendArgs& a, int dtype, const MergeArgs& m, void* stream);
+// How k_attn_chunk.hip goes about a call: expanded tiles of keys, rows per workgroup, splits, and where
+// its parts of the workspace begin (bytes).
+struct ChunkPlan {
+  int ntiles, rb, blocks, nsplit;
+  size_t info_at, partial_at, end;
+};
+int launch_kv_chunk(const KvAttendArgs& a, int dtype, const ChunkPlan& p, const DequantArgs& da, void* stream);
 
 // The library-owned scratch of bq_quantize_nested_noalloc (k_scratch.hip): kScratchBytes per
 // device, 256-byte aligned.  scratch_buffer sets *ptr to the current device's copy (its device

@@ -5,7 +5,8 @@
 // with the running maximum and sum of the softmax.
 //
 // Factored form.  The matrix cores (v_mfma_f32_16x16x32_f16) multiply the codes' table entries,
-// rounded once to binary16; the block maxima enter in binary32:
+// times 2^14 (binary16 then keeps 11 bits of every entry down to its least, 2^-20) and rounded once to
+// binary16; the block maxima enter in binary32:
 //   s_ij = R_i sum_b a_jb (sum_{d in b} q'_id c_jd)   q' = q 2^-e_i exact in binary16, R_i = scale 2^e_i
 //   o_i  = sum_j (p_ij a'_jb) c'_jd                    for d in block b of the values
 // so no cached value is formed: a code byte indexes a table in LDS that holds its two binary16
@@ -243,7 +244,7 @@ struct Occupancy {
 
 template <int D, int NB, int KB, int RT>
 __global__ __launch_bounds__((64 * Occupancy<D, NB, RT>::kWaves), (Occupancy<D, NB, RT>::kPerSimd)) void attend_kernel(
-    KvAttendArgs aa, DequantArgs da, int nsplit, int bf16) {
+    KvAttendArgs aa, DequantArgs da, int nsplit, float* partial, int rows, int bf16) {
   constexpr int W = Occupancy<D, NB, RT>::kWaves;
   using S = Shape<D, NB, KB>;
   constexpr int kThreads = 64 * W;
@@ -267,7 +268,7 @@ __global__ __launch_bounds__((64 * Occupancy<D, NB, RT>::kWaves), (Occupancy<D, 
   const int group = aa.heads / aa.cache.kv_heads;
   const Sequence sq = sequence(aa, seq);
   const int nrows = min(sq.nq, aa.max_q_len) * group;  // rows of the sequence for this key/value head
-  if (tile * kRows >= nrows) return;
+  if (tile * kRows >= nrows || !takes(rows, min(sq.nq, aa.max_q_len), group, aa.num_seqs)) return;
 
   // Keys of the tile's rows together, this split's groups of 32 of them, and this wave's: groups
   // wave, wave + W, ... of the split.
@@ -366,7 +367,7 @@ __global__ __launch_bounds__((64 * Occupancy<D, NB, RT>::kWaves), (Occupancy<D, 
   // Table: entry b in copy c at (b * kCopies + c) * 4; a lane reads copy `lane`.
   if (tid < 256) {
     const float lo = da.c[KB == 4 ? tid & 15 : tid], hi = da.c[KB == 4 ? tid >> 4 : tid];
-    const uint32_t e = pack_f16(lo, hi);
+    const uint32_t e = pack_f16(__builtin_ldexpf(lo, kTopBit), __builtin_ldexpf(hi, kTopBit));
     const u32x4 e4 = {e, e, e, e};
 #pragma unroll
     for (int i = 0; i < kCopies / 4; ++i)  // in turn over the banks
@@ -418,7 +419,7 @@ __global__ __launch_bounds__((64 * Occupancy<D, NB, RT>::kWaves), (Occupancy<D, 
       }
       s_q[(wave * S::kSteps + s) * 64 + lane] = __builtin_bit_cast(f16x8, o);
     }
-    if (g == 0) s_scale[wave * 16 + m] = __builtin_ldexpf(aa.scale * 1.44269504088896341f, ex);
+    if (g == 0) s_scale[wave * 16 + m] = __builtin_ldexpf(aa.scale * 1.44269504088896341f, ex - kTopBit);
   }
   __syncthreads();  // table and queries are in place
 
@@ -623,7 +624,7 @@ __global__ __launch_bounds__((64 * Occupancy<D, NB, RT>::kWaves), (Occupancy<D, 
     float top = -INFINITY;
 #pragma unroll
     for (int v = 0; v < W; ++v) top = fmaxf(top, s_part[v][t * 16 + m].m);
-    const float f = ref[t] == -INFINITY ? 0.0f : exp2_hw(ref[t] - top);
+    const float f = ref[t] == -INFINITY ? 0.0f : __builtin_ldexpf(exp2_hw(ref[t] - top), -kTopBit);
 #pragma unroll
     for (int i = 0; i < S::kTiles; ++i)
 #pragma unroll
@@ -659,9 +660,8 @@ __global__ __launch_bounds__((64 * Occupancy<D, NB, RT>::kWaves), (Occupancy<D, 
         if (d == 0 && aa.lse != nullptr) aa.lse[token * aa.heads + head] = log_sum(m_all, l_all);
       } else {
         const int64_t part = (token * aa.heads + head) * nsplit + split;
-        float* wsum = static_cast<float*>(aa.workspace);
-        *reinterpret_cast<f32x4*>(wsum + part * D + d) = o;
-        if (d == 0) reinterpret_cast<Partial*>(wsum + aa.tokens * aa.heads * nsplit * D)[part] = {m_all, l_all};
+        *reinterpret_cast<f32x4*>(partial + part * D + d) = o;
+        if (d == 0) reinterpret_cast<Partial*>(partial + aa.tokens * aa.heads * nsplit * D)[part] = {m_all, l_all};
       }
     }
     if (t + 1 < RT) __syncthreads();
@@ -670,18 +670,48 @@ __global__ __launch_bounds__((64 * Occupancy<D, NB, RT>::kWaves), (Occupancy<D, 
 
 }  // namespace
 
-// Rows per tile and splits of the keys, by what the call's shape bounds.
+// How a call is done: tiles of 16 rt rows and splits of the keys for the splitting kernel, for every
+// sequence or for those with few rows, and the plan of the chunk kernels where some may have many.
 struct Plan {
+  bool few, many;
   int rt, tiles, nsplit;
+  size_t partial_at, bytes;
+  ChunkPlan chunk;
 };
 
+// The expanded keys and values may take this much of the workspace; a call that would need more is
+// left to the splitting kernel.
+constexpr int64_t kMaxExpanded = (int64_t)4 << 30;
+
 static Plan make_plan(const KvAttendArgs& a) {
-  Plan p;
-  const int64_t rows = (int64_t)a.max_q_len * (a.heads / a.cache.kv_heads);
-  p.rt = rows > 16 && a.cache.head_dim <= 128 ? 2 : 1;
+  Plan p = {};
+  const int64_t group = a.heads / a.cache.kv_heads, D = a.cache.head_dim, cus = cu_count();
+  int64_t rows = a.max_q_len * group;
+  const int64_t ntiles = ((int64_t)a.max_kv_len + 63) / 64;
+  const int64_t expanded = ntiles * a.cache.kv_heads * a.num_seqs * 64 * D * 4;
+  p.many = rows > 2 * kFewRows && ntiles > 0 && expanded <= kMaxExpanded;
+  p.few = !p.many || a.num_seqs > 1;
+  if (p.many) {
+    ChunkPlan& c = p.chunk;
+    c.ntiles = (int)ntiles;
+    c.rb = D == 64 ? 2 : 1;
+    c.blocks = (int)((rows + 128 * c.rb - 1) / (128 * c.rb));
+    // workgroups without splits: the rows there are, whatever their sequences
+    const int64_t base = a.cache.kv_heads * ((a.tokens * group + 128 * c.rb - 1) / (128 * c.rb));
+    int64_t n = (cus + base - 1) / base;
+    n = n < ntiles / 4 ? n : ntiles / 4;
+    c.nsplit = (int)(n < 1 ? 1 : n > kMaxSplits ? kMaxSplits : n);
+    c.info_at = (size_t)expanded;
+    c.partial_at = (c.info_at + (size_t)(ntiles * a.cache.kv_heads * a.num_seqs) * 16 + 255) & ~(size_t)255;
+    c.end = c.partial_at + (c.nsplit > 1 ? (size_t)a.tokens * a.heads * c.nsplit * (D + 2) * 4 : 0);
+    p.partial_at = (c.end + 255) & ~(size_t)255;
+    rows = kFewRows;  // the splitting kernel's sequences
+  }
+  p.bytes = p.partial_at;
+  if (!p.few) return p;
+  p.rt = rows > 16 && D <= 128 ? 2 : 1;
   p.tiles = (int)((rows + 16 * p.rt - 1) / (16 * p.rt));
   const int64_t base = (int64_t)p.tiles * a.cache.kv_heads * a.num_seqs;
-  const int64_t cus = cu_count();
   auto splits = [&](int64_t target, int64_t keys) {
     const int64_t most = ((int64_t)a.max_kv_len + keys - 1) / keys;
     int64_t n = (target + base - 1) / base;
@@ -691,21 +721,20 @@ static Plan make_plan(const KvAttendArgs& a) {
   int64_t n = splits(8 * cus, 512);
   if (n * base < 2 * cus) n = splits(2 * cus, 256);
   p.nsplit = (int)n;
+  if (n > 1) p.bytes += (size_t)a.tokens * a.heads * n * (D + 2) * 4;
   return p;
 }
 
-size_t kv_attend_workspace(const KvAttendArgs& a, int) {
-  const Plan p = make_plan(a);
-  if (p.nsplit == 1) return 0;
-  return (size_t)a.tokens * a.heads * p.nsplit * (a.cache.head_dim + 2) * 4;
-}
+size_t kv_attend_workspace(const KvAttendArgs& a, int) { return make_plan(a).bytes; }
 
 namespace {
 
 template <int D, int NB, int KB, int RT>
 hipError_t launch_rows(const KvAttendArgs& a, const Plan& p, int dtype, const DequantArgs& da, hipStream_t s) {
   const dim3 grid((unsigned)p.nsplit, (unsigned)(p.tiles * a.cache.kv_heads), (unsigned)a.num_seqs);
-  return launch_kernel(attend_kernel<D, NB, KB, RT>, grid, dim3(64 * Occupancy<D, NB, RT>::kWaves), s, a, da, p.nsplit, dtype == BF16);
+  float* partial = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + p.partial_at);
+  return launch_kernel(attend_kernel<D, NB, KB, RT>, grid, dim3(64 * Occupancy<D, NB, RT>::kWaves), s, a, da, p.nsplit,
+                       partial, p.many ? kFewOnly : kAllRows, dtype == BF16);
 }
 
 template <int D, int NB>
@@ -716,31 +745,38 @@ hipError_t launch_blocks(const KvAttendArgs& a, const Plan& p, int dtype, const 
   return da.K == 16 ? launch_rows<D, NB, 4, 1>(a, p, dtype, da, s) : launch_rows<D, NB, 8, 1>(a, p, dtype, da, s);
 }
 
+hipError_t launch_few(const KvAttendArgs& a, const Plan& p, int dtype, const DequantArgs& da, hipStream_t s) {
+  const int nb = a.cache.head_dim >> a.cache.log2b;
+  if (a.cache.head_dim == 64)
+    return nb == 1 ? launch_blocks<64, 1>(a, p, dtype, da, s) : launch_blocks<64, 2>(a, p, dtype, da, s);
+  if (a.cache.head_dim == 128)
+    return nb == 1   ? launch_blocks<128, 1>(a, p, dtype, da, s)
+           : nb == 2 ? launch_blocks<128, 2>(a, p, dtype, da, s)
+                     : launch_blocks<128, 4>(a, p, dtype, da, s);
+  return nb == 1   ? launch_blocks<256, 1>(a, p, dtype, da, s)
+         : nb == 2 ? launch_blocks<256, 2>(a, p, dtype, da, s)
+         : nb == 4 ? launch_blocks<256, 4>(a, p, dtype, da, s)
+                   : launch_blocks<256, 8>(a, p, dtype, da, s);
+}
+
 }  // namespace
 
 int launch_kv_attend(const KvAttendArgs& a, int dtype, const DequantArgs& da, void* stream) {
-  hipStream_t s = static_cast<hipStream_t>(stream);
   const Plan p = make_plan(a);
-  if ((int64_t)p.tiles * a.cache.kv_heads > 65535) {  // grid rows
+  // grid rows
+  if ((p.few && (int64_t)p.tiles * a.cache.kv_heads > 65535) || (p.many && (p.chunk.blocks > 65535 || a.cache.kv_heads > 65535))) {
     g_launch_refused_for_size = true;
     return (int)hipErrorInvalidConfiguration;
   }
-  const int nb = a.cache.head_dim >> a.cache.log2b;
-  hipError_t e;
-  if (a.cache.head_dim == 64) {
-    e = nb == 1 ? launch_blocks<64, 1>(a, p, dtype, da, s) : launch_blocks<64, 2>(a, p, dtype, da, s);
-  } else if (a.cache.head_dim == 128) {
-    e = nb == 1   ? launch_blocks<128, 1>(a, p, dtype, da, s)
-        : nb == 2 ? launch_blocks<128, 2>(a, p, dtype, da, s)
-                  : launch_blocks<128, 4>(a, p, dtype, da, s);
-  } else {
-    e = nb == 1   ? launch_blocks<256, 1>(a, p, dtype, da, s)
-        : nb == 2 ? launch_blocks<256, 2>(a, p, dtype, da, s)
-        : nb == 4 ? launch_blocks<256, 4>(a, p, dtype, da, s)
-                  : launch_blocks<256, 8>(a, p, dtype, da, s);
-  }
-  if (e != hipSuccess || p.nsplit == 1) return (int)e;
-  return launch_kv_merge(a, dtype, p.nsplit, stream);
+  char* const ws = static_cast<char*>(a.workspace);
+  const MergeArgs m = {{reinterpret_cast<float*>(ws + p.partial_at), reinterpret_cast<float*>(ws + p.chunk.partial_at)},
+                       {p.few ? p.nsplit : 0, p.many ? p.chunk.nsplit : 0},
+                       p.few && p.many,
+                       p.many};
+  int e = p.many ? launch_kv_chunk(a, dtype, p.chunk, da, stream) : 0;
+  if (e == 0 && p.few) e = (int)launch_few(a, p, dtype, da, static_cast<hipStream_t>(stream));
+  if (e != 0 || (m.nsplit[0] <= 1 && m.nsplit[1] <= 1)) return e;
+  return launch_kv_merge(a, dtype, m, stream);
 }
 
 }  // namespace bq

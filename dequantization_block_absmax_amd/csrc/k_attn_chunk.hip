@@ -1,0 +1,431 @@
+// k_attn_chunk.hip -- attention of longer runs of new tokens over the cache.
+//
+// With many rows to a key the arithmetic of the products bounds the call, and decoding the codes anew
+// for every tile of rows would double the vector work.  So the keys and values of the sequences that bring
+// many rows are first expanded once into the workspace (expand_kernel), as binary16 in the order in which
+// the matrix cores take them, and chunk_kernel multiplies from there:
+//   K' = RN16(fl32(c a) 2^(14-ek)), V' = RN16(fl32(c a) 2^(14-ev)), per tile of 64 keys of a head
+// with 2^ek, 2^ev powers of two at least as large as the tile's largest maximum: every cached value
+// keeps 11 bits, whatever the type of q and the size of the values (down to 2^-28 of the power of two).
+// ek joins the scale of the scores.  ev is a multiple of 8, so that one sequence's tiles nearly always
+// share it; sums are kept relative to the largest ev so far (E), and for a tile with a smaller one the
+// weights are scaled by 2^(ev - E) before the product (what that rounds away is below 2^-25 of the
+// largest values).
+//
+// chunk_kernel: a workgroup of four waves takes 128 RB rows (new token x query head of one key/value
+// head) and walks the tiles of 64 keys with the running maximum and sum of the softmax.  A wave takes
+// RB x 32 rows, with v_mfma_f32_32x32x16_f16; lane l = 32 g + n:
+//   S^T = K' Q^T   A = K' from LDS, B = Q in registers; the result holds row n's scores of the keys
+//                  8 (v / 4) + 4 g + v % 4 of each 32 (element v)
+//   O^T = V'^T P^T B = P^T: 8 keys per lane and step, taken in just that order, so the weights stay where
+//                  they were computed; V' is stored with its keys in the same order.
+#include <hip/hip_runtime.h>
+
+#include "bq_attn.h"
+#include "bq_internal.h"
+#include "bq_launch.h"
+
+namespace bq {
+namespace {
+
+constexpr int kTile = 64;   // keys
+constexpr float kSlack = 6.0f;
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+// What a tile's expansion leaves beside its values: exponents, and which of its keys exist.
+struct TileInfo {
+  int32_t ek, ev;
+  uint64_t keys;
+};
+
+// ---- expansion ----------------------------------------------------------------------------
+//
+// Workgroup: one tile of one head.  Fragment order of a tile (16-byte pieces of 8 binary16):
+//   K' piece ((kb * D/16 + s) * 64 + 32 g + n): key 32 kb + n, d = 16 s + 8 g + 0 .. 7
+//   V' piece ((db * 4 + ks) * 64 + 32 g + n):   d = 32 db + n, keys 16 ks + 8 (e / 4) + 4 g + e % 4, e = 0 .. 7
+template <int D, int KB>
+__global__ __launch_bounds__(256) void expand_kernel(KvAttendArgs aa, DequantArgs da, int ntiles, u32x4* tiles,
+                                                     TileInfo* infos) {
+  __shared__ float s_c[256];
+  __shared__ float s_a[2][kTile * 8];    // block maxima of the tile's keys and values, zero for keys that do not exist
+  __shared__ int64_t s_row[kTile];       // pool row of each key
+  __shared__ uint32_t s_top[2][4];
+  __shared__ uint32_t s_listed[2];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int tile = blockIdx.x, kvh = blockIdx.y, seq = blockIdx.z;
+  const Sequence sq = sequence(aa, seq);
+  const int group = aa.heads / aa.cache.kv_heads;
+  if (!many_rows(min(sq.nq, aa.max_q_len), group, aa.num_seqs)) return;
+  const int i_last = min(sq.nq, aa.max_q_len) - 1;
+  if (tile * kTile >= end_key(aa, sq, i_last) || (tile + 1) * kTile <= first_key(aa, sq, 0)) return;  // not read
+  const int log2nb = __builtin_ctz(D) - aa.cache.log2b, nb = 1 << log2nb;
+
+  s_c[tid] = da.c[tid];
+  if (wave == 0) {
+    const int j = tile * kTile + lane;
+    const int id = j < sq.kv ? aa.page_table[(int64_t)seq * aa.table_stride + (j >> aa.cache.log2_page)] : -1;
+    const bool listed = (uint32_t)id < (uint32_t)aa.cache.num_pages;
+    s_row[lane] = listed ? (((int64_t)id * aa.cache.kv_heads + kvh) << aa.cache.log2_page) +
+                               (j & ((1 << aa.cache.log2_page) - 1))
+                         : -1;
+    const uint64_t all = __ballot(listed);
+    if (lane < 2) s_listed[lane] = (uint32_t)(all >> (32 * lane));
+  }
+  __syncthreads();
+  uint32_t top[2] = {0, 0};
+  for (int e = tid; e < kTile << log2nb; e += 256) {
+    const int64_t row = s_row[e >> log2nb];
+#pragma unroll
+    for (int side = 0; side < 2; ++side) {
+      const float a = row >= 0 ? aa.cache.absmax[side][(row << log2nb) + (e & (nb - 1))] : 0.0f;
+      s_a[side][e] = a;
+      top[side] = max(top[side], f32_bits(a) & 0x7fffffffu);
+    }
+  }
+#pragma unroll
+  for (int side = 0; side < 2; ++side) {
+#pragma unroll
+    for (int x = 1; x < 64; x <<= 1) top[side] = max(top[side], (uint32_t)__shfl_xor((int)top[side], x));
+    if (lane == 0) s_top[side][wave] = top[side];
+  }
+  __syncthreads();
+  // exponents: |a| < 2^e (zeros: the least)
+  auto exponent = [&](int side) {
+    const uint32_t t = max(max(s_top[side][0], s_top[side][1]), max(s_top[side][2], s_top[side][3]));
+    return min(max((int)(t >> 23) - 126, -100), 120);
+  };
+  const int ek = exponent(0), ev = (exponent(1) + 127) / 8 * 8 - 120;
+  const float fk = __builtin_ldexpf(1.0f, kTopBit - ek), fv = __builtin_ldexpf(1.0f, kTopBit - ev);
+  const int64_t at = ((int64_t)seq * aa.cache.kv_heads + kvh) * ntiles + tile;
+  if (tid == 0) infos[at] = {ek, ev, s_listed[0] | (uint64_t)s_listed[1] << 32};
+  u32x4* const kt = tiles + at * (2 * kTile * D / 8);
+  u32x4* const vt = kt + kTile * D / 8;
+
+  constexpr int kRow = D * KB / 8;
+  // keys: a unit is 8 d of one key
+#pragma unroll
+  for (int p0 = 0; p0 < kTile * D / 8; p0 += 256) {
+    const int p = p0 + tid;
+    const int s = (p >> 6) % (D / 16), d8 = 2 * s + ((p >> 5) & 1), key = (p >> 6) / (D / 16) * 32 + (p & 31);
+    const int64_t row = max(s_row[key], (int64_t)0);
+    const uint8_t* src = aa.cache.packed[0] + row * kRow + d8 * KB;
+    const float a = s_a[0][(key << log2nb) + (d8 * 8 >> aa.cache.log2b)];
+    u32x2 c;
+    if constexpr (KB == 4) c = (u32x2){*reinterpret_cast<const uint32_t*>(src), 0u};
+    else c = *reinterpret_cast<const u32x2*>(src);
+    u32x4 w;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t q0 = KB == 4 ? (c.x >> (8 * k + 4)) & 15u : ((k < 2 ? c.x : c.y) >> (16 * (k & 1))) & 255u;
+      const uint32_t q1 = KB == 4 ? (c.x >> (8 * k)) & 15u : ((k < 2 ? c.x : c.y) >> (16 * (k & 1) + 8)) & 255u;
+      w[k] = pack_f16((s_c[q0] * a) * fk, (s_c[q1] * a) * fk);
+    }
+    kt[p] = w;
+  }
+  // values: a unit is 4 d of the 8 keys of a piece
+#pragma unroll
+  for (int p0 = 0; p0 < kTile * D / 32; p0 += 256) {
+    const int p = p0 + tid;
+    if (kTile * D / 32 < 256 && p >= kTile * D / 32) break;
+    const int d4 = p % (D / 4), oct = p / (D / 4), g = oct & 1, ks = oct >> 1;
+    float v[8][4];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int key = 16 * ks + 8 * (e >> 2) + 4 * g + (e & 3);
+      const int64_t row = max(s_row[key], (int64_t)0);
+      const uint8_t* src = aa.cache.packed[1] + row * kRow + d4 * KB / 2;
+      const float a = s_a[1][(key << log2nb) + (d4 * 4 >> aa.cache.log2b)];
+      const uint32_t c = KB == 4 ? *reinterpret_cast<const uint16_t*>(src) : *reinterpret_cast<const uint32_t*>(src);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t q = KB == 4 ? (c >> (8 * (i >> 1) + ((i & 1) ? 0 : 4))) & 15u : (c >> (8 * i)) & 255u;
+        v[e][i] = (s_c[q] * a) * fv;
+      }
+    }
+    const int d = d4 * 4;
+    u32x4* dst = vt + ((d >> 5) * 4 + ks) * 64 + 32 * g + (d & 31);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      dst[i] = (u32x4){pack_f16(v[0][i], v[1][i]), pack_f16(v[2][i], v[3][i]), pack_f16(v[4][i], v[5][i]),
+                       pack_f16(v[6][i], v[7][i])};
+  }
+}
+
+// ---- attention ----------------------------------------------------------------------------
+
+template <int D, int RB>
+struct ChunkOccupancy {
+  static constexpr int kPerSimd = RB * D <= 128 ? 2 : 1;
+};
+
+template <int D, int RB>
+__global__ __launch_bounds__(256, (ChunkOccupancy<D, RB>::kPerSimd)) void chunk_kernel(KvAttendArgs aa, int ntiles,
+                                                                                     const u32x4* tiles,
+                                                                                     const TileInfo* infos,
+                                                                                     int nsplit, float* partial,
+                                                                                     int bf16) {
+  constexpr int kRows = 128 * RB;
+  constexpr int kSteps = D / 16, kBlocks = D / 32;
+  constexpr int kPieces = kTile * D / 8;          // of keys, and of values, in a tile
+  constexpr int kStage = 2 * kPieces / 256;       // pieces a thread stages
+  __shared__ u32x4 s_tile[2][2 * kPieces];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int n = lane & 31, g = lane >> 5;
+  const int kvh = blockIdx.x % aa.cache.kv_heads, split = blockIdx.x / aa.cache.kv_heads;
+  const int seq = blockIdx.z;
+  const int group = aa.heads / aa.cache.kv_heads;
+  const Sequence sq = sequence(aa, seq);
+  const int nq = min(sq.nq, aa.max_q_len);
+  const int nrows = nq * group;
+  const int block = (int)gridDim.y - 1 - (int)blockIdx.y;  // later rows see more keys: first
+  if (block * kRows >= nrows || !many_rows(nq, group, aa.num_seqs)) return;
+
+  // Tiles of the block's rows together, and this split's.
+  const int last_row = min(block * kRows + kRows, nrows) - 1;
+  const int begin = first_key(aa, sq, block * kRows / group) / kTile;
+  const int end = (end_key(aa, sq, last_row / group) + kTile - 1) / kTile;
+  const int count = max(end - begin, 0), per = (count + nsplit - 1) / nsplit;
+  const int t_first = begin + split * per, t_end = min(t_first + per, end);
+  // keys that every row of the wave sees, and the last that any does
+  const int w_first = min(block * kRows + wave * 32 * RB, last_row), w_last = min(w_first + 32 * RB - 1, last_row);
+  const int lo_all = first_key(aa, sq, w_last / group), hi_all = end_key(aa, sq, w_first / group);
+  const int hi_any = end_key(aa, sq, w_last / group), lo_any = first_key(aa, sq, w_first / group);
+
+  const int64_t head_at = ((int64_t)seq * aa.cache.kv_heads + kvh) * ntiles;
+  u32x4 stage[kStage];
+  auto fetch = [&](int t) {
+    const u32x4* src = tiles + (head_at + t) * (2 * kPieces) + tid;
+#pragma unroll
+    for (int k = 0; k < kStage; ++k) stage[k] = src[256 * k];
+  };
+  auto put = [&](int buf) {
+#pragma unroll
+    for (int k = 0; k < kStage; ++k) s_tile[buf][256 * k + tid] = stage[k];
+  };
+  if (t_first < t_end) fetch(t_first);
+
+  // Queries as operands: binary16 relative to a power of two of the row, the scale's sign included.
+  int lo[RB], hi[RB];
+  float scale[RB];
+  f16x8 q[RB][kSteps];
+#pragma unroll
+  for (int b = 0; b < RB; ++b) {
+    const int r = block * kRows + (wave * RB + b) * 32 + n;
+    const bool live = r < nrows;
+    const int i = live ? r / group : 0;
+    const int head = kvh * group + (live ? r - i * group : 0);
+    lo[b] = live ? first_key(aa, sq, i) : 0;
+    hi[b] = live ? end_key(aa, sq, i) : 0;
+    const char* src = static_cast<const char*>(aa.q) + ((int64_t)(sq.q0 + i) * aa.q_stride + (int64_t)head * D + 8 * g) * 2;
+    u32x4 w[kSteps];
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) w[s] = *reinterpret_cast<const u32x4*>(src + 32 * s);
+    // magnitudes of 16-bit floats are ordered like their bits
+    uint32_t top = 0;
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) top = max(top, max(w[s][k] & 0x7fffu, (w[s][k] >> 16) & 0x7fffu));
+    top = max(top, (uint32_t)__shfl_xor((int)top, 32));
+    if (top >= (bf16 ? 0x7f80u : 0x7c00u)) top = 0;
+    const float tf = bf16 ? bits_f32(top << 16) : (float)__builtin_bit_cast(_Float16, (uint16_t)top);
+    const int ex = tf > 0.0f ? __builtin_amdgcn_frexp_expf(tf) : 0;  // |q| < 2^ex
+    const float sign = aa.scale < 0.0f ? -1.0f : 1.0f;
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+      u32x4 o;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t x = w[s][k];
+        const f16x2 h = __builtin_bit_cast(f16x2, x);
+        const float x0 = bf16 ? bits_f32(x << 16) : (float)h.x, x1 = bf16 ? bits_f32(x & 0xffff0000u) : (float)h.y;
+        o[k] = pack_f16(__builtin_ldexpf(x0, -ex) * sign, __builtin_ldexpf(x1, -ex) * sign);
+      }
+      q[b][s] = __builtin_bit_cast(f16x8, o);
+    }
+    scale[b] = __builtin_ldexpf(fabsf(aa.scale) * 1.44269504088896341f, ex);
+  }
+
+  float ref[RB], sum[RB];
+  f32x16 acc[RB][kBlocks];
+#pragma unroll
+  for (int b = 0; b < RB; ++b) {
+    ref[b] = -INFINITY;
+    sum[b] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kBlocks; ++i)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) acc[b][i][v] = 0.0f;
+  }
+  int e_all = -1000;  // exponent of the sums
+
+  if (t_first < t_end) {
+    put(0);
+    __syncthreads();
+  }
+  for (int t = t_first; t < t_end; ++t) {
+    const int buf = (t - t_first) & 1;
+    fetch(min(t + 1, t_end - 1));
+    const TileInfo info = infos[head_at + t];
+    const int ek = __builtin_amdgcn_readfirstlane(info.ek), ev = __builtin_amdgcn_readfirstlane(info.ev);
+    const int j0 = t * kTile;
+    if (j0 < hi_any && j0 + kTile > lo_any) {  // uniform
+      const f16x8* kp = reinterpret_cast<const f16x8*>(s_tile[buf]) + lane;
+      const f16x8* vp = kp + kPieces;
+      f32x16 s[RB][2];
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb) {
+#pragma unroll
+        for (int b = 0; b < RB; ++b)
+#pragma unroll
+          for (int v = 0; v < 16; ++v) s[b][kb][v] = 0.0f;
+#pragma unroll
+        for (int k = 0; k < kSteps; ++k) {
+          const f16x8 a = kp[(kb * kSteps + k) * 64];
+#pragma unroll
+          for (int b = 0; b < RB; ++b) s[b][kb] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a, q[b][k], s[b][kb], 0, 0, 0);
+        }
+      }
+      if (!(j0 >= lo_all && j0 + kTile <= hi_all && info.keys == ~0ull)) {  // some key hidden from some row
+        const uint32_t there[2] = {(uint32_t)info.keys >> (4 * g), (uint32_t)(info.keys >> 32) >> (4 * g)};
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+          for (int v = 0; v < 16; ++v) {
+            const int key = 8 * (v >> 2) + (v & 3), j = j0 + 32 * kb + 4 * g + key;
+            const uint32_t hide = (~there[kb] >> key) & 1u;
+#pragma unroll
+            for (int b = 0; b < RB; ++b)
+              s[b][kb][v] = hide | (uint32_t)(j < lo[b]) | (uint32_t)(j >= hi[b]) ? -INFINITY : s[b][kb][v];
+          }
+      }
+      if (ev > e_all) {  // uniform; nearly always the first tile only
+        const float f = __builtin_ldexpf(1.0f, max(e_all - ev, -1000));
+#pragma unroll
+        for (int b = 0; b < RB; ++b)
+#pragma unroll
+          for (int i = 0; i < kBlocks; ++i)
+#pragma unroll
+            for (int v = 0; v < 16; ++v) acc[b][i][v] *= f;
+        e_all = ev;
+      }
+      u32x4 p[RB][4];
+#pragma unroll
+      for (int b = 0; b < RB; ++b) {
+        // at least 2^-126: a hidden key's -infinity stays what it is
+        const float sc = fmaxf(__builtin_ldexpf(scale[b], ek - kTopBit), 0x1p-126f);
+        float top = -INFINITY;
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+          for (int v = 0; v < 16; ++v) top = fmaxf(top, s[b][kb][v]);
+        top *= sc;
+        if (__any(top > ref[b] + kSlack)) {  // rare after the first tiles
+          const u32x2 o = __builtin_amdgcn_permlane32_swap(f32_bits(top), f32_bits(top), false, false);
+          const float up = fmaxf(ref[b], fmaxf(bits_f32(o.x), bits_f32(o.y)));
+          const float f = ref[b] == -INFINITY ? 0.0f : exp2_hw(ref[b] - up);
+          ref[b] = up;
+          sum[b] *= f;
+#pragma unroll
+          for (int i = 0; i < kBlocks; ++i)
+#pragma unroll
+            for (int v = 0; v < 16; ++v) acc[b][i][v] *= f;
+        }
+        const float safe = fmaxf(ref[b], -0x1p120f);
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+          for (int v = 0; v < 16; v += 2) {
+            const uint32_t w = pack_f16(exp2_hw(fmaf(s[b][kb][v], sc, -safe)), exp2_hw(fmaf(s[b][kb][v + 1], sc, -safe)));
+            // the sum takes the weights as rounded: a row that one key fills gives that key's value
+            sum[b] = __builtin_amdgcn_fdot2(__builtin_bit_cast(f16x2, w), (f16x2){(_Float16)1.0f, (_Float16)1.0f}, sum[b], false);
+            p[b][2 * kb + (v >> 3)][(v & 7) >> 1] = w;
+          }
+      }
+      if (ev < e_all) {  // uniform, rare: the tile's values are in smaller units, so its weights shrink
+        const _Float16 f1 = (_Float16)__builtin_ldexpf(1.0f, max(ev - e_all, -24));
+        const f16x2 f = {f1, f1};
+#pragma unroll
+        for (int b = 0; b < RB; ++b)
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t w = p[b][ks][k];
+              p[b][ks][k] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, w) * f);
+            }
+      }
+#pragma unroll
+      for (int ks = 0; ks < 4; ++ks)
+#pragma unroll
+        for (int i = 0; i < kBlocks; ++i) {
+          const f16x8 a = vp[(i * 4 + ks) * 64];
+#pragma unroll
+          for (int b = 0; b < RB; ++b)
+            acc[b][i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a, __builtin_bit_cast(f16x8, p[b][ks]), acc[b][i], 0, 0, 0);
+        }
+    }
+    put(buf ^ 1);
+    __syncthreads();
+  }
+
+  const float unit = e_all > -1000 ? __builtin_ldexpf(1.0f, e_all - kTopBit) : 0.0f;
+#pragma unroll
+  for (int b = 0; b < RB; ++b) {
+    const int r = block * kRows + (wave * RB + b) * 32 + n;
+    const u32x2 o2 = __builtin_amdgcn_permlane32_swap(f32_bits(sum[b]), f32_bits(sum[b]), false, false);
+    const float l = bits_f32(o2.x) + bits_f32(o2.y);
+    if (r >= nrows) continue;
+    const int i = r / group, head = kvh * group + (r - i * group);
+    const int64_t token = sq.q0 + i;
+    const int64_t part = (token * aa.heads + head) * nsplit + split;
+    const float inv = nsplit > 1 ? unit : (l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l)) * unit;
+#pragma unroll
+    for (int k = 0; k < kBlocks; ++k)
+#pragma unroll
+      for (int v = 0; v < 16; v += 4) {
+        const int d = 32 * k + 2 * v + 4 * g;
+        const f32x4 o = {acc[b][k][v] * inv, acc[b][k][v + 1] * inv, acc[b][k][v + 2] * inv, acc[b][k][v + 3] * inv};
+        if (nsplit > 1) {
+          *reinterpret_cast<f32x4*>(partial + part * D + d) = o;
+        } else {
+          const u32x2 o16 = {pack16(o[0], o[1], bf16), pack16(o[2], o[3], bf16)};
+          *reinterpret_cast<u32x2*>(static_cast<char*>(aa.out) + (token * aa.out_stride + (int64_t)head * D + d) * 2) = o16;
+        }
+      }
+    if (g == 0) {
+      if (nsplit > 1) reinterpret_cast<Partial*>(partial + aa.tokens * aa.heads * nsplit * D)[part] = {ref[b], l};
+      else if (aa.lse != nullptr) aa.lse[token * aa.heads + head] = log_sum(ref[b], l);
+    }
+  }
+}
+
+template <int D, int RB>
+hipError_t launch_chunk(const KvAttendArgs& a, const ChunkPlan& p, int bf16, const DequantArgs& da, hipStream_t s) {
+  u32x4* tiles = static_cast<u32x4*>(a.workspace);
+  TileInfo* infos = reinterpret_cast<TileInfo*>(static_cast<char*>(a.workspace) + p.info_at);
+  float* partial = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + p.partial_at);
+  const dim3 grid((unsigned)p.ntiles, (unsigned)a.cache.kv_heads, (unsigned)a.num_seqs);
+  hipError_t e = da.K == 16 ? launch_kernel(expand_kernel<D, 4>, grid, dim3(256), s, a, da, p.ntiles, tiles, infos)
+                            : launch_kernel(expand_kernel<D, 8>, grid, dim3(256), s, a, da, p.ntiles, tiles, infos);
+  if (e != hipSuccess) return e;
+  const dim3 grid2((unsigned)(a.cache.kv_heads * p.nsplit), (unsigned)p.blocks, (unsigned)a.num_seqs);
+  return launch_kernel(chunk_kernel<D, RB>, grid2, dim3(256), s, a, p.ntiles, tiles, infos, p.nsplit, partial, bf16);
+}
+
+}  // namespace
+
+static_assert(sizeof(TileInfo) == 16, "workspace layout");
+
+int launch_kv_chunk(const KvAttendArgs& a, int dtype, const ChunkPlan& p, const DequantArgs& da, void* stream) {
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const int bf16 = dtype == BF16;
+  if (a.cache.head_dim == 64) return (int)launch_chunk<64, 2>(a, p, bf16, da, s);
+  if (a.cache.head_dim == 128) return (int)launch_chunk<128, 1>(a, p, bf16, da, s);
+  return (int)launch_chunk<256, 1>(a, p, bf16, da, s);
+}
+
+}  // namespace bq
