@@ -36,6 +36,19 @@ __device__ __forceinline__ float rows_sum(float v) {
   return bits_f32(s.x) + bits_f32(s.y);
 }
 
+// Larger of three in one instruction (fmaxf of values that may be signalling NaNs, as the compiler has to take
+// a product's, adds an instruction for each).
+__device__ __forceinline__ float max3_hw(float a, float b, float c) {
+  float m;
+  asm("v_max3_f32 %0, %1, %2, %3" : "=v"(m) : "v"(a), "v"(b), "v"(c));
+  return m;
+}
+
+// Weights may grow by 2^kSlack over the running reference of a row before its sums are rescaled: binary16
+// holds them up to 2^16, and with little slack the rows of a wave between them rescale in every other
+// step (slack 2^6: 777 tokens over 6000 keys, head 256: 74 us, 2^12: 65).
+constexpr float kSlack = 12.0f;
+
 // Cached values enter the matrix cores multiplied by a power of two that puts the largest just below
 // 2^kTopBit, so that binary16 (down to 2^-14 in full precision) keeps 11 bits of small ones too.
 constexpr int kTopBit = 14;

@@ -206,9 +206,11 @@ int launch_kv_merge(const KvAttendArgs& a, int dtype, const MergeArgs& m, void* 
 // How k_attn_chunk.hip goes about a call: expanded tiles of keys, rows per workgroup, splits, and where
 // its parts of the workspace begin (bytes).
 struct ChunkPlan {
-  int ntiles, rb, blocks, nsplit;
+  int ntiles, blocks, nsplit;
   size_t info_at, partial_at, end;
 };
+constexpr int kChunkRows = 128;
+int chunk_slots(int head_dim);  // workgroups of that kernel the device holds at once
 int launch_kv_chunk(const KvAttendArgs& a, int dtype, const ChunkPlan& p, const DequantArgs& da, void* stream);
 
 // The library-owned scratch of bq_quantize_nested_noalloc (k_scratch.hip): kScratchBytes per

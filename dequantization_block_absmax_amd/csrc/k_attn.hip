@@ -14,7 +14,7 @@
 // to the largest of their row), q' where it falls 2^-14 below its row's largest element, and the
 // result.  e_i is the exponent of the row's largest |q|.  Weights are kept in range by the reference
 //   M_i = max_j (log2-domain s_ij + E_j),   E_j the exponent of token j's largest value maximum,
-// in place of the plain running maximum: the weights p a' = 2^(s - M) a' then stay below 2^8 whatever
+// in place of the plain running maximum: the weights p a' = 2^(s - M) a' then stay below 2^14 whatever
 // the size of the values, and sum and weighted sum carry the same factor, which cancels.
 //
 // Decomposition.  Work is split over (16 RT rows: new token x query head of one key/value head) x
@@ -43,7 +43,6 @@ namespace {
 
 constexpr int kGroup = 32;        // keys per wave and step
 constexpr int kCopies = 64;       // copies of the LDS table, one per bank: no lookup waits for another
-constexpr float kSlack = 6.0f;    // weights may grow by 2^6 before the sums are rescaled
 
 template <int D, int NB, int KB>
 struct Shape {
@@ -516,9 +515,9 @@ __global__ __launch_bounds__((64 * Occupancy<D, NB, RT>::kWaves), (Occupancy<D, 
     for (int u = 0; u < 2; ++u)
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        float a = 0x1p-100f;
+        float a = max3_hw(0x1p-100f, fabsf(va[u][r][0]), fabsf(va[u][r][NB > 1 ? 1 : 0]));
 #pragma unroll
-        for (int b = 0; b < NB; ++b) a = fmaxf(a, fabsf(va[u][r][b]));
+        for (int b = 2; b + 1 < NB; b += 2) a = max3_hw(a, fabsf(va[u][r][b]), fabsf(va[u][r][b + 1]));
         ev[u][r] = (float)__builtin_amdgcn_frexp_expf(a);
       }
 #pragma unroll
@@ -527,7 +526,7 @@ __global__ __launch_bounds__((64 * Occupancy<D, NB, RT>::kWaves), (Occupancy<D, 
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) top = fmaxf(top, s[t][u][r] + ev[u][r]);
+        for (int r = 0; r < 4; r += 2) top = max3_hw(top, s[t][u][r] + ev[u][r], s[t][u][r + 1] + ev[u][r + 1]);
       if (__any(top > ref[t] + kSlack)) {  // rare after the first groups: raise the reference
         const float up = fmaxf(ref[t], rows_max(top));
         const float f = ref[t] == -INFINITY ? 0.0f : exp2_hw(ref[t] - up);
@@ -694,13 +693,21 @@ static Plan make_plan(const KvAttendArgs& a) {
   if (p.many) {
     ChunkPlan& c = p.chunk;
     c.ntiles = (int)ntiles;
-    c.rb = D == 64 ? 2 : 1;
-    c.blocks = (int)((rows + 128 * c.rb - 1) / (128 * c.rb));
-    // workgroups without splits: the rows there are, whatever their sequences
-    const int64_t base = a.cache.kv_heads * ((a.tokens * group + 128 * c.rb - 1) / (128 * c.rb));
-    int64_t n = (cus + base - 1) / base;
-    n = n < ntiles / 4 ? n : ntiles / 4;
-    c.nsplit = (int)(n < 1 ? 1 : n > kMaxSplits ? kMaxSplits : n);
+    c.blocks = (int)((rows + kChunkRows - 1) / kChunkRows);
+    // Workgroups without splits: the rows there are, whatever their sequences.  Of the numbers of splits,
+    // the one whose rounds of resident workgroups take the least time, a workgroup costing its tiles and
+    // about 6 more (start, end, and its part of the join).
+    const int64_t base = a.cache.kv_heads * ((a.tokens * group + kChunkRows - 1) / kChunkRows);
+    const int64_t slots = chunk_slots(a.cache.head_dim);
+    int64_t best = INT64_MAX;
+    c.nsplit = 1;
+    for (int64_t n = 1; n <= 32 && (n == 1 || n * 4 <= ntiles); ++n) {
+      const int64_t cost = (base * n + slots - 1) / slots * ((ntiles + n - 1) / n + 6);
+      if (cost < best) {
+        best = cost;
+        c.nsplit = (int)n;
+      }
+    }
     c.info_at = (size_t)expanded;
     c.partial_at = (c.info_at + (size_t)(ntiles * a.cache.kv_heads * a.num_seqs) * 16 + 255) & ~(size_t)255;
     c.end = c.partial_at + (c.nsplit > 1 ? (size_t)a.tokens * a.heads * c.nsplit * (D + 2) * 4 : 0);

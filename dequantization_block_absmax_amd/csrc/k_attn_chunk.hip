@@ -12,14 +12,16 @@
 // weights are scaled by 2^(ev - E) before the product (what that rounds away is below 2^-25 of the
 // largest values).
 //
-// chunk_kernel: a workgroup of four waves takes 128 RB rows (new token x query head of one key/value
+// chunk_kernel: a workgroup of four waves takes 128 rows (new token x query head of one key/value
 // head) and walks the tiles of 64 keys with the running maximum and sum of the softmax.  A wave takes
-// RB x 32 rows, with v_mfma_f32_32x32x16_f16; lane l = 32 g + n:
+// 32 rows, with v_mfma_f32_32x32x16_f16; lane l = 32 g + n:
 //   S^T = K' Q^T   A = K' from LDS, B = Q in registers; the result holds row n's scores of the keys
 //                  8 (v / 4) + 4 g + v % 4 of each 32 (element v)
 //   O^T = V'^T P^T B = P^T: 8 keys per lane and step, taken in just that order, so the weights stay where
 //                  they were computed; V' is stored with its keys in the same order.
 #include <hip/hip_runtime.h>
+
+#include <type_traits>
 
 #include "bq_attn.h"
 #include "bq_internal.h"
@@ -29,7 +31,6 @@ namespace bq {
 namespace {
 
 constexpr int kTile = 64;   // keys
-constexpr float kSlack = 6.0f;
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
@@ -155,22 +156,19 @@ __global__ __launch_bounds__(256) void expand_kernel(KvAttendArgs aa, DequantArg
 
 // ---- attention ----------------------------------------------------------------------------
 
-template <int D, int RB>
-struct ChunkOccupancy {
-  static constexpr int kPerSimd = RB * D <= 128 ? 2 : 1;
-};
+// Workgroups per CU (= waves per SIMD) by registers and LDS.
+template <int D>
+constexpr int kChunkPerCu = D == 64 ? 3 : D == 128 ? 2 : 1;
 
-template <int D, int RB>
-__global__ __launch_bounds__(256, (ChunkOccupancy<D, RB>::kPerSimd)) void chunk_kernel(KvAttendArgs aa, int ntiles,
-                                                                                     const u32x4* tiles,
-                                                                                     const TileInfo* infos,
-                                                                                     int nsplit, float* partial,
-                                                                                     int bf16) {
-  constexpr int kRows = 128 * RB;
+template <int D>
+__global__ __launch_bounds__(256, kChunkPerCu<D>) void chunk_kernel(KvAttendArgs aa, int ntiles, const u32x4* tiles,
+                                                                    const TileInfo* infos, int nsplit, float* partial,
+                                                                    int bf16) {
   constexpr int kSteps = D / 16, kBlocks = D / 32;
   constexpr int kPieces = kTile * D / 8;          // of keys, and of values, in a tile
-  constexpr int kStage = 2 * kPieces / 256;       // pieces a thread stages
-  __shared__ u32x4 s_tile[2][2 * kPieces];
+  constexpr int kStage = kPieces / 256;           // pieces of each that a thread stages
+  __shared__ u32x4 s_key[2][kPieces];
+  __shared__ u32x4 s_value[2][kPieces];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int n = lane & 31, g = lane >> 5;
@@ -181,45 +179,52 @@ __global__ __launch_bounds__(256, (ChunkOccupancy<D, RB>::kPerSimd)) void chunk_
   const int nq = min(sq.nq, aa.max_q_len);
   const int nrows = nq * group;
   const int block = (int)gridDim.y - 1 - (int)blockIdx.y;  // later rows see more keys: first
-  if (block * kRows >= nrows || !many_rows(nq, group, aa.num_seqs)) return;
+  if (block * kChunkRows >= nrows || !many_rows(nq, group, aa.num_seqs)) return;
 
   // Tiles of the block's rows together, and this split's.
-  const int last_row = min(block * kRows + kRows, nrows) - 1;
-  const int begin = first_key(aa, sq, block * kRows / group) / kTile;
+  const int last_row = min(block * kChunkRows + kChunkRows, nrows) - 1;
+  const int begin = first_key(aa, sq, block * kChunkRows / group) / kTile;
   const int end = (end_key(aa, sq, last_row / group) + kTile - 1) / kTile;
   const int count = max(end - begin, 0), per = (count + nsplit - 1) / nsplit;
   const int t_first = begin + split * per, t_end = min(t_first + per, end);
-  // keys that every row of the wave sees, and the last that any does
-  const int w_first = min(block * kRows + wave * 32 * RB, last_row), w_last = min(w_first + 32 * RB - 1, last_row);
+  // keys that every row of the wave sees
+  const int w_first = min(block * kChunkRows + wave * 32, last_row), w_last = min(w_first + 31, last_row);
   const int lo_all = first_key(aa, sq, w_last / group), hi_all = end_key(aa, sq, w_first / group);
-  const int hi_any = end_key(aa, sq, w_last / group), lo_any = first_key(aa, sq, w_first / group);
 
   const int64_t head_at = ((int64_t)seq * aa.cache.kv_heads + kvh) * ntiles;
-  u32x4 stage[kStage];
-  auto fetch = [&](int t) {
-    const u32x4* src = tiles + (head_at + t) * (2 * kPieces) + tid;
+  u32x4 stage_k[kStage], stage_v[kStage];
+  auto fetch = [&](u32x4* stage, int t, int side) {
+    const u32x4* src = tiles + (head_at + t) * (2 * kPieces) + side * kPieces + tid;
 #pragma unroll
     for (int k = 0; k < kStage; ++k) stage[k] = src[256 * k];
   };
-  auto put = [&](int buf) {
+  auto put = [&](const u32x4* stage, u32x4* dst) {
 #pragma unroll
-    for (int k = 0; k < kStage; ++k) s_tile[buf][256 * k + tid] = stage[k];
+    for (int k = 0; k < kStage; ++k) dst[256 * k + tid] = stage[k];
   };
-  if (t_first < t_end) fetch(t_first);
+  // a tile ahead and by scalar loads: waiting for them does not wait for the tiles on their way
+  typedef const __attribute__((address_space(4))) uint32_t* ScalarWords;
+  auto find = [&](int t) {
+    const ScalarWords src = (ScalarWords)(uintptr_t)(infos + head_at + t);
+    TileInfo i;
+    i.ek = (int32_t)src[0];
+    i.ev = (int32_t)src[1];
+    i.keys = src[2] | (uint64_t)src[3] << 32;
+    return i;
+  };
+  if (t_first < t_end) fetch(stage_k, t_first, 0);
 
   // Queries as operands: binary16 relative to a power of two of the row, the scale's sign included.
-  int lo[RB], hi[RB];
-  float scale[RB];
-  f16x8 q[RB][kSteps];
-#pragma unroll
-  for (int b = 0; b < RB; ++b) {
-    const int r = block * kRows + (wave * RB + b) * 32 + n;
-    const bool live = r < nrows;
-    const int i = live ? r / group : 0;
-    const int head = kvh * group + (live ? r - i * group : 0);
-    lo[b] = live ? first_key(aa, sq, i) : 0;
-    hi[b] = live ? end_key(aa, sq, i) : 0;
-    const char* src = static_cast<const char*>(aa.q) + ((int64_t)(sq.q0 + i) * aa.q_stride + (int64_t)head * D + 8 * g) * 2;
+  const int r = block * kChunkRows + wave * 32 + n;
+  const bool live = r < nrows;
+  const int row_i = live ? r / group : 0;
+  const int head = kvh * group + (live ? r - row_i * group : 0);
+  const int64_t token = sq.q0 + row_i;
+  const int lo = live ? first_key(aa, sq, row_i) : 0, hi = live ? end_key(aa, sq, row_i) : 0;
+  float scale;
+  f16x8 q[kSteps];
+  {
+    const char* src = static_cast<const char*>(aa.q) + (token * aa.q_stride + (int64_t)head * D + 8 * g) * 2;
     u32x4 w[kSteps];
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) w[s] = *reinterpret_cast<const u32x4*>(src + 32 * s);
@@ -244,166 +249,192 @@ __global__ __launch_bounds__(256, (ChunkOccupancy<D, RB>::kPerSimd)) void chunk_
         const float x0 = bf16 ? bits_f32(x << 16) : (float)h.x, x1 = bf16 ? bits_f32(x & 0xffff0000u) : (float)h.y;
         o[k] = pack_f16(__builtin_ldexpf(x0, -ex) * sign, __builtin_ldexpf(x1, -ex) * sign);
       }
-      q[b][s] = __builtin_bit_cast(f16x8, o);
+      q[s] = __builtin_bit_cast(f16x8, o);
     }
-    scale[b] = __builtin_ldexpf(fabsf(aa.scale) * 1.44269504088896341f, ex);
+    scale = __builtin_ldexpf(fabsf(aa.scale) * 1.44269504088896341f, ex);
   }
 
-  float ref[RB], sum[RB];
-  f32x16 acc[RB][kBlocks];
+  float ref = -INFINITY, sum = 0.0f;
+  f32x16 acc[kBlocks];
 #pragma unroll
-  for (int b = 0; b < RB; ++b) {
-    ref[b] = -INFINITY;
-    sum[b] = 0.0f;
+  for (int i = 0; i < kBlocks; ++i)
+#pragma unroll
+    for (int v = 0; v < 16; ++v) acc[i][v] = 0.0f;
+  int e_all = -1000;  // exponent of the sums
+
+  // Half steps of 32 keys, so that each has independent work for the matrix cores and the vector units:
+  // while half h's weights are computed from its scores, the scores of half h + 1 and the sums with
+  // the weights of half h - 1 are multiplied.
+  f32x16 sc[2];            // scores of the tile's two halves
+  u32x4 w[2][2];           // weights of the halves, 16 keys each
+  w[1][0] = w[1][1] = (u32x4){0, 0, 0, 0};
+  auto multiply_keys = [&](int half, const u32x4* tile) {
+    const f16x8* kp = reinterpret_cast<const f16x8*>(tile) + lane + half * kSteps * 64;
+    f32x16 z;
+#pragma unroll
+    for (int v = 0; v < 16; ++v) z[v] = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kSteps; ++k) z = __builtin_amdgcn_mfma_f32_32x32x16_f16(kp[k * 64], q[k], z, 0, 0, 0);
+    return z;
+  };
+  auto add_values = [&](int half, const u32x4* tile) {
+    const f16x8* vp = reinterpret_cast<const f16x8*>(tile) + lane + half * 2 * 64;
 #pragma unroll
     for (int i = 0; i < kBlocks; ++i)
 #pragma unroll
-      for (int v = 0; v < 16; ++v) acc[b][i][v] = 0.0f;
-  }
-  int e_all = -1000;  // exponent of the sums
-
-  if (t_first < t_end) {
-    put(0);
-    __syncthreads();
-  }
-  for (int t = t_first; t < t_end; ++t) {
-    const int buf = (t - t_first) & 1;
-    fetch(min(t + 1, t_end - 1));
-    const TileInfo info = infos[head_at + t];
-    const int ek = __builtin_amdgcn_readfirstlane(info.ek), ev = __builtin_amdgcn_readfirstlane(info.ev);
-    const int j0 = t * kTile;
-    if (j0 < hi_any && j0 + kTile > lo_any) {  // uniform
-      const f16x8* kp = reinterpret_cast<const f16x8*>(s_tile[buf]) + lane;
-      const f16x8* vp = kp + kPieces;
-      f32x16 s[RB][2];
+      for (int ks = 0; ks < 2; ++ks)
+        acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vp[(i * 4 + ks) * 64], __builtin_bit_cast(f16x8, w[half][ks]), acc[i], 0, 0, 0);
+  };
+  // The half step of half `half` of tile t: next = the tile (and half) whose scores follow, prev = the
+  // tile whose values the other half's weights belong to.
+  auto half_step = [&](auto half_c, int t, const TileInfo& info, const u32x4* next, const u32x4* prev) {
+    constexpr int half = half_c.value;
+    const int ek = info.ek, ev = info.ev;
+    const int j0 = t * kTile + 32 * half;
+    const uint32_t keys = half ? (uint32_t)(info.keys >> 32) : (uint32_t)info.keys;
+    f32x16& s = sc[half];
+    // The half step's products in order: scores of the next half and sums of the previous one in turn, so
+    // that no product waits for the one before it, their operands read kAhead products ahead.
+    constexpr int kMul = 2 * kSteps, kAhead = 6;
+    const f16x8* kp = reinterpret_cast<const f16x8*>(next) + lane + (half ^ 1) * kSteps * 64;
+    const f16x8* vp = reinterpret_cast<const f16x8*>(prev) + lane + (half ^ 1) * 2 * 64;
+    auto operand = [&](int z) { return z & 1 ? vp[((z >> 1) % kBlocks * 4 + (z >> 1) / kBlocks) * 64] : kp[(z >> 1) * 64]; };
+    f16x8 a[kMul];
 #pragma unroll
-      for (int kb = 0; kb < 2; ++kb) {
+    for (int z = 0; z < kAhead; ++z) a[z] = operand(z);
+    __builtin_amdgcn_sched_barrier(0);
+    if (!(j0 >= lo_all && j0 + 32 <= hi_all && keys == ~0u)) {  // some key hidden from some row
 #pragma unroll
-        for (int b = 0; b < RB; ++b)
-#pragma unroll
-          for (int v = 0; v < 16; ++v) s[b][kb][v] = 0.0f;
-#pragma unroll
-        for (int k = 0; k < kSteps; ++k) {
-          const f16x8 a = kp[(kb * kSteps + k) * 64];
-#pragma unroll
-          for (int b = 0; b < RB; ++b) s[b][kb] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a, q[b][k], s[b][kb], 0, 0, 0);
-        }
+      for (int v = 0; v < 16; ++v) {
+        const int key = 8 * (v >> 2) + (v & 3), j = j0 + 4 * g + key;
+        const uint32_t hide = (~(keys >> (4 * g)) >> key) & 1u;
+        s[v] = hide | (uint32_t)(j < lo) | (uint32_t)(j >= hi) ? -INFINITY : s[v];
       }
-      if (!(j0 >= lo_all && j0 + kTile <= hi_all && info.keys == ~0ull)) {  // some key hidden from some row
-        const uint32_t there[2] = {(uint32_t)info.keys >> (4 * g), (uint32_t)(info.keys >> 32) >> (4 * g)};
-#pragma unroll
-        for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-          for (int v = 0; v < 16; ++v) {
-            const int key = 8 * (v >> 2) + (v & 3), j = j0 + 32 * kb + 4 * g + key;
-            const uint32_t hide = (~there[kb] >> key) & 1u;
-#pragma unroll
-            for (int b = 0; b < RB; ++b)
-              s[b][kb][v] = hide | (uint32_t)(j < lo[b]) | (uint32_t)(j >= hi[b]) ? -INFINITY : s[b][kb][v];
-          }
+    }
+    // at least 2^-126: a hidden key's -infinity stays what it is
+    const float f = fmaxf(__builtin_ldexpf(scale, ek - kTopBit), 0x1p-126f);
+    const float sum_before = sum;
+    float top = -INFINITY, p = 0.0f;
+    u32x4 x[2];
+    // Weights of scores v .. v + 1 relative to the reference, and their sum.  The sum takes the weights as
+    // rounded: a row that one key fills gives that key's value.
+    auto weigh = [&](int v, float safe) {
+      const float e = exp2_hw(fmaf(s[v], f, -safe));
+      if (v & 1) {
+        uint32_t pair = pack_f16(p, e);
+        asm volatile("" : "+v"(pair));  // here, beside the products, and not on the side of the branch below
+        sum = __builtin_amdgcn_fdot2(__builtin_bit_cast(f16x2, pair), (f16x2){(_Float16)1.0f, (_Float16)1.0f}, sum, false);
+        x[v >> 3][(v & 7) >> 1] = pair;
+      } else {
+        p = e;
       }
-      if (ev > e_all) {  // uniform; nearly always the first tile only
-        const float f = __builtin_ldexpf(1.0f, max(e_all - ev, -1000));
+    };
+    const float safe = fmaxf(ref, -0x1p120f);
+    f32x16& z_next = sc[half ^ 1];
 #pragma unroll
-        for (int b = 0; b < RB; ++b)
+    for (int v = 0; v < 16; ++v) z_next[v] = 0.0f;
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-          for (int i = 0; i < kBlocks; ++i)
-#pragma unroll
-            for (int v = 0; v < 16; ++v) acc[b][i][v] *= f;
-        e_all = ev;
+    for (int z = 0; z < kMul; ++z) {  // kept in this order
+      if (z & 1) {
+        const int i = (z >> 1) % kBlocks, ks = (z >> 1) / kBlocks;
+        acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a[z], __builtin_bit_cast(f16x8, w[half ^ 1][ks]), acc[i], 0, 0, 0);
+      } else {
+        z_next = __builtin_amdgcn_mfma_f32_32x32x16_f16(a[z], q[z >> 1], z_next, 0, 0, 0);
       }
-      u32x4 p[RB][4];
+      if (z + kAhead < kMul) a[z + kAhead] = operand(z + kAhead);
 #pragma unroll
-      for (int b = 0; b < RB; ++b) {
-        // at least 2^-126: a hidden key's -infinity stays what it is
-        const float sc = fmaxf(__builtin_ldexpf(scale[b], ek - kTopBit), 0x1p-126f);
-        float top = -INFINITY;
-#pragma unroll
-        for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-          for (int v = 0; v < 16; ++v) top = fmaxf(top, s[b][kb][v]);
-        top *= sc;
-        if (__any(top > ref[b] + kSlack)) {  // rare after the first tiles
-          const u32x2 o = __builtin_amdgcn_permlane32_swap(f32_bits(top), f32_bits(top), false, false);
-          const float up = fmaxf(ref[b], fmaxf(bits_f32(o.x), bits_f32(o.y)));
-          const float f = ref[b] == -INFINITY ? 0.0f : exp2_hw(ref[b] - up);
-          ref[b] = up;
-          sum[b] *= f;
-#pragma unroll
-          for (int i = 0; i < kBlocks; ++i)
-#pragma unroll
-            for (int v = 0; v < 16; ++v) acc[b][i][v] *= f;
-        }
-        const float safe = fmaxf(ref[b], -0x1p120f);
-#pragma unroll
-        for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-          for (int v = 0; v < 16; v += 2) {
-            const uint32_t w = pack_f16(exp2_hw(fmaf(s[b][kb][v], sc, -safe)), exp2_hw(fmaf(s[b][kb][v + 1], sc, -safe)));
-            // the sum takes the weights as rounded: a row that one key fills gives that key's value
-            sum[b] = __builtin_amdgcn_fdot2(__builtin_bit_cast(f16x2, w), (f16x2){(_Float16)1.0f, (_Float16)1.0f}, sum[b], false);
-            p[b][2 * kb + (v >> 3)][(v & 7) >> 1] = w;
-          }
+      for (int v = z * 16 / kMul; v < (z + 1) * 16 / kMul; ++v) {
+        weigh(v, safe);
+        if (v & 1) top = max3_hw(top, s[v - 1], s[v]);
       }
-      if (ev < e_all) {  // uniform, rare: the tile's values are in smaller units, so its weights shrink
-        const _Float16 f1 = (_Float16)__builtin_ldexpf(1.0f, max(ev - e_all, -24));
-        const f16x2 f = {f1, f1};
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    top *= f;
+    if (ev > e_all || __any(top > ref + kSlack)) {
+      // Rare after the first tiles: larger units or a larger reference.  The sums so far move to them, and
+      // the weights are taken again.
+      const u32x2 o = __builtin_amdgcn_permlane32_swap(f32_bits(top), f32_bits(top), false, false);
+      const float up = fmaxf(ref, fmaxf(bits_f32(o.x), bits_f32(o.y)));
+      const float down = ref == -INFINITY ? 0.0f : exp2_hw(ref - up);
+      ref = up;
+      sum = sum_before * down;
+      const float units = ev > e_all ? __builtin_ldexpf(down, max(e_all - ev, -1000)) : down;
+      e_all = max(ev, e_all);
 #pragma unroll
-        for (int b = 0; b < RB; ++b)
+      for (int i = 0; i < kBlocks; ++i)
 #pragma unroll
-          for (int ks = 0; ks < 4; ++ks)
+        for (int v = 0; v < 16; ++v) acc[i][v] *= units;
+      const float again = fmaxf(ref, -0x1p120f);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const uint32_t w = p[b][ks][k];
-              p[b][ks][k] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, w) * f);
-            }
-      }
+      for (int v = 0; v < 16; ++v) weigh(v, again);
+    }
+    w[half][0] = x[0];
+    w[half][1] = x[1];
+    if (ev < e_all) {  // uniform, rare: the tile's values are in smaller units, so its weights shrink
+      const _Float16 f1 = (_Float16)__builtin_ldexpf(1.0f, max(ev - e_all, -24));
+      const f16x2 f2 = {f1, f1};
 #pragma unroll
-      for (int ks = 0; ks < 4; ++ks)
+      for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
-        for (int i = 0; i < kBlocks; ++i) {
-          const f16x8 a = vp[(i * 4 + ks) * 64];
-#pragma unroll
-          for (int b = 0; b < RB; ++b)
-            acc[b][i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a, __builtin_bit_cast(f16x8, p[b][ks]), acc[b][i], 0, 0, 0);
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t x = w[half][ks][k];
+          w[half][ks][k] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, x) * f2);
         }
     }
-    put(buf ^ 1);
+  };
+
+  if (t_first < t_end) {
+    put(stage_k, s_key[0]);
+#pragma unroll
+    for (int k = 0; k < kStage; ++k) s_value[1][256 * k + tid] = (u32x4){0, 0, 0, 0};  // no weights wait at first
+    fetch(stage_k, min(t_first + 1, t_end - 1), 0);
+    fetch(stage_v, t_first, 1);
     __syncthreads();
+    sc[0] = multiply_keys(0, s_key[0]);
+    TileInfo info = find(t_first);
+    for (int t = t_first; t < t_end; ++t) {
+      const int b = (t - t_first) & 1;
+      const TileInfo info_next = find(min(t + 1, t_end - 1));
+      half_step(std::integral_constant<int, 0>(), t, info, s_key[b], s_value[b ^ 1]);
+      // The buffers written now were last read in the half step before the previous barrier.
+      put(stage_k, s_key[b ^ 1]);
+      put(stage_v, s_value[b]);
+      __syncthreads();
+      fetch(stage_k, min(t + 2, t_end - 1), 0);
+      fetch(stage_v, min(t + 1, t_end - 1), 1);
+      half_step(std::integral_constant<int, 1>(), t, info, s_key[b ^ 1], s_value[b]);
+      info = info_next;
+    }
+    add_values(1, s_value[(t_end - 1 - t_first) & 1]);
   }
 
   const float unit = e_all > -1000 ? __builtin_ldexpf(1.0f, e_all - kTopBit) : 0.0f;
+  const u32x2 o2 = __builtin_amdgcn_permlane32_swap(f32_bits(sum), f32_bits(sum), false, false);
+  const float l = bits_f32(o2.x) + bits_f32(o2.y);
+  if (!live) return;
+  const int64_t part = (token * aa.heads + head) * nsplit + split;
+  const float inv = nsplit > 1 ? unit : (l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l)) * unit;
 #pragma unroll
-  for (int b = 0; b < RB; ++b) {
-    const int r = block * kRows + (wave * RB + b) * 32 + n;
-    const u32x2 o2 = __builtin_amdgcn_permlane32_swap(f32_bits(sum[b]), f32_bits(sum[b]), false, false);
-    const float l = bits_f32(o2.x) + bits_f32(o2.y);
-    if (r >= nrows) continue;
-    const int i = r / group, head = kvh * group + (r - i * group);
-    const int64_t token = sq.q0 + i;
-    const int64_t part = (token * aa.heads + head) * nsplit + split;
-    const float inv = nsplit > 1 ? unit : (l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l)) * unit;
+  for (int k = 0; k < kBlocks; ++k)
 #pragma unroll
-    for (int k = 0; k < kBlocks; ++k)
-#pragma unroll
-      for (int v = 0; v < 16; v += 4) {
-        const int d = 32 * k + 2 * v + 4 * g;
-        const f32x4 o = {acc[b][k][v] * inv, acc[b][k][v + 1] * inv, acc[b][k][v + 2] * inv, acc[b][k][v + 3] * inv};
-        if (nsplit > 1) {
-          *reinterpret_cast<f32x4*>(partial + part * D + d) = o;
-        } else {
-          const u32x2 o16 = {pack16(o[0], o[1], bf16), pack16(o[2], o[3], bf16)};
-          *reinterpret_cast<u32x2*>(static_cast<char*>(aa.out) + (token * aa.out_stride + (int64_t)head * D + d) * 2) = o16;
-        }
+    for (int v = 0; v < 16; v += 4) {
+      const int d = 32 * k + 2 * v + 4 * g;
+      const f32x4 o = {acc[k][v] * inv, acc[k][v + 1] * inv, acc[k][v + 2] * inv, acc[k][v + 3] * inv};
+      if (nsplit > 1) {
+        *reinterpret_cast<f32x4*>(partial + part * D + d) = o;
+      } else {
+        const u32x2 o16 = {pack16(o[0], o[1], bf16), pack16(o[2], o[3], bf16)};
+        *reinterpret_cast<u32x2*>(static_cast<char*>(aa.out) + (token * aa.out_stride + (int64_t)head * D + d) * 2) = o16;
       }
-    if (g == 0) {
-      if (nsplit > 1) reinterpret_cast<Partial*>(partial + aa.tokens * aa.heads * nsplit * D)[part] = {ref[b], l};
-      else if (aa.lse != nullptr) aa.lse[token * aa.heads + head] = log_sum(ref[b], l);
     }
+  if (g == 0) {
+    if (nsplit > 1) reinterpret_cast<Partial*>(partial + aa.tokens * aa.heads * nsplit * D)[part] = {ref, l};
+    else if (aa.lse != nullptr) aa.lse[token * aa.heads + head] = log_sum(ref, l);
   }
 }
 
-template <int D, int RB>
+template <int D>
 hipError_t launch_chunk(const KvAttendArgs& a, const ChunkPlan& p, int bf16, const DequantArgs& da, hipStream_t s) {
   u32x4* tiles = static_cast<u32x4*>(a.workspace);
   TileInfo* infos = reinterpret_cast<TileInfo*>(static_cast<char*>(a.workspace) + p.info_at);
@@ -413,19 +444,24 @@ hipError_t launch_chunk(const KvAttendArgs& a, const ChunkPlan& p, int bf16, con
                             : launch_kernel(expand_kernel<D, 8>, grid, dim3(256), s, a, da, p.ntiles, tiles, infos);
   if (e != hipSuccess) return e;
   const dim3 grid2((unsigned)(a.cache.kv_heads * p.nsplit), (unsigned)p.blocks, (unsigned)a.num_seqs);
-  return launch_kernel(chunk_kernel<D, RB>, grid2, dim3(256), s, a, p.ntiles, tiles, infos, p.nsplit, partial, bf16);
+  return launch_kernel(chunk_kernel<D>, grid2, dim3(256), s, a, p.ntiles, tiles, infos, p.nsplit, partial, bf16);
 }
 
 }  // namespace
+
+// Workgroups of the attention kernel that the device holds at once.
+int chunk_slots(int head_dim) {
+  return cu_count() * (head_dim == 64 ? kChunkPerCu<64> : head_dim == 128 ? kChunkPerCu<128> : kChunkPerCu<256>);
+}
 
 static_assert(sizeof(TileInfo) == 16, "workspace layout");
 
 int launch_kv_chunk(const KvAttendArgs& a, int dtype, const ChunkPlan& p, const DequantArgs& da, void* stream) {
   hipStream_t s = static_cast<hipStream_t>(stream);
   const int bf16 = dtype == BF16;
-  if (a.cache.head_dim == 64) return (int)launch_chunk<64, 2>(a, p, bf16, da, s);
-  if (a.cache.head_dim == 128) return (int)launch_chunk<128, 1>(a, p, bf16, da, s);
-  return (int)launch_chunk<256, 1>(a, p, bf16, da, s);
+  if (a.cache.head_dim == 64) return (int)launch_chunk<64>(a, p, bf16, da, s);
+  if (a.cache.head_dim == 128) return (int)launch_chunk<128>(a, p, bf16, da, s);
+  return (int)launch_chunk<256>(a, p, bf16, da, s);
 }
 
 }  // namespace bq
