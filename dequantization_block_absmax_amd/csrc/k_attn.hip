@@ -261,6 +261,14 @@ __global__ __launch_bounds__((64 * Occupancy<D, NB, RT>::kWaves), (Occupancy<D, 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int m = lane & 15, g = lane >> 4;
+  // The table's entries are asked for first: they come with the arguments, beside the chain of loads from the
+  // sequence to its pages to its keys.
+  float entry_lo = 0.0f, entry_hi = 0.0f;
+  if (tid < 256) {
+    entry_lo = da.c[KB == 4 ? tid & 15 : tid];
+    entry_hi = da.c[KB == 4 ? tid >> 4 : tid];
+  }
+  load_fence();
   const int split = blockIdx.x;
   const int kvh = blockIdx.y % aa.cache.kv_heads, tile = blockIdx.y / aa.cache.kv_heads;
   const int seq = blockIdx.z;
@@ -365,8 +373,7 @@ __global__ __launch_bounds__((64 * Occupancy<D, NB, RT>::kWaves), (Occupancy<D, 
 
   // Table: entry b in copy c at (b * kCopies + c) * 4; a lane reads copy `lane`.
   if (tid < 256) {
-    const float lo = da.c[KB == 4 ? tid & 15 : tid], hi = da.c[KB == 4 ? tid >> 4 : tid];
-    const uint32_t e = pack_f16(__builtin_ldexpf(lo, kTopBit), __builtin_ldexpf(hi, kTopBit));
+    const uint32_t e = pack_f16(__builtin_ldexpf(entry_lo, kTopBit), __builtin_ldexpf(entry_hi, kTopBit));
     const u32x4 e4 = {e, e, e, e};
 #pragma unroll
     for (int i = 0; i < kCopies / 4; ++i)  // in turn over the banks
@@ -725,7 +732,7 @@ static Plan make_plan(const KvAttendArgs& a) {
     n = n < most ? n : most;
     return n < 1 ? 1 : n > kMaxSplits ? kMaxSplits : n;
   };
-  int64_t n = splits(8 * cus, 512);
+  int64_t n = splits(4 * cus, 512);
   if (n * base < 2 * cus) n = splits(2 * cus, 256);
   p.nsplit = (int)n;
   if (n > 1) p.bytes += (size_t)a.tokens * a.heads * n * (D + 2) * 4;
