@@ -689,6 +689,24 @@ struct Plan {
 // left to the splitting kernel.
 constexpr int64_t kMaxExpanded = (int64_t)4 << 30;
 
+// Splits of the keys: those whose rounds of resident workgroups (`slots`; `base` without splits) take the least
+// time, a workgroup costing its steps of 256 keys and about 3 more (24 windows of 4000 keys, 5 heads: 4 splits
+// 24.4 us, 8 splits 30.0; 64 sequences of up to 8192 keys, 8 heads: 1 split 90.3, 2 splits and their join
+// 89.3, 4 splits 92.5).  With several sequences, whose lengths may differ, a workgroup takes 8192 keys at most.
+static int64_t choose_splits(int64_t base, int64_t slots, int64_t keys, int num_seqs) {
+  const int64_t steps = (keys + 255) / 256;
+  const int64_t least = num_seqs > 1 ? (steps + 31) / 32 : 1;
+  int64_t best = INT64_MAX, n = 1;
+  for (int64_t k = least < kMaxSplits ? least : kMaxSplits; k <= kMaxSplits && (k <= steps || k <= 1); ++k) {
+    const int64_t cost = (base * k + slots - 1) / slots * ((steps + k - 1) / k + 3);
+    if (cost < best) {
+      best = cost;
+      n = k;
+    }
+  }
+  return n < 1 ? 1 : n;
+}
+
 static Plan make_plan(const KvAttendArgs& a) {
   Plan p = {};
   const int64_t group = a.heads / a.cache.kv_heads, D = a.cache.head_dim, cus = cu_count();
@@ -726,14 +744,14 @@ static Plan make_plan(const KvAttendArgs& a) {
   p.rt = rows > 16 && D <= 128 ? 2 : 1;
   p.tiles = (int)((rows + 16 * p.rt - 1) / (16 * p.rt));
   const int64_t base = (int64_t)p.tiles * a.cache.kv_heads * a.num_seqs;
-  auto splits = [&](int64_t target, int64_t keys) {
-    const int64_t most = ((int64_t)a.max_kv_len + keys - 1) / keys;
-    int64_t n = (target + base - 1) / base;
-    n = n < most ? n : most;
-    return n < 1 ? 1 : n > kMaxSplits ? kMaxSplits : n;
-  };
-  int64_t n = splits(4 * cus, 512);
-  if (n * base < 2 * cus) n = splits(2 * cus, 256);
+  const int nb = a.cache.head_dim >> a.cache.log2b;
+  const int64_t slots = cus * (D == 256 || nb == 4 || (p.rt == 2 && D == 128) ? 1 : 2);
+  // the workspace is asked for without a window, and holds for any
+  int64_t n = choose_splits(base, slots, a.max_kv_len, a.num_seqs);
+  if (a.window > 0 && (int64_t)a.window + a.max_q_len < a.max_kv_len) {
+    const int64_t k = choose_splits(base, slots, (int64_t)a.window + a.max_q_len, a.num_seqs);
+    n = k < n ? k : n;
+  }
   p.nsplit = (int)n;
   if (n > 1) p.bytes += (size_t)a.tokens * a.heads * n * (D + 2) * 4;
   return p;
