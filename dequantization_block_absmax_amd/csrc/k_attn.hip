@@ -42,7 +42,8 @@ namespace bq {
 namespace {
 
 constexpr int kGroup = 32;        // keys per wave and step
-constexpr int kCopies = 64;       // copies of the LDS table, one per bank: no lookup waits for another
+constexpr int kEntryBytes = 256;  // of the LDS table: copies for 64 lanes (32 where an entry takes 8 bytes), side
+                                  // by side over the banks: no lookup waits for another
 
 template <int D, int NB, int KB>
 struct Shape {
@@ -110,24 +111,77 @@ __device__ __forceinline__ void load_words(uint32_t* w, Global src) {
   }
 }
 
-// LDS offset of the lane's copy of the entry for byte b of w: byte << 8 | 4 * lane, one permute
-// (lane4 = 4 * lane).
-__device__ __forceinline__ uint32_t entry_of(uint32_t w, int b, uint32_t lane4) {
-  return __builtin_amdgcn_perm(w, lane4, 0x0c0c0000u | (uint32_t)(4 + b) << 8);
+// LDS offset of the lane's copy of the entry for byte b of w: byte << 8 | copy, one permute (copy: the
+// lane's offset in a row of copies).
+__device__ __forceinline__ uint32_t entry_of(uint32_t w, int b, uint32_t copy) {
+  return __builtin_amdgcn_perm(w, copy, 0x0c0c0000u | (uint32_t)(4 + b) << 8);
 }
 
-// Two consecutive operands of a product: 4-bit codes, the pair at byte b of w (low nibble's entry in the
-// low half); 8-bit codes, the entries of byte b of w and byte b2 of w2.
-template <int KB>
-__device__ __forceinline__ uint32_t operand_pair(const char* lut, uint32_t w, int b, uint32_t w2, int b2, uint32_t lane4) {
-  if constexpr (KB == 4) {
-    return *reinterpret_cast<const uint32_t*>(lut + entry_of(w, b, lane4));
-  } else {
-    const f16x2 v = {*reinterpret_cast<const _Float16*>(lut + entry_of(w, b, lane4)),
-                     *reinterpret_cast<const _Float16*>(lut + entry_of(w2, b2, lane4))};
-    return __builtin_bit_cast(uint32_t, v);
+// How a table entry enters the products.  One part (q in bfloat16): its binary16 rounding, 2^-12 relative, far
+// below what the result's rounding leaves.  Two parts (q in binary16): the rounding and, beside it, the
+// rounded rest, 2^-24 relative together; the other operand repeats, and the sum over k adds both.
+//   entries in LDS, by byte: 4-bit codes the pair (low nibble, high nibble), then the rests' pair; 8-bit codes
+//   one entry, then its rest
+template <int KB, bool HL>
+struct Operand {
+  static constexpr int kParts = HL ? 2 : 1;          // products for 8 consecutive operands
+  static constexpr int kLookups = KB == 4 ? 4 : 8;   // bytes that hold their codes
+  static constexpr int kCopyBytes = HL && KB == 4 ? 8 : 4;
+
+  // The 8 entries of the codes at bytes by[] of wd[].
+  static __device__ __forceinline__ void look_up(const char* lut, uint32_t copy, const uint32_t (&wd)[kLookups],
+                                                 const int (&by)[kLookups], f16x8 (&a)[kParts]) {
+    u32x4 x[kParts];
+#pragma unroll
+    for (int i = 0; i < kLookups; ++i) {
+      const char* at = lut + entry_of(wd[i], by[i], copy);
+      if constexpr (KB == 4 && HL) {
+        const u32x2 e = *reinterpret_cast<const u32x2*>(at);
+        x[i / 2][2 * (i & 1)] = e.x;
+        x[i / 2][2 * (i & 1) + 1] = e.y;
+      } else if constexpr (KB == 4) {
+        x[0][i] = *reinterpret_cast<const uint32_t*>(at);
+      } else if constexpr (HL) {
+        x[i / 4][i & 3] = *reinterpret_cast<const uint32_t*>(at);
+      } else if ((i & 1) == 0) {
+        const f16x2 pair = {*reinterpret_cast<const _Float16*>(at),
+                            *reinterpret_cast<const _Float16*>(lut + entry_of(wd[i + 1], by[i + 1], copy))};
+        x[0][i / 2] = __builtin_bit_cast(uint32_t, pair);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kParts; ++k) a[k] = __builtin_bit_cast(f16x8, x[k]);
   }
-}
+
+  // The other operand, from pairs of its 8 values.  `repeat` sets each beside an entry and beside the entry's rest;
+  // `beside` beside the entry only.
+  static __device__ __forceinline__ void repeat(const u32x4& pairs, f16x8 (&b)[kParts]) {
+    if constexpr (!HL) {
+      b[0] = __builtin_bit_cast(f16x8, pairs);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const uint32_t p0 = pairs[2 * k], p1 = pairs[2 * k + 1];
+        u32x4 x;
+        if constexpr (KB == 4) x = (u32x4){p0, p0, p1, p1};
+        else
+          x = (u32x4){__builtin_amdgcn_perm(p0, p0, 0x01000100u), __builtin_amdgcn_perm(p0, p0, 0x03020302u),
+                      __builtin_amdgcn_perm(p1, p1, 0x01000100u), __builtin_amdgcn_perm(p1, p1, 0x03020302u)};
+        b[k] = __builtin_bit_cast(f16x8, x);
+      }
+    }
+  }
+  static __device__ __forceinline__ void beside(const u32x4& pairs, f16x8 (&b)[kParts]) {
+#pragma unroll
+    for (int k = 0; k < kParts; ++k) {
+      const uint32_t p0 = pairs[(2 * k) & 3], p1 = pairs[(2 * k + 1) & 3];
+      u32x4 x;
+      if constexpr (KB == 4) x = (u32x4){p0, 0u, p1, 0u};
+      else x = (u32x4){p0 & 0xffffu, p0 >> 16, p1 & 0xffffu, p1 >> 16};
+      b[k] = __builtin_bit_cast(f16x8, x);
+    }
+  }
+};
 
 // Exchange between lanes m and p of a row of 16: of the lane's bytes in w (two halves), the lane with
 // `upper` false keeps its first half and takes the partner's first half as its second; the other
@@ -239,18 +293,22 @@ template <int D, int NB, int RT>
 struct Occupancy {
   static constexpr int kWaves = D == 256 && NB == 8 ? 4 : 8;
   static constexpr int kPerSimd = D == 256 && NB == 8 ? 1 : RT * D <= 128 && NB <= 2 ? 4 : 2;
+  // room for the weights' rests too (q in binary16; without them the weights are rounded once, 2^-12)
+  static constexpr bool kRests = kPerSimd == 4 ? RT * NB * D <= 128 : kPerSimd == 2 && (NB <= 2 || RT * D == 128);
 };
 
-template <int D, int NB, int KB, int RT>
+template <int D, int NB, int KB, int RT, bool HL>
 __global__ __launch_bounds__((64 * Occupancy<D, NB, RT>::kWaves), (Occupancy<D, NB, RT>::kPerSimd)) void attend_kernel(
-    KvAttendArgs aa, DequantArgs da, int nsplit, float* partial, int rows, int bf16) {
+    KvAttendArgs aa, DequantArgs da, int nsplit, float* partial, int rows) {
+  using O = Operand<KB, HL>;
+  constexpr bool bf16 = !HL;  // the type of q and out
   constexpr int W = Occupancy<D, NB, RT>::kWaves;
   using S = Shape<D, NB, KB>;
   constexpr int kThreads = 64 * W;
   constexpr int kRows = 16 * RT;
   constexpr int kPitch = D + 4;  // of a row of partial sums in LDS
-  constexpr int kLut = 256 * kCopies * 4;
-  constexpr int kQueries = RT * S::kSteps * 64 * 16;     // in the order the lanes read them
+  constexpr int kLut = 256 * kEntryBytes;
+  constexpr int kQueries = RT * S::kSteps * O::kParts * 64 * 16;  // in the order the lanes read them
   constexpr int kMaxima = 32 * NB * 4;                   // one side of a wave's group
   constexpr int kLoop = kLut + kQueries + 2 * W * kMaxima, kSums = W * 16 * kPitch * 4;
   // table, queries and block maxima; after the keys, the waves' sums
@@ -371,15 +429,18 @@ __global__ __launch_bounds__((64 * Occupancy<D, NB, RT>::kWaves), (Occupancy<D, 
     load_values(gi, now, xv);
   }
 
-  // Table: entry b in copy c at (b * kCopies + c) * 4; a lane reads copy `lane`.
+  // Table (see Operand).
   if (tid < 256) {
-    const uint32_t e = pack_f16(__builtin_ldexpf(entry_lo, kTopBit), __builtin_ldexpf(entry_hi, kTopBit));
-    const u32x4 e4 = {e, e, e, e};
+    const float x0 = __builtin_ldexpf(entry_lo, kTopBit), x1 = __builtin_ldexpf(entry_hi, kTopBit);
+    const float r0 = (float)(_Float16)x0, r1 = (float)(_Float16)x1;
+    const uint32_t e = KB == 8 && HL ? pack_f16(x0, x0 - r0) : pack_f16(x0, x1);
+    const uint32_t rest = KB == 4 && HL ? pack_f16(x0 - r0, x1 - r1) : e;
+    const u32x4 e4 = {e, rest, e, rest};
 #pragma unroll
-    for (int i = 0; i < kCopies / 4; ++i)  // in turn over the banks
-      *reinterpret_cast<u32x4*>(s_mem + tid * (kCopies * 4) + ((i + tid) & (kCopies / 4 - 1)) * 16) = e4;
+    for (int i = 0; i < kEntryBytes / 16; ++i)  // in turn over the banks
+      *reinterpret_cast<u32x4*>(s_mem + tid * kEntryBytes + ((i + tid) & (kEntryBytes / 16 - 1)) * 16) = e4;
   }
-  const uint32_t lane4 = lane * 4;
+  const uint32_t copy = (lane * O::kCopyBytes) & (kEntryBytes - 1);
 
   // Queries: wave t sets up the 16 rows of tile t, as the products' operands and a scale per row.
   f16x8* const s_q = reinterpret_cast<f16x8*>(s_mem + kLut);
@@ -423,7 +484,10 @@ __global__ __launch_bounds__((64 * Occupancy<D, NB, RT>::kWaves), (Occupancy<D, 
         // 4-bit codes: the first element of a byte is its high nibble, the high half of the table's pair
         o[k] = KB == 4 ? pack_f16(b, a) : pack_f16(a, b);
       }
-      s_q[(wave * S::kSteps + s) * 64 + lane] = __builtin_bit_cast(f16x8, o);
+      f16x8 b[O::kParts];
+      O::repeat(o, b);
+#pragma unroll
+      for (int k = 0; k < O::kParts; ++k) s_q[((wave * S::kSteps + s) * O::kParts + k) * 64 + lane] = b[k];
     }
     if (g == 0) s_scale[wave * 16 + m] = __builtin_ldexpf(aa.scale * 1.44269504088896341f, ex - kTopBit);
   }
@@ -463,22 +527,23 @@ __global__ __launch_bounds__((64 * Occupancy<D, NB, RT>::kWaves), (Occupancy<D, 
       f32x4 z[RT];
 #pragma unroll
       for (int k = 0; k < S::kSteps; ++k) {
-        u32x4 w;
+        uint32_t wd[O::kLookups];
+        int by[O::kLookups];
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          if constexpr (KB == 4) w[b] = operand_pair<4>(s_mem, x.code[u][k], b, 0, 0, lane4);
-          else {
-            const uint32_t c = x.code[u][2 * k + (b >> 1)];
-            w[b] = operand_pair<8>(s_mem, c, 2 * (b & 1), c, 2 * (b & 1) + 1, lane4);
-          }
+        for (int b = 0; b < O::kLookups; ++b) {
+          wd[b] = x.code[u][k * S::kStepWords + b / 4];
+          by[b] = b & 3;
         }
-        const f16x8 a = __builtin_bit_cast(f16x8, w);
+        f16x8 a[O::kParts];
+        O::look_up(s_mem, copy, wd, by, a);
         constexpr int per_block = S::kSteps / NB;
         const int b = k / per_block;
 #pragma unroll
         for (int t = 0; t < RT; ++t) {
           if (k % per_block == 0) z[t] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
-          z[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, s_q[(t * S::kSteps + k) * 64 + lane], z[t], 0, 0, 0);
+#pragma unroll
+          for (int h = 0; h < O::kParts; ++h)
+            z[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[h], s_q[((t * S::kSteps + k) * O::kParts + h) * 64 + lane], z[t], 0, 0, 0);
           if (k % per_block == per_block - 1) {
 #pragma unroll
             for (int r = 0; r < 4; ++r)
@@ -496,7 +561,8 @@ __global__ __launch_bounds__((64 * Occupancy<D, NB, RT>::kWaves), (Occupancy<D, 
   };
 
   // Weights of the lane's 8 keys, block by block, as pairs of binary16.
-  uint32_t w[RT][NB][4];
+  constexpr bool kRests = HL && Occupancy<D, NB, RT>::kRests;
+  u32x4 w[RT][NB], rest[RT][kRests ? NB : 1];  // and what rounding them left
   auto weights = [&](int j0, const Pages& p, const Values<D, NB, KB>& x) {
     float va[2][4][NB];
     put_maxima(1, x.a);
@@ -552,7 +618,15 @@ __global__ __launch_bounds__((64 * Occupancy<D, NB, RT>::kWaves), (Occupancy<D, 
           const float p0 = exp2_hw(s[t][u][r] - safe), p1 = exp2_hw(s[t][u][r + 1] - safe);
           sum[t] += p0 + p1;
 #pragma unroll
-          for (int b = 0; b < NB; ++b) w[t][b][2 * u + r / 2] = pack_f16(p0 * va[u][r][b], p1 * va[u][r + 1][b]);
+          for (int b = 0; b < NB; ++b) {
+            const float w0 = p0 * va[u][r][b], w1 = p1 * va[u][r + 1][b];
+            const uint32_t pair = pack_f16(w0, w1);
+            w[t][b][2 * u + r / 2] = pair;
+            if constexpr (kRests) {
+              const f16x2 h = __builtin_bit_cast(f16x2, pair);
+              rest[t][b][2 * u + r / 2] = pack_f16(w0 - (float)h.x, w1 - (float)h.y);
+            }
+          }
         }
     }
   };
@@ -577,19 +651,29 @@ __global__ __launch_bounds__((64 * Occupancy<D, NB, RT>::kWaves), (Occupancy<D, 
       for (int by = 0; by < kBytes; ++by)
 #pragma unroll
         for (int h = 0; h < kPer; ++h) {
-          u32x4 a;
+          uint32_t wds[O::kLookups];
+          int bys[O::kLookups];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            if constexpr (KB == 4) a[k] = operand_pair<4>(s_mem, pair[k][h], by, 0, 0, lane4);
-            else a[k] = operand_pair<8>(s_mem, x.code[2 * k][wd], by, x.code[2 * k + 1][wd], by, lane4);
+          for (int k = 0; k < O::kLookups; ++k) {
+            wds[k] = KB == 4 ? pair[k & 3][h] : x.code[k][wd];
+            bys[k] = by;
           }
+          f16x8 a[O::kParts];
+          O::look_up(s_mem, copy, wds, bys, a);
           const int i = (4 * wd + by) * kPer + h;  // tile: place i of the lane's d's
           const int b = i / S::kPerBlock;
 #pragma unroll
-          for (int t = 0; t < RT; ++t)
-            acc[t][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
-                __builtin_bit_cast(f16x8, a),
-                __builtin_bit_cast(f16x8, (u32x4){w[t][b][0], w[t][b][1], w[t][b][2], w[t][b][3]}), acc[t][i], 0, 0, 0);
+          for (int t = 0; t < RT; ++t) {
+            f16x8 p[O::kParts];
+            O::repeat(w[t][b], p);
+#pragma unroll
+            for (int k = 0; k < O::kParts; ++k) acc[t][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[k], p[k], acc[t][i], 0, 0, 0);
+            if constexpr (kRests) {
+              O::beside(rest[t][b], p);
+#pragma unroll
+              for (int k = 0; k < O::kParts; ++k) acc[t][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[k], p[k], acc[t][i], 0, 0, 0);
+            }
+          }
         }
     }
   };
@@ -761,12 +845,17 @@ size_t kv_attend_workspace(const KvAttendArgs& a, int) { return make_plan(a).byt
 
 namespace {
 
-template <int D, int NB, int KB, int RT>
-hipError_t launch_rows(const KvAttendArgs& a, const Plan& p, int dtype, const DequantArgs& da, hipStream_t s) {
+template <int D, int NB, int KB, int RT, bool HL>
+hipError_t launch_type(const KvAttendArgs& a, const Plan& p, const DequantArgs& da, hipStream_t s) {
   const dim3 grid((unsigned)p.nsplit, (unsigned)(p.tiles * a.cache.kv_heads), (unsigned)a.num_seqs);
   float* partial = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + p.partial_at);
-  return launch_kernel(attend_kernel<D, NB, KB, RT>, grid, dim3(64 * Occupancy<D, NB, RT>::kWaves), s, a, da, p.nsplit,
-                       partial, p.many ? kFewOnly : kAllRows, dtype == BF16);
+  return launch_kernel(attend_kernel<D, NB, KB, RT, HL>, grid, dim3(64 * Occupancy<D, NB, RT>::kWaves), s, a, da, p.nsplit,
+                       partial, p.many ? kFewOnly : kAllRows);
+}
+
+template <int D, int NB, int KB, int RT>
+hipError_t launch_rows(const KvAttendArgs& a, const Plan& p, int dtype, const DequantArgs& da, hipStream_t s) {
+  return dtype == F16 ? launch_type<D, NB, KB, RT, true>(a, p, da, s) : launch_type<D, NB, KB, RT, false>(a, p, da, s);
 }
 
 template <int D, int NB>
