@@ -75,6 +75,39 @@ __global__ __launch_bounds__(256) void expand_kernel(KvAttendArgs aa, DequantArg
     if (lane < 2) s_listed[lane] = (uint32_t)(all >> (32 * lane));
   }
   __syncthreads();
+  constexpr int kRow = D * KB / 8;
+  // The codes are on their way while the maxima are worked out.
+  // keys: a unit is 8 d of one key; values: 4 d of the 8 keys of a piece
+  constexpr int kKeyUnits = kTile * D / 8 / 256, kValueUnits = (kTile * D / 32 + 255) / 256;
+  u32x2 key_code[kKeyUnits];
+  uint32_t value_code[kValueUnits][8];
+  auto key_unit = [&](int p, int& key, int& d8) {
+    const int s = (p >> 6) % (D / 16);
+    d8 = 2 * s + ((p >> 5) & 1);
+    key = (p >> 6) / (D / 16) * 32 + (p & 31);
+  };
+  auto value_unit = [&](int p, int e, int& key, int& d4) {
+    const int oct = p / (D / 4), g = oct & 1, ks = oct >> 1;
+    d4 = p % (D / 4);
+    key = 16 * ks + 8 * (e >> 2) + 4 * g + (e & 3);
+  };
+#pragma unroll
+  for (int k = 0; k < kKeyUnits; ++k) {
+    int key, d8;
+    key_unit(256 * k + tid, key, d8);
+    const uint8_t* src = aa.cache.packed[0] + max(s_row[key], (int64_t)0) * kRow + d8 * KB;
+    if constexpr (KB == 4) key_code[k] = (u32x2){*reinterpret_cast<const uint32_t*>(src), 0u};
+    else key_code[k] = *reinterpret_cast<const u32x2*>(src);
+  }
+#pragma unroll
+  for (int k = 0; k < kValueUnits; ++k)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      int key, d4;
+      value_unit(min(256 * k + tid, kTile * D / 32 - 1), e, key, d4);
+      const uint8_t* src = aa.cache.packed[1] + max(s_row[key], (int64_t)0) * kRow + d4 * KB / 2;
+      value_code[k][e] = KB == 4 ? *reinterpret_cast<const uint16_t*>(src) : *reinterpret_cast<const uint32_t*>(src);
+    }
   uint32_t top[2] = {0, 0};
   for (int e = tid; e < kTile << log2nb; e += 256) {
     const int64_t row = s_row[e >> log2nb];
@@ -104,49 +137,40 @@ __global__ __launch_bounds__(256) void expand_kernel(KvAttendArgs aa, DequantArg
   u32x4* const kt = tiles + at * (2 * kTile * D / 8);
   u32x4* const vt = kt + kTile * D / 8;
 
-  constexpr int kRow = D * KB / 8;
-  // keys: a unit is 8 d of one key
 #pragma unroll
-  for (int p0 = 0; p0 < kTile * D / 8; p0 += 256) {
-    const int p = p0 + tid;
-    const int s = (p >> 6) % (D / 16), d8 = 2 * s + ((p >> 5) & 1), key = (p >> 6) / (D / 16) * 32 + (p & 31);
-    const int64_t row = max(s_row[key], (int64_t)0);
-    const uint8_t* src = aa.cache.packed[0] + row * kRow + d8 * KB;
+  for (int k = 0; k < kKeyUnits; ++k) {
+    int key, d8;
+    key_unit(256 * k + tid, key, d8);
     const float a = s_a[0][(key << log2nb) + (d8 * 8 >> aa.cache.log2b)];
-    u32x2 c;
-    if constexpr (KB == 4) c = (u32x2){*reinterpret_cast<const uint32_t*>(src), 0u};
-    else c = *reinterpret_cast<const u32x2*>(src);
+    const u32x2 c = key_code[k];
     u32x4 w;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const uint32_t q0 = KB == 4 ? (c.x >> (8 * k + 4)) & 15u : ((k < 2 ? c.x : c.y) >> (16 * (k & 1))) & 255u;
-      const uint32_t q1 = KB == 4 ? (c.x >> (8 * k)) & 15u : ((k < 2 ? c.x : c.y) >> (16 * (k & 1) + 8)) & 255u;
-      w[k] = pack_f16((s_c[q0] * a) * fk, (s_c[q1] * a) * fk);
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t q0 = KB == 4 ? (c.x >> (8 * i + 4)) & 15u : ((i < 2 ? c.x : c.y) >> (16 * (i & 1))) & 255u;
+      const uint32_t q1 = KB == 4 ? (c.x >> (8 * i)) & 15u : ((i < 2 ? c.x : c.y) >> (16 * (i & 1) + 8)) & 255u;
+      w[i] = pack_f16((s_c[q0] * a) * fk, (s_c[q1] * a) * fk);
     }
-    kt[p] = w;
+    kt[256 * k + tid] = w;
   }
-  // values: a unit is 4 d of the 8 keys of a piece
 #pragma unroll
-  for (int p0 = 0; p0 < kTile * D / 32; p0 += 256) {
-    const int p = p0 + tid;
+  for (int k = 0; k < kValueUnits; ++k) {
+    const int p = 256 * k + tid;
     if (kTile * D / 32 < 256 && p >= kTile * D / 32) break;
-    const int d4 = p % (D / 4), oct = p / (D / 4), g = oct & 1, ks = oct >> 1;
     float v[8][4];
+    int key, d4;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const int key = 16 * ks + 8 * (e >> 2) + 4 * g + (e & 3);
-      const int64_t row = max(s_row[key], (int64_t)0);
-      const uint8_t* src = aa.cache.packed[1] + row * kRow + d4 * KB / 2;
+      value_unit(p, e, key, d4);
       const float a = s_a[1][(key << log2nb) + (d4 * 4 >> aa.cache.log2b)];
-      const uint32_t c = KB == 4 ? *reinterpret_cast<const uint16_t*>(src) : *reinterpret_cast<const uint32_t*>(src);
+      const uint32_t c = value_code[k][e];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const uint32_t q = KB == 4 ? (c >> (8 * (i >> 1) + ((i & 1) ? 0 : 4))) & 15u : (c >> (8 * i)) & 255u;
         v[e][i] = (s_c[q] * a) * fv;
       }
     }
-    const int d = d4 * 4;
-    u32x4* dst = vt + ((d >> 5) * 4 + ks) * 64 + 32 * g + (d & 31);
+    const int d = d4 * 4, oct = p / (D / 4);
+    u32x4* dst = vt + ((d >> 5) * 4 + (oct >> 1)) * 64 + 32 * (oct & 1) + (d & 31);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       dst[i] = (u32x4){pack_f16(v[0][i], v[1][i]), pack_f16(v[2][i], v[3][i]), pack_f16(v[4][i], v[5][i]),

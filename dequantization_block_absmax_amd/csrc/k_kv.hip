@@ -11,9 +11,12 @@
 // Work decomposition.  A unit is 8 consecutive elements of one token's head.  Lane `tid` of a
 // 256-lane workgroup handles units (tile * U + u) * 256 + tid, u < U, of the tokens' units in
 // (token, head, d) order; grid row 0 takes the keys, row 1 the values.  A block is B / 8 = 4 .. 32
-// neighbouring lanes, whose maximum is joined by lane permutes.  Both kernels stream: U = 4 units
-// per lane keep that many 16-byte loads in flight and spread the table over 8192 elements; calls
-// whose tiles of 4 would leave compute units without a workgroup take U = 1.
+// neighbouring lanes, whose maximum is joined by lane permutes.  Both kernels stream and are bound by HBM for
+// long inputs, by their launch for a decoding step (3 us).  On MI355X:
+//   write  one unit per lane, ordinary loads: 16384 tokens of 8 x 128 bf16 into 8-bit codes, B = 128, take 22.0 us
+//          (4.6 TB/s of input and cache); two units 22.4, four 25.0, four with non-temporal loads 27.0
+//   read   two units per lane where that leaves every CU several workgroups: 32768 tokens of 8 x 128 from
+//          4-bit codes, B = 64, to bf16 take 25.9 us (6.6 TB/s); one unit 32.5, four 27.3, eight 29.9
 #include <hip/hip_runtime.h>
 
 #include "bq_device.h"
@@ -100,7 +103,7 @@ struct KvWriteArgs {
   uint8_t* packed[2];
 };
 
-template <int DT, int KB, int MODE, int M, int U>
+template <int DT, int KB, int MODE, int M>
 __global__ __launch_bounds__(kThreads) void kv_write_kernel(KvWriteArgs ka, KvShape sh, QuantArgs qa) {
   using E = typename Entry<M>::type;
   __shared__ float s_thr[260];
@@ -111,66 +114,58 @@ __global__ __launch_bounds__(kThreads) void kv_write_kernel(KvWriteArgs ka, KvSh
   const int64_t stride = ka.stride[side];
 
   const auto lw = lut_fetch<MODE, M, kThreads>(qa, tid);
-  Place at[U];
-  Unit<DT> x[U];
+  const uint32_t u = blockIdx.x * (uint32_t)kThreads + tid;
+  Place at = place(min(u, sh.units - 1), sh);
+  // lanes past the end repeat the last unit; whole blocks of them (units come in whole rows)
+  if (u >= sh.units) at.flat = -1;
+  const u32x4* src = reinterpret_cast<const u32x4*>(in + at.token * stride + (int64_t)at.col * (DT == F32 ? 4 : 2));
+  Unit<DT> x;
 #pragma unroll
-  for (int i = 0; i < U; ++i) {
-    const uint32_t u = (blockIdx.x * U + i) * (uint32_t)kThreads + tid;
-    at[i] = place(min(u, sh.units - 1), sh);
-    const u32x4* src = reinterpret_cast<const u32x4*>(in + at[i].token * stride + (int64_t)at[i].col * (DT == F32 ? 4 : 2));
-    // lanes past the end repeat the last unit; whole blocks of them (units come in whole rows)
-    if (u >= sh.units) at[i].flat = -1;
-#pragma unroll
-    for (int k = 0; k < (DT == F32 ? 2 : 1); ++k) {
-      const u32x4 v = __builtin_nontemporal_load(src + k);
-      x[i].w[4 * k] = v.x;
-      x[i].w[4 * k + 1] = v.y;
-      x[i].w[4 * k + 2] = v.z;
-      x[i].w[4 * k + 3] = v.w;
-    }
+  for (int k = 0; k < (DT == F32 ? 2 : 1); ++k) {
+    const u32x4 v = src[k];
+    x.w[4 * k] = v.x;
+    x.w[4 * k + 1] = v.y;
+    x.w[4 * k + 2] = v.z;
+    x.w[4 * k + 3] = v.w;
   }
   lut_fill<MODE, M, kThreads>(qa, lw, s_lut, s_thr, tid);
 
+  // Block maximum over finite elements, as the bits of |x| (ordered like the values).
   const int lanes = 1 << (sh.log2b - 3);  // lanes of a block
+  uint32_t m = 0;
+  bool finite = true;
 #pragma unroll
-  for (int i = 0; i < U; ++i) {
-    // Block maximum over finite elements, as the bits of |x| (ordered like the values).
-    uint32_t m = 0;
-    bool finite = true;
+  for (int e = 0; e < 8; ++e) {
+    const uint32_t b = f32_bits(element<DT>(x, e)) & 0x7fffffffu;
+    finite = finite && b < 0x7f800000u;
+    m = max(m, b < 0x7f800000u ? b : 0u);
+  }
+  m = group_max_u32(m, lanes);
+  const float a = bits_f32(m);
+  const float s = a < 0x1p-64f ? 0x1p64f : (a > 0x1p64f ? 0x1p-64f : 1.0f);
+  const float r = 1.0f / (a * s);
+  uint32_t q[8];
+  if (__builtin_expect(__all(finite && s == 1.0f && a > 0.0f), 1)) {
+#pragma unroll
+    for (int e = 0; e < 8; e += 2)
+      nearest_pair<MODE, M>(element<DT>(x, e) * r, element<DT>(x, e + 1) * r, qa, s_lut, s_thr, q[e], q[e + 1]);
+  } else {
+    // a non-finite element and every element of a zero block take y = 0, whose code is z
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const uint32_t b = f32_bits(element<DT>(x[i], e)) & 0x7fffffffu;
-      finite = finite && b < 0x7f800000u;
-      m = max(m, b < 0x7f800000u ? b : 0u);
+      const float v = element<DT>(x, e);
+      const float y = (v * s) * r;
+      q[e] = nearest_code<MODE, M>(a > 0.0f && fabsf(v) <= 0x1.fffffep127f ? y : 0.0f, qa, s_lut, s_thr);
     }
-    m = group_max_u32(m, lanes);
-    const float a = bits_f32(m);
-    const float s = a < 0x1p-64f ? 0x1p64f : (a > 0x1p64f ? 0x1p-64f : 1.0f);
-    const float r = 1.0f / (a * s);
-    uint32_t q[8];
-    if (__builtin_expect(__all(finite && s == 1.0f && a > 0.0f), 1)) {
-#pragma unroll
-      for (int e = 0; e < 8; e += 2)
-        nearest_pair<MODE, M>(element<DT>(x[i], e) * r, element<DT>(x[i], e + 1) * r, qa, s_lut, s_thr, q[e],
-                              q[e + 1]);
+  }
+  if (at.flat >= 0) {
+    if constexpr (KB == 4) {
+      *reinterpret_cast<uint32_t*>(ka.packed[side] + (at.flat >> 1)) = pack_word<4>(q);
     } else {
-      // a non-finite element and every element of a zero block take y = 0, whose code is z
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float v = element<DT>(x[i], e);
-        const float y = (v * s) * r;
-        q[e] = nearest_code<MODE, M>(a > 0.0f && fabsf(v) <= 0x1.fffffep127f ? y : 0.0f, qa, s_lut, s_thr);
-      }
+      const u32x2 w = {pack_word<8>(q), pack_word<8>(q + 4)};
+      *reinterpret_cast<u32x2*>(ka.packed[side] + at.flat) = w;
     }
-    if (at[i].flat >= 0) {
-      if constexpr (KB == 4) {
-        *reinterpret_cast<uint32_t*>(ka.packed[side] + (at[i].flat >> 1)) = pack_word<4>(q);
-      } else {
-        const u32x2 w = {pack_word<8>(q), pack_word<8>(q + 4)};
-        *reinterpret_cast<u32x2*>(ka.packed[side] + at[i].flat) = w;
-      }
-      if ((tid & (lanes - 1)) == 0) ka.absmax[side][at[i].flat >> sh.log2b] = a;
-    }
+    if ((tid & (lanes - 1)) == 0) ka.absmax[side][at.flat >> sh.log2b] = a;
   }
 }
 
@@ -264,8 +259,8 @@ KvShape make_shape(const KvCacheArgs& c, int64_t tokens, const int64_t* slots) {
   return sh;
 }
 
-// Units per lane: 4 once the tiles of 4 give every CU two workgroups.
-int units_per_lane(const KvShape& sh) { return (int64_t)sh.units >= (int64_t)cu_count() * 4 * kThreads ? 4 : 1; }
+// Units per lane of a read: 2 once tiles of 2 give every CU four workgroups.
+int units_per_lane(const KvShape& sh) { return (int64_t)sh.units >= (int64_t)cu_count() * 4 * kThreads ? 2 : 1; }
 
 dim3 kv_grid(const KvShape& sh, int u) {
   return dim3((unsigned)(((int64_t)sh.units + u * kThreads - 1) / (u * kThreads)), 2);
@@ -273,9 +268,7 @@ dim3 kv_grid(const KvShape& sh, int u) {
 
 template <int DT, int KB, int MODE, int M>
 hipError_t write_units(const KvWriteArgs& ka, const KvShape& sh, const QuantArgs& qa, hipStream_t s) {
-  if (units_per_lane(sh) == 4)
-    return launch_kernel(kv_write_kernel<DT, KB, MODE, M, 4>, kv_grid(sh, 4), dim3(kThreads), s, ka, sh, qa);
-  return launch_kernel(kv_write_kernel<DT, KB, MODE, M, 1>, kv_grid(sh, 1), dim3(kThreads), s, ka, sh, qa);
+  return launch_kernel(kv_write_kernel<DT, KB, MODE, M>, kv_grid(sh, 1), dim3(kThreads), s, ka, sh, qa);
 }
 
 template <int DT, int KB>
@@ -301,8 +294,8 @@ hipError_t write_dt(const KvWriteArgs& ka, const KvShape& sh, const PreparedTabl
 
 template <int DT, int KB>
 hipError_t read_units(const KvReadArgs& ka, const KvShape& sh, const DequantArgs& da, hipStream_t s) {
-  if (units_per_lane(sh) == 4)
-    return launch_kernel(kv_read_kernel<DT, KB, 4>, kv_grid(sh, 4), dim3(kThreads), s, ka, sh, da);
+  if (units_per_lane(sh) == 2)
+    return launch_kernel(kv_read_kernel<DT, KB, 2>, kv_grid(sh, 2), dim3(kThreads), s, ka, sh, da);
   return launch_kernel(kv_read_kernel<DT, KB, 1>, kv_grid(sh, 1), dim3(kThreads), s, ka, sh, da);
 }
 
