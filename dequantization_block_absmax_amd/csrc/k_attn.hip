@@ -327,8 +327,8 @@ __global__ __launch_bounds__((64 * Occupancy<D, NB, RT>::kWaves), (Occupancy<D, 
     entry_hi = da.c[KB == 4 ? tid >> 4 : tid];
   }
   load_fence();
-  const int split = blockIdx.x;
-  const int kvh = blockIdx.y % aa.cache.kv_heads, tile = blockIdx.y / aa.cache.kv_heads;
+  const int split = blockIdx.x % nsplit, tile = blockIdx.x / nsplit;
+  const int kvh = blockIdx.y;
   const int seq = blockIdx.z;
   const int group = aa.heads / aa.cache.kv_heads;
   const Sequence sq = sequence(aa, seq);
@@ -847,7 +847,7 @@ namespace {
 
 template <int D, int NB, int KB, int RT, bool HL>
 hipError_t launch_type(const KvAttendArgs& a, const Plan& p, const DequantArgs& da, hipStream_t s) {
-  const dim3 grid((unsigned)p.nsplit, (unsigned)(p.tiles * a.cache.kv_heads), (unsigned)a.num_seqs);
+  const dim3 grid((unsigned)(p.tiles * p.nsplit), (unsigned)a.cache.kv_heads, (unsigned)a.num_seqs);
   float* partial = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + p.partial_at);
   return launch_kernel(attend_kernel<D, NB, KB, RT, HL>, grid, dim3(64 * Occupancy<D, NB, RT>::kWaves), s, a, da, p.nsplit,
                        partial, p.many ? kFewOnly : kAllRows);
@@ -884,8 +884,8 @@ hipError_t launch_few(const KvAttendArgs& a, const Plan& p, int dtype, const Deq
 
 int launch_kv_attend(const KvAttendArgs& a, int dtype, const DequantArgs& da, void* stream) {
   const Plan p = make_plan(a);
-  // grid rows
-  if ((p.few && (int64_t)p.tiles * a.cache.kv_heads > 65535) || (p.many && (p.chunk.blocks > 65535 || a.cache.kv_heads > 65535))) {
+  // workgroups along x (the launch itself counts threads), grid rows
+  if ((p.few && (int64_t)p.tiles * p.nsplit > INT32_MAX) || a.cache.kv_heads > 32767 || (p.many && p.chunk.blocks > 65535)) {
     g_launch_refused_for_size = true;
     return (int)hipErrorInvalidConfiguration;
   }

@@ -42,20 +42,22 @@ struct TileInfo {
 
 // ---- expansion ----------------------------------------------------------------------------
 //
-// Workgroup: one tile of one head.  Fragment order of a tile (16-byte pieces of 8 binary16):
+// Workgroup: the keys or the values of one tile of one head.  Fragment order of a tile (16-byte pieces of 8 binary16):
 //   K' piece ((kb * D/16 + s) * 64 + 32 g + n): key 32 kb + n, d = 16 s + 8 g + 0 .. 7
 //   V' piece ((db * 4 + ks) * 64 + 32 g + n):   d = 32 db + n, keys 16 ks + 8 (e / 4) + 4 g + e % 4, e = 0 .. 7
 template <int D, int KB>
 __global__ __launch_bounds__(256) void expand_kernel(KvAttendArgs aa, DequantArgs da, int ntiles, u32x4* tiles,
                                                      TileInfo* infos) {
   __shared__ float s_c[256];
-  __shared__ float s_a[2][kTile * 8];    // block maxima of the tile's keys and values, zero for keys that do not exist
+  __shared__ float s_a[kTile * 8];       // block maxima of the tile's keys or values, zero for keys that do not exist
   __shared__ int64_t s_row[kTile];       // pool row of each key
-  __shared__ uint32_t s_top[2][4];
+  __shared__ uint32_t s_top[4];
   __shared__ uint32_t s_listed[2];
+  __shared__ u32x4 s_out[kTile * D / 8]; // values' pieces, in their order
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int tile = blockIdx.x, kvh = blockIdx.y, seq = blockIdx.z;
+  const int tile = blockIdx.x, kvh = blockIdx.y >> 1, side = blockIdx.y & 1, seq = blockIdx.z;
+  const float entry = da.c[tid];
   const Sequence sq = sequence(aa, seq);
   const int group = aa.heads / aa.cache.kv_heads;
   if (!many_rows(min(sq.nq, aa.max_q_len), group, aa.num_seqs)) return;
@@ -63,7 +65,7 @@ __global__ __launch_bounds__(256) void expand_kernel(KvAttendArgs aa, DequantArg
   if (tile * kTile >= end_key(aa, sq, i_last) || (tile + 1) * kTile <= first_key(aa, sq, 0)) return;  // not read
   const int log2nb = __builtin_ctz(D) - aa.cache.log2b, nb = 1 << log2nb;
 
-  s_c[tid] = da.c[tid];
+  s_c[tid] = entry;
   if (wave == 0) {
     const int j = tile * kTile + lane;
     const int id = j < sq.kv ? aa.page_table[(int64_t)seq * aa.table_stride + (j >> aa.cache.log2_page)] : -1;
@@ -76,6 +78,7 @@ __global__ __launch_bounds__(256) void expand_kernel(KvAttendArgs aa, DequantArg
   }
   __syncthreads();
   constexpr int kRow = D * KB / 8;
+  const uint8_t* const packed = aa.cache.packed[side];
   // The codes are on their way while the maxima are worked out.
   // keys: a unit is 8 d of one key; values: 4 d of the 8 keys of a piece
   constexpr int kKeyUnits = kTile * D / 8 / 256, kValueUnits = (kTile * D / 32 + 255) / 256;
@@ -91,66 +94,67 @@ __global__ __launch_bounds__(256) void expand_kernel(KvAttendArgs aa, DequantArg
     d4 = p % (D / 4);
     key = 16 * ks + 8 * (e >> 2) + 4 * g + (e & 3);
   };
+  if (side == 0) {
 #pragma unroll
-  for (int k = 0; k < kKeyUnits; ++k) {
-    int key, d8;
-    key_unit(256 * k + tid, key, d8);
-    const uint8_t* src = aa.cache.packed[0] + max(s_row[key], (int64_t)0) * kRow + d8 * KB;
-    if constexpr (KB == 4) key_code[k] = (u32x2){*reinterpret_cast<const uint32_t*>(src), 0u};
-    else key_code[k] = *reinterpret_cast<const u32x2*>(src);
-  }
-#pragma unroll
-  for (int k = 0; k < kValueUnits; ++k)
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      int key, d4;
-      value_unit(min(256 * k + tid, kTile * D / 32 - 1), e, key, d4);
-      const uint8_t* src = aa.cache.packed[1] + max(s_row[key], (int64_t)0) * kRow + d4 * KB / 2;
-      value_code[k][e] = KB == 4 ? *reinterpret_cast<const uint16_t*>(src) : *reinterpret_cast<const uint32_t*>(src);
+    for (int k = 0; k < kKeyUnits; ++k) {
+      int key, d8;
+      key_unit(256 * k + tid, key, d8);
+      const uint8_t* src = packed + max(s_row[key], (int64_t)0) * kRow + d8 * KB;
+      if constexpr (KB == 4) key_code[k] = (u32x2){*reinterpret_cast<const uint32_t*>(src), 0u};
+      else key_code[k] = *reinterpret_cast<const u32x2*>(src);
     }
-  uint32_t top[2] = {0, 0};
+  } else {
+#pragma unroll
+    for (int k = 0; k < kValueUnits; ++k)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        int key, d4;
+        value_unit(min(256 * k + tid, kTile * D / 32 - 1), e, key, d4);
+        const uint8_t* src = packed + max(s_row[key], (int64_t)0) * kRow + d4 * KB / 2;
+        value_code[k][e] = KB == 4 ? *reinterpret_cast<const uint16_t*>(src) : *reinterpret_cast<const uint32_t*>(src);
+      }
+  }
+  uint32_t top = 0;
   for (int e = tid; e < kTile << log2nb; e += 256) {
     const int64_t row = s_row[e >> log2nb];
-#pragma unroll
-    for (int side = 0; side < 2; ++side) {
-      const float a = row >= 0 ? aa.cache.absmax[side][(row << log2nb) + (e & (nb - 1))] : 0.0f;
-      s_a[side][e] = a;
-      top[side] = max(top[side], f32_bits(a) & 0x7fffffffu);
-    }
+    const float a = row >= 0 ? aa.cache.absmax[side][(row << log2nb) + (e & (nb - 1))] : 0.0f;
+    s_a[e] = a;
+    top = max(top, f32_bits(a) & 0x7fffffffu);
   }
 #pragma unroll
-  for (int side = 0; side < 2; ++side) {
-#pragma unroll
-    for (int x = 1; x < 64; x <<= 1) top[side] = max(top[side], (uint32_t)__shfl_xor((int)top[side], x));
-    if (lane == 0) s_top[side][wave] = top[side];
-  }
+  for (int x = 1; x < 64; x <<= 1) top = max(top, (uint32_t)__shfl_xor((int)top, x));
+  if (lane == 0) s_top[wave] = top;
   __syncthreads();
-  // exponents: |a| < 2^e (zeros: the least)
-  auto exponent = [&](int side) {
-    const uint32_t t = max(max(s_top[side][0], s_top[side][1]), max(s_top[side][2], s_top[side][3]));
-    return min(max((int)(t >> 23) - 126, -100), 120);
-  };
-  const int ek = exponent(0), ev = (exponent(1) + 127) / 8 * 8 - 120;
-  const float fk = __builtin_ldexpf(1.0f, kTopBit - ek), fv = __builtin_ldexpf(1.0f, kTopBit - ev);
+  // exponent: |a| < 2^e (zeros: the least); the values' is a multiple of 8
+  top = max(max(s_top[0], s_top[1]), max(s_top[2], s_top[3]));
+  const int least = min(max((int)(top >> 23) - 126, -100), 120);
+  const int ex = side == 0 ? least : (least + 127) / 8 * 8 - 120;
+  const float f = __builtin_ldexpf(1.0f, kTopBit - ex);
   const int64_t at = ((int64_t)seq * aa.cache.kv_heads + kvh) * ntiles + tile;
-  if (tid == 0) infos[at] = {ek, ev, s_listed[0] | (uint64_t)s_listed[1] << 32};
-  u32x4* const kt = tiles + at * (2 * kTile * D / 8);
-  u32x4* const vt = kt + kTile * D / 8;
+  if (tid == 0) {
+    if (side == 0) infos[at].ek = ex;
+    else infos[at].ev = ex;
+    if (side == 0) infos[at].keys = s_listed[0] | (uint64_t)s_listed[1] << 32;
+  }
+  u32x4* const out = tiles + at * (2 * kTile * D / 8) + side * (kTile * D / 8);
 
+  if (side == 0) {
 #pragma unroll
-  for (int k = 0; k < kKeyUnits; ++k) {
-    int key, d8;
-    key_unit(256 * k + tid, key, d8);
-    const float a = s_a[0][(key << log2nb) + (d8 * 8 >> aa.cache.log2b)];
-    const u32x2 c = key_code[k];
-    u32x4 w;
+    for (int k = 0; k < kKeyUnits; ++k) {
+      int key, d8;
+      key_unit(256 * k + tid, key, d8);
+      const float a = s_a[(key << log2nb) + (d8 * 8 >> aa.cache.log2b)];
+      const u32x2 c = key_code[k];
+      u32x4 w;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t q0 = KB == 4 ? (c.x >> (8 * i + 4)) & 15u : ((i < 2 ? c.x : c.y) >> (16 * (i & 1))) & 255u;
-      const uint32_t q1 = KB == 4 ? (c.x >> (8 * i)) & 15u : ((i < 2 ? c.x : c.y) >> (16 * (i & 1) + 8)) & 255u;
-      w[i] = pack_f16((s_c[q0] * a) * fk, (s_c[q1] * a) * fk);
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t q0 = KB == 4 ? (c.x >> (8 * i + 4)) & 15u : ((i < 2 ? c.x : c.y) >> (16 * (i & 1))) & 255u;
+        const uint32_t q1 = KB == 4 ? (c.x >> (8 * i)) & 15u : ((i < 2 ? c.x : c.y) >> (16 * (i & 1) + 8)) & 255u;
+        w[i] = pack_f16((s_c[q0] * a) * f, (s_c[q1] * a) * f);
+      }
+      out[256 * k + tid] = w;
     }
-    kt[256 * k + tid] = w;
+    return;
   }
 #pragma unroll
   for (int k = 0; k < kValueUnits; ++k) {
@@ -161,21 +165,24 @@ __global__ __launch_bounds__(256) void expand_kernel(KvAttendArgs aa, DequantArg
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       value_unit(p, e, key, d4);
-      const float a = s_a[1][(key << log2nb) + (d4 * 4 >> aa.cache.log2b)];
+      const float a = s_a[(key << log2nb) + (d4 * 4 >> aa.cache.log2b)];
       const uint32_t c = value_code[k][e];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const uint32_t q = KB == 4 ? (c >> (8 * (i >> 1) + ((i & 1) ? 0 : 4))) & 15u : (c >> (8 * i)) & 255u;
-        v[e][i] = (s_c[q] * a) * fv;
+        v[e][i] = (s_c[q] * a) * f;
       }
     }
     const int d = d4 * 4, oct = p / (D / 4);
-    u32x4* dst = vt + ((d >> 5) * 4 + (oct >> 1)) * 64 + 32 * (oct & 1) + (d & 31);
+    u32x4* dst = s_out + ((d >> 5) * 4 + (oct >> 1)) * 64 + 32 * (oct & 1) + (d & 31);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       dst[i] = (u32x4){pack_f16(v[0][i], v[1][i]), pack_f16(v[2][i], v[3][i]), pack_f16(v[4][i], v[5][i]),
                        pack_f16(v[6][i], v[7][i])};
   }
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < kTile * D / 8 / 256; ++k) out[256 * k + tid] = s_out[256 * k + tid];
 }
 
 // ---- attention ----------------------------------------------------------------------------
@@ -463,7 +470,7 @@ hipError_t launch_chunk(const KvAttendArgs& a, const ChunkPlan& p, int bf16, con
   u32x4* tiles = static_cast<u32x4*>(a.workspace);
   TileInfo* infos = reinterpret_cast<TileInfo*>(static_cast<char*>(a.workspace) + p.info_at);
   float* partial = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + p.partial_at);
-  const dim3 grid((unsigned)p.ntiles, (unsigned)a.cache.kv_heads, (unsigned)a.num_seqs);
+  const dim3 grid((unsigned)p.ntiles, (unsigned)a.cache.kv_heads * 2, (unsigned)a.num_seqs);
   hipError_t e = da.K == 16 ? launch_kernel(expand_kernel<D, 4>, grid, dim3(256), s, a, da, p.ntiles, tiles, infos)
                             : launch_kernel(expand_kernel<D, 8>, grid, dim3(256), s, a, da, p.ntiles, tiles, infos);
   if (e != hipSuccess) return e;
