@@ -382,8 +382,8 @@ size_t bq_kv_attention_workspace_bytes(const bq_kv_cache* cache, const bq_kv_bat
  *     out[i] = sum_j p_ij v_j,   p_ij = softmax over j of scale * (q_i . k_j),
  * query head h over key/value head h / (heads / kv_heads), keys and values being the cached
  * fl32(c[q] * a).  Row i at position t sees the keys j <= t if `causal` is nonzero, else all kv_len;
- * of these, if window > 0, those with j > t - window.  Cached values of keys it does not see do not
- * matter (they may be NaN).  A row that sees no key gives zeros, and -infinity in lse.
+ * of these, if window > 0, those with j > t - window.  What is cached for keys that no row of a
+ * sequence sees does not matter (it may be NaN).  A row that sees no key gives zeros, and -infinity in lse.
  *   dtype      BQ_F16 or BQ_BF16: the type of q and out.
  *   q          [device] tokens rows of heads * head_dim elements, 16-byte aligned; q_stride elements
  *              from row to row (at least heads * head_dim, a multiple of 8).
