@@ -461,8 +461,8 @@ static bq_status check_attention_shape(const bq_kv_cache* cache, const bq_kv_bat
   if (cache->head_dim != 64 && cache->head_dim != 128 && cache->head_dim != 256) return BQ_ERR_FORMAT;
   if (b == nullptr) return BQ_ERR_NULL;
   if (heads < 1 || heads % cache->kv_heads != 0 || heads > (1 << 20)) return BQ_ERR_SIZE;
-  if (b->num_seqs < 0 || b->num_seqs > 65535 || b->tokens < 0 || b->tokens > INT32_MAX || b->table_stride < 0 ||
-      b->table_stride > INT32_MAX || b->max_q_len < 0 || b->max_kv_len < 0)
+  if (b->num_seqs < 0 || b->num_seqs > 65535 || b->tokens < 0 || b->tokens > INT32_MAX / heads ||
+      b->table_stride < 0 || b->table_stride > INT32_MAX || b->max_q_len < 0 || b->max_kv_len < 0)
     return BQ_ERR_SIZE;
   a->table_stride = b->table_stride;
   a->tokens = b->tokens;
@@ -472,6 +472,7 @@ static bq_status check_attention_shape(const bq_kv_cache* cache, const bq_kv_bat
   // keys the page table can hold at all
   const int64_t held = b->table_stride * cache->page_size;
   a->max_kv_len = held < b->max_kv_len ? (int32_t)held : b->max_kv_len;
+  if (a->max_kv_len > 1 << 30) return BQ_ERR_SIZE;
   a->heads = heads;
   return BQ_OK;
 }

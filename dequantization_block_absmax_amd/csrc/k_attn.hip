@@ -738,7 +738,7 @@ __global__ __launch_bounds__((64 * Occupancy<D, NB, RT>::kWaves), (Occupancy<D, 
 #pragma unroll
       for (int v = 0; v < W; ++v) {
         const Partial p = s_part[v][t * 16 + row];
-        l_all += p.m == -INFINITY ? 0.0f : p.l * exp2_hw(p.m - m_all);
+        l_all += p.m == -INFINITY ? p.l : p.l * exp2_hw(p.m - m_all);  // no reference: zero, or NaN from q
       }
       f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
@@ -796,8 +796,9 @@ static Plan make_plan(const KvAttendArgs& a) {
   const int64_t group = a.heads / a.cache.kv_heads, D = a.cache.head_dim, cus = cu_count();
   int64_t rows = a.max_q_len * group;
   const int64_t ntiles = ((int64_t)a.max_kv_len + 63) / 64;
-  const int64_t expanded = ntiles * a.cache.kv_heads * a.num_seqs * 64 * D * 4;
-  p.many = rows > 2 * kFewRows && ntiles > 0 && expanded <= kMaxExpanded;
+  const int64_t per_tile = (int64_t)a.cache.kv_heads * a.num_seqs * 64 * D * 4;  // at most 2^52
+  p.many = rows > 2 * kFewRows && ntiles > 0 && ntiles <= kMaxExpanded / per_tile;
+  const int64_t expanded = p.many ? ntiles * per_tile : 0;
   p.few = !p.many || a.num_seqs > 1;
   if (p.many) {
     ChunkPlan& c = p.chunk;
@@ -885,7 +886,8 @@ hipError_t launch_few(const KvAttendArgs& a, const Plan& p, int dtype, const Deq
 int launch_kv_attend(const KvAttendArgs& a, int dtype, const DequantArgs& da, void* stream) {
   const Plan p = make_plan(a);
   // workgroups along x (the launch itself counts threads), grid rows
-  if ((p.few && (int64_t)p.tiles * p.nsplit > INT32_MAX) || a.cache.kv_heads > 32767 || (p.many && p.chunk.blocks > 65535)) {
+  if ((p.few && (int64_t)p.tiles * p.nsplit > INT32_MAX) || a.cache.kv_heads > 32767 ||
+      (p.many && (int64_t)a.cache.kv_heads * p.chunk.nsplit * p.chunk.blocks > INT32_MAX)) {
     g_launch_refused_for_size = true;
     return (int)hipErrorInvalidConfiguration;
   }

@@ -34,7 +34,7 @@ constexpr int kTile = 64;   // keys
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
-// What a tile's expansion leaves beside its values: exponents, and which of its keys exist.
+// What a tile's expansion leaves beside its values: exponents, and which of its keys some row sees.
 struct TileInfo {
   int32_t ek, ev;
   uint64_t keys;
@@ -49,7 +49,7 @@ template <int D, int KB>
 __global__ __launch_bounds__(256) void expand_kernel(KvAttendArgs aa, DequantArgs da, int ntiles, u32x4* tiles,
                                                      TileInfo* infos) {
   __shared__ float s_c[256];
-  __shared__ float s_a[kTile * 8];       // block maxima of the tile's keys or values, zero for keys that do not exist
+  __shared__ float s_a[kTile * 8];       // block maxima of the tile's keys or values; zero (theirs may be NaN) where no row sees the key
   __shared__ int64_t s_row[kTile];       // pool row of each key
   __shared__ uint32_t s_top[4];
   __shared__ uint32_t s_listed[2];
@@ -62,13 +62,14 @@ __global__ __launch_bounds__(256) void expand_kernel(KvAttendArgs aa, DequantArg
   const int group = aa.heads / aa.cache.kv_heads;
   if (!many_rows(min(sq.nq, aa.max_q_len), group, aa.num_seqs)) return;
   const int i_last = min(sq.nq, aa.max_q_len) - 1;
-  if (tile * kTile >= end_key(aa, sq, i_last) || (tile + 1) * kTile <= first_key(aa, sq, 0)) return;  // not read
+  const int first = first_key(aa, sq, 0), end = end_key(aa, sq, i_last);  // keys that some row sees
+  if (tile * kTile >= end || (tile + 1) * kTile <= first) return;         // not read
   const int log2nb = __builtin_ctz(D) - aa.cache.log2b, nb = 1 << log2nb;
 
   s_c[tid] = entry;
   if (wave == 0) {
     const int j = tile * kTile + lane;
-    const int id = j < sq.kv ? aa.page_table[(int64_t)seq * aa.table_stride + (j >> aa.cache.log2_page)] : -1;
+    const int id = j >= first && j < end ? aa.page_table[(int64_t)seq * aa.table_stride + (j >> aa.cache.log2_page)] : -1;
     const bool listed = (uint32_t)id < (uint32_t)aa.cache.num_pages;
     s_row[lane] = listed ? (((int64_t)id * aa.cache.kv_heads + kvh) << aa.cache.log2_page) +
                                (j & ((1 << aa.cache.log2_page) - 1))
@@ -193,8 +194,8 @@ constexpr int kChunkPerCu = D == 64 ? 3 : D == 128 ? 2 : 1;
 
 template <int D>
 __global__ __launch_bounds__(256, kChunkPerCu<D>) void chunk_kernel(KvAttendArgs aa, int ntiles, const u32x4* tiles,
-                                                                    const TileInfo* infos, int nsplit, float* partial,
-                                                                    int bf16) {
+                                                                    const TileInfo* infos, int nblocks, int nsplit,
+                                                                    float* partial, int bf16) {
   constexpr int kSteps = D / 16, kBlocks = D / 32;
   constexpr int kPieces = kTile * D / 8;          // of keys, and of values, in a tile
   constexpr int kStage = kPieces / 256;           // pieces of each that a thread stages
@@ -203,13 +204,15 @@ __global__ __launch_bounds__(256, kChunkPerCu<D>) void chunk_kernel(KvAttendArgs
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int n = lane & 31, g = lane >> 5;
-  const int kvh = blockIdx.x % aa.cache.kv_heads, split = blockIdx.x / aa.cache.kv_heads;
+  // fastest the key/value head: with 8 of them each stays on one XCD, whose L2 its tiles share
+  const int kvh = blockIdx.x % aa.cache.kv_heads, rest = blockIdx.x / aa.cache.kv_heads;
+  const int split = rest % nsplit;
   const int seq = blockIdx.z;
   const int group = aa.heads / aa.cache.kv_heads;
   const Sequence sq = sequence(aa, seq);
   const int nq = min(sq.nq, aa.max_q_len);
   const int nrows = nq * group;
-  const int block = (int)gridDim.y - 1 - (int)blockIdx.y;  // later rows see more keys: first
+  const int block = nblocks - 1 - rest / nsplit;  // later rows see more keys: first
   if (block * kChunkRows >= nrows || !many_rows(nq, group, aa.num_seqs)) return;
 
   // Tiles of the block's rows together, and this split's.
@@ -474,8 +477,8 @@ hipError_t launch_chunk(const KvAttendArgs& a, const ChunkPlan& p, int bf16, con
   hipError_t e = da.K == 16 ? launch_kernel(expand_kernel<D, 4>, grid, dim3(256), s, a, da, p.ntiles, tiles, infos)
                             : launch_kernel(expand_kernel<D, 8>, grid, dim3(256), s, a, da, p.ntiles, tiles, infos);
   if (e != hipSuccess) return e;
-  const dim3 grid2((unsigned)(a.cache.kv_heads * p.nsplit), (unsigned)p.blocks, (unsigned)a.num_seqs);
-  return launch_kernel(chunk_kernel<D>, grid2, dim3(256), s, a, p.ntiles, tiles, infos, p.nsplit, partial, bf16);
+  const dim3 grid2((unsigned)(a.cache.kv_heads * p.nsplit * p.blocks), 1u, (unsigned)a.num_seqs);
+  return launch_kernel(chunk_kernel<D>, grid2, dim3(256), s, a, p.ntiles, tiles, infos, p.blocks, p.nsplit, partial, bf16);
 }
 
 }  // namespace

@@ -171,7 +171,7 @@ __global__ __launch_bounds__(64 * kWaves) void merge_kernel(KvAttendArgs aa, Mer
 template <int D>
 hipError_t launch_dim(const KvAttendArgs& a, const MergeArgs& m, int bf16, hipStream_t s) {
   const int64_t rows = a.tokens * a.heads;
-  if (m.nsplit[0] > 16 || m.nsplit[1] > 16)
+  if ((m.nsplit[0] > 16 || m.nsplit[1] > 16) && rows <= 1 << 24)  // a launch counts threads in 32 bits
     return launch_kernel(merge_kernel<D>, dim3((unsigned)rows), dim3(64 * kWaves), s, a, m, bf16);
   const int64_t per = kWaves * (64 / (D / 4));
   return launch_kernel(merge_few_kernel<D>, dim3((unsigned)((rows + per - 1) / per)), dim3(64 * kWaves), s, a, m, bf16);
@@ -182,10 +182,6 @@ hipError_t launch_dim(const KvAttendArgs& a, const MergeArgs& m, int bf16, hipSt
 int launch_kv_merge(const KvAttendArgs& a, int dtype, const MergeArgs& m, void* stream) {
   hipStream_t s = static_cast<hipStream_t>(stream);
   const int bf16 = dtype == BF16;
-  if (a.tokens * a.heads > INT32_MAX) {
-    g_launch_refused_for_size = true;
-    return (int)hipErrorInvalidConfiguration;
-  }
   if (a.cache.head_dim == 64) return (int)launch_dim<64>(a, m, bf16, s);
   if (a.cache.head_dim == 128) return (int)launch_dim<128>(a, m, bf16, s);
   return (int)launch_dim<256>(a, m, bf16, s);

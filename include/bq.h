@@ -395,8 +395,9 @@ size_t bq_kv_attention_workspace_bytes(const bq_kv_cache* cache, const bq_kv_bat
  * Products are summed in binary32; see k_attn.hip for what is rounded to 16 bits on the way.
  * Results are the same on every call on one device.  Block maxima of keys that are seen must be
  * finite and at most 2^100.
- * Errors: BQ_ERR_DTYPE; BQ_ERR_SIZE (a negative count or length, num_seqs > 65535, heads, a stride,
- * window < 0, a scale that is not finite, or a launch of more than 2^32 - 1 threads); BQ_ERR_WORKSPACE;
+ * Errors: BQ_ERR_DTYPE; BQ_ERR_SIZE (a negative count or length, num_seqs > 65535, heads, tokens * heads
+ * above INT32_MAX, more than 2^30 keys, a stride, window < 0, a scale that is not finite, kv_heads above
+ * 32767, or a launch of more than 2^32 - 1 threads); BQ_ERR_WORKSPACE;
  * otherwise as bq_kv_write.  tokens, num_seqs or max_q_len of 0 enqueue nothing. */
 bq_status bq_kv_attention(const bq_kv_cache* cache, const bq_kv_batch* batch, bq_dtype dtype, const void* q,
                           int64_t q_stride, int32_t heads, float scale, int32_t causal, int32_t window, void* out,

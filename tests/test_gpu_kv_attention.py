@@ -7,7 +7,7 @@ import torch
 import dequantization_block_absmax_amd as bq
 import synth
 from gpu_helpers import BQ_DT
-from kv_helpers import Batch, Pool, check_attention, hide_unused, queries, run_attention
+from kv_helpers import Batch, Pool, check_attention, hide_unused, queries, reference, run_attention
 
 pytestmark = pytest.mark.gpu
 
@@ -239,3 +239,58 @@ def test_offsets_beyond_32_bits(dev):
     bq.check(bq.bq_kv_attention(cache, b, bq.BQ_F16, q, q.stride(0), 8, 0.06, 1, 0, out, out.stride(0), None, ws, size))
     torch.cuda.synchronize()
     assert torch.equal(out.view(torch.int16), want.view(torch.int16))
+
+
+@pytest.mark.parametrize("dim,B,bits", [(64, 32, 4), (128, 128, 8), (256, 64, 4)])
+@pytest.mark.parametrize("lens,window", [([(1, 200), (3, 150)], 70), ([(90, 300), (70, 110), (2, 90)], 37),
+                                         ([(150, 500)], 100)], ids=["few", "many", "alone"])
+def test_keys_that_no_row_sees_may_be_nan(dev, lens, window, dim, B, bits):
+    """Behind the window (within a page and a tile that later keys share) the cache holds NaN maxima."""
+    rng, pool, batch = setup(dev, 21, lens, 4, 2, dim, B, 32, bits)
+    for s, (n, kv) in enumerate(lens):
+        j = np.arange(max(0, kv - n - window + 1))
+        page, slot = torch.from_numpy(batch.table[s, j // 32]).long().to(dev), torch.from_numpy(j % 32).to(dev)
+        for side in range(2):
+            pool.absmax[side].view(pool.num_pages, 2, 32, dim // B)[page, :, slot] = float("nan")
+    q = queries(dev, rng, batch.tokens, 4, dim, "bfloat16")
+    check_attention(dev, pool, batch, q, "bfloat16", 0.09, 1, window)
+
+
+@pytest.mark.parametrize("lens", [[(1, 130)], [(5, 3000)], [(2, 40), (90, 400)], [(100, 5000)]],
+                         ids=["one", "splits", "mixed", "chunk splits"])
+@pytest.mark.parametrize("bad", ["nan", "inf", "-inf"])
+def test_queries_that_are_not_finite(dev, lens, bad):
+    """A query that is not finite makes its own result NaN and no other."""
+    rng, pool, batch = setup(dev, 22, lens, 8, 2, 128, 64, 16, 4)
+    q = queries(dev, rng, batch.tokens, 8, 128, "bfloat16")
+    want, want_lse, tol, tol_lse = reference(pool, batch, q, "bfloat16", 0.09)
+    rows = [(batch.tokens - 1, 3), (0, 6)]
+    for token, head in rows:
+        q[token, head, 5 + head] = float(bad)
+    out, lse = run_attention(dev, pool, batch, q, "bfloat16", 0.09)
+    torch.cuda.synchronize()
+    out, lse = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    for token, head in rows:
+        assert np.isnan(out[token, head]).all()
+        assert bad != "nan" or np.isnan(lse[token, head])
+        out[token, head], lse[token, head] = want[token, head], want_lse[token, head]
+    assert (np.abs(out - want) <= tol).all() and (np.abs(lse - want_lse) <= tol_lse).all()
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_mixed_sizes(dev, seed):
+    """Heads, head sizes, pages, blocks and batches of single tokens, drafts and chunks, drawn."""
+    rng = np.random.default_rng(1000 + seed)
+    dim, B = SHAPES[rng.integers(len(SHAPES))]
+    kv_heads, group = int(rng.integers(1, 4)), int(rng.choice([1, 2, 3, 5, 8]))
+    lens = []
+    for _ in range(rng.integers(1, 6)):
+        n = int(rng.choice([0, 1, 1, 4, 37, 170]))
+        lens.append((n, n + int(rng.choice([0, 3, 100, 800, 2500]))))
+    lens.append((int(rng.choice([1, 3, 70])), int(rng.integers(70, 1500))))
+    window = int(rng.choice([0, 0, 50, 700]))
+    dtype = "float16" if rng.integers(2) else "bfloat16"
+    rng, pool, batch = setup(dev, seed, lens, group * kv_heads, kv_heads, dim, B, int(rng.choice([16, 32, 128])),
+                             int(rng.choice([4, 8])))
+    q = queries(dev, rng, batch.tokens, group * kv_heads, dim, dtype)
+    check_attention(dev, pool, batch, q, dtype, dim ** -0.5, int(seed % 5 != 0), window, tag=str(lens))

@@ -135,3 +135,17 @@ def test_attention_workspace():
     assert attend(b=long, workspace_bytes=need - 1) == bq.BQ_ERR_WORKSPACE
     assert attend(b=long, workspace=None) == bq.BQ_ERR_WORKSPACE
     assert attend(b=long, workspace=FAKE + 128) == bq.BQ_ERR_ALIGNMENT
+
+
+def test_attention_sizes_beyond_int32():
+    """Counts whose products leave 32 or 64 bits are refused, or planned without overflow."""
+    for kw in (dict(tokens=(1 << 31) // 16), dict(tokens=1 << 30, max_q_len=1 << 30)):
+        assert attend(b=batch(**kw)) == bq.BQ_ERR_SIZE, kw
+    wide = dict(max_kv_len=2 ** 31 - 1, table_stride=2 ** 31 - 1)
+    assert attend(b=batch(**wide)) == bq.BQ_ERR_SIZE
+    assert bq.bq_kv_attention_workspace_bytes(cache(), batch(**wide), bq.BQ_BF16, 16) == 0
+    # an expanded copy of 2^77 bytes is not taken for a small one
+    c = cache(kv_heads=1 << 19, num_pages=1, page_size=16, head_dim=128, blocksize=128)
+    b = batch(num_seqs=65535, tokens=2047, max_q_len=2047, max_kv_len=1 << 30, table_stride=1 << 26)
+    need = bq.bq_kv_attention_workspace_bytes(c, b, bq.BQ_BF16, 1 << 20)
+    assert need <= (2047 << 20) * 64 * (128 + 2) * 4 + 256
