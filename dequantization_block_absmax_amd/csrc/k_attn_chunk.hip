@@ -227,14 +227,11 @@ __global__ __launch_bounds__(256, kChunkPerCu<D>) void chunk_kernel(KvAttendArgs
 
   const int64_t head_at = ((int64_t)seq * aa.cache.kv_heads + kvh) * ntiles;
   u32x4 stage_k[kStage], stage_v[kStage];
+  auto source = [&](int t, int side) { return tiles + (head_at + t) * (2 * kPieces) + side * kPieces + tid; };
   auto fetch = [&](u32x4* stage, int t, int side) {
-    const u32x4* src = tiles + (head_at + t) * (2 * kPieces) + side * kPieces + tid;
+    const u32x4* src = source(t, side);
 #pragma unroll
     for (int k = 0; k < kStage; ++k) stage[k] = src[256 * k];
-  };
-  auto put = [&](const u32x4* stage, u32x4* dst) {
-#pragma unroll
-    for (int k = 0; k < kStage; ++k) dst[256 * k + tid] = stage[k];
   };
   // a tile ahead and by scalar loads: waiting for them does not wait for the tiles on their way
   typedef const __attribute__((address_space(4))) uint32_t* ScalarWords;
@@ -320,8 +317,8 @@ __global__ __launch_bounds__(256, kChunkPerCu<D>) void chunk_kernel(KvAttendArgs
         acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vp[(i * 4 + ks) * 64], __builtin_bit_cast(f16x8, w[half][ks]), acc[i], 0, 0, 0);
   };
   // The half step of half `half` of tile t: next = the tile (and half) whose scores follow, prev = the
-  // tile whose values the other half's weights belong to.
-  auto half_step = [&](auto half_c, int t, const TileInfo& info, const u32x4* next, const u32x4* prev) {
+  // tile whose values the other half's weights belong to; beside every second product, move(k) passes a piece on.
+  auto half_step = [&](auto half_c, int t, const TileInfo& info, const u32x4* next, const u32x4* prev, auto move) {
     constexpr int half = half_c.value;
     const int ek = info.ek, ev = info.ev;
     const int j0 = t * kTile + 32 * half;
@@ -377,6 +374,7 @@ __global__ __launch_bounds__(256, kChunkPerCu<D>) void chunk_kernel(KvAttendArgs
         z_next = __builtin_amdgcn_mfma_f32_32x32x16_f16(a[z], q[z >> 1], z_next, 0, 0, 0);
       }
       if (z + kAhead < kMul) a[z + kAhead] = operand(z + kAhead);
+      if (z & 1) move(z >> 1);
 #pragma unroll
       for (int v = z * 16 / kMul; v < (z + 1) * 16 / kMul; ++v) {
         weigh(v, safe);
@@ -419,9 +417,11 @@ __global__ __launch_bounds__(256, kChunkPerCu<D>) void chunk_kernel(KvAttendArgs
   };
 
   if (t_first < t_end) {
-    put(stage_k, s_key[0]);
 #pragma unroll
-    for (int k = 0; k < kStage; ++k) s_value[1][256 * k + tid] = (u32x4){0, 0, 0, 0};  // no weights wait at first
+    for (int k = 0; k < kStage; ++k) {
+      s_key[0][256 * k + tid] = stage_k[k];
+      s_value[1][256 * k + tid] = (u32x4){0, 0, 0, 0};  // no weights wait at first
+    }
     fetch(stage_k, min(t_first + 1, t_end - 1), 0);
     fetch(stage_v, t_first, 1);
     __syncthreads();
@@ -430,14 +430,20 @@ __global__ __launch_bounds__(256, kChunkPerCu<D>) void chunk_kernel(KvAttendArgs
     for (int t = t_first; t < t_end; ++t) {
       const int b = (t - t_first) & 1;
       const TileInfo info_next = find(min(t + 1, t_end - 1));
-      half_step(std::integral_constant<int, 0>(), t, info, s_key[b], s_value[b ^ 1]);
-      // The buffers written now were last read in the half step before the previous barrier.
-      put(stage_k, s_key[b ^ 1]);
-      put(stage_v, s_value[b]);
+      // The next tile's keys and this one's values go from registers to LDS, and those that follow them are
+      // asked for, one piece at a time beside the products (all at once between the half steps:
+      // 657 -> 613 us for 2048 tokens over 18432 keys, 32 heads of 128; 65.3 -> 57.2 for 777 over 6000, 8 of 256).  The buffers written were last read before the previous
+      // barrier.
+      const u32x4* src_k = source(min(t + 2, t_end - 1), 0);
+      const u32x4* src_v = source(min(t + 1, t_end - 1), 1);
+      half_step(std::integral_constant<int, 0>(), t, info, s_key[b], s_value[b ^ 1], [&](int k) {
+        u32x4& piece = k < kStage ? stage_k[k] : stage_v[k - kStage];
+        u32x4* dst = k < kStage ? s_key[b ^ 1] + 256 * k : s_value[b] + 256 * (k - kStage);
+        dst[tid] = piece;
+        piece = k < kStage ? src_k[256 * k] : src_v[256 * (k - kStage)];
+      });
       __syncthreads();
-      fetch(stage_k, min(t + 2, t_end - 1), 0);
-      fetch(stage_v, min(t + 1, t_end - 1), 1);
-      half_step(std::integral_constant<int, 1>(), t, info, s_key[b ^ 1], s_value[b]);
+      half_step(std::integral_constant<int, 1>(), t, info, s_key[b ^ 1], s_value[b], [](int) {});
       info = info_next;
     }
     add_values(1, s_value[(t_end - 1 - t_first) & 1]);
