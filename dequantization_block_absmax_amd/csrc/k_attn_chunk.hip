@@ -243,7 +243,12 @@ __global__ __launch_bounds__(256, kChunkPerCu<D>) void chunk_kernel(KvAttendArgs
     i.keys = src[2] | (uint64_t)src[3] << 32;
     return i;
   };
-  if (t_first < t_end) fetch(stage_k, t_first, 0);
+  TileInfo info = {0, 0, 0};
+  if (t_first < t_end) {  // on their way while the queries are set up
+    fetch(stage_k, t_first, 0);
+    fetch(stage_v, t_first, 1);
+    info = find(t_first);
+  }
 
   // Queries as operands: binary16 relative to a power of two of the row, the scale's sign included.
   const int r = block * kChunkRows + wave * 32 + n;
@@ -268,20 +273,26 @@ __global__ __launch_bounds__(256, kChunkPerCu<D>) void chunk_kernel(KvAttendArgs
     top = max(top, (uint32_t)__shfl_xor((int)top, 32));
     if (top >= (bf16 ? 0x7f80u : 0x7c00u)) top = 0;
     const float tf = bf16 ? bits_f32(top << 16) : (float)__builtin_bit_cast(_Float16, (uint16_t)top);
-    const int ex = tf > 0.0f ? __builtin_amdgcn_frexp_expf(tf) : 0;  // |q| < 2^ex
-    const float sign = aa.scale < 0.0f ? -1.0f : 1.0f;
+    const int ex = tf > 0.0f ? max(__builtin_amdgcn_frexp_expf(tf), -126) : 0;  // |q| < 2^ex
+    const float unit = __builtin_ldexpf(aa.scale < 0.0f ? -1.0f : 1.0f, -ex);
+    if (bf16) {
 #pragma unroll
-    for (int s = 0; s < kSteps; ++s) {
-      u32x4 o;
+      for (int s = 0; s < kSteps; ++s)
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const uint32_t x = w[s][k];
-        const f16x2 h = __builtin_bit_cast(f16x2, x);
-        const float x0 = bf16 ? bits_f32(x << 16) : (float)h.x, x1 = bf16 ? bits_f32(x & 0xffff0000u) : (float)h.y;
-        o[k] = pack_f16(__builtin_ldexpf(x0, -ex) * sign, __builtin_ldexpf(x1, -ex) * sign);
-      }
-      q[s] = __builtin_bit_cast(f16x8, o);
+        for (int k = 0; k < 4; ++k)
+          w[s][k] = pack_f16(bits_f32(w[s][k] << 16) * unit, bits_f32(w[s][k] & 0xffff0000u) * unit);
+    } else {
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t x = w[s][k];
+          const f16x2 h = __builtin_bit_cast(f16x2, x);
+          w[s][k] = pack_f16((float)h.x * unit, (float)h.y * unit);
+        }
     }
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) q[s] = __builtin_bit_cast(f16x8, w[s]);
     scale = __builtin_ldexpf(fabsf(aa.scale) * 1.44269504088896341f, ex);
   }
 
@@ -423,10 +434,8 @@ __global__ __launch_bounds__(256, kChunkPerCu<D>) void chunk_kernel(KvAttendArgs
       s_value[1][256 * k + tid] = (u32x4){0, 0, 0, 0};  // no weights wait at first
     }
     fetch(stage_k, min(t_first + 1, t_end - 1), 0);
-    fetch(stage_v, t_first, 1);
     __syncthreads();
     sc[0] = multiply_keys(0, s_key[0]);
-    TileInfo info = find(t_first);
     for (int t = t_first; t < t_end; ++t) {
       const int b = (t - t_first) & 1;
       const TileInfo info_next = find(min(t + 1, t_end - 1));
