@@ -483,7 +483,7 @@ size_t bq_kv_attention_workspace_bytes(const bq_kv_cache* cache, const bq_kv_bat
   bq::KvAttendArgs a;
   if (check_attention_shape(cache, batch, dtype, heads, &t.data, &a) != BQ_OK) return 0;
   if (a.tokens == 0 || a.num_seqs == 0 || a.max_q_len == 0) return 0;
-  return bq::kv_attend_workspace(a, t.data.K);
+  return bq::kv_attend_workspace(a, dtype);
 }
 
 bq_status bq_kv_attention(const bq_kv_cache* cache, const bq_kv_batch* batch, bq_dtype dtype, const void* q,
@@ -506,7 +506,7 @@ bq_status bq_kv_attention(const bq_kv_cache* cache, const bq_kv_batch* batch, bq
   if (pt != BQ_OK || !aligned(q, 16) || !aligned(out, 16) || q_stride % 8 != 0 || out_stride % 8 != 0 ||
       !aligned(batch->q_start, 4) || !aligned(batch->kv_len, 4) || !aligned(batch->page_table, 4) || !aligned(lse, 4))
     return BQ_ERR_ALIGNMENT;
-  const size_t need = bq::kv_attend_workspace(a, t.data.K);
+  const size_t need = bq::kv_attend_workspace(a, dtype);
   if (need > 0) {
     if (workspace == nullptr || workspace_bytes < need) return BQ_ERR_WORKSPACE;
     if (!aligned(workspace, 256)) return BQ_ERR_ALIGNMENT;

@@ -1,4 +1,4 @@
-// bq_attn.h -- device helpers shared by the attention kernels (k_attn.hip, k_attn_merge.hip).
+// bq_attn.h -- device helpers shared by the attention kernels (k_attn.hip, k_attn_chunk.hip, k_attn_merge.hip).
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -96,16 +96,21 @@ __device__ __forceinline__ int end_key(const KvAttendArgs& aa, const Sequence& s
 }
 
 // Partial results of a row over one split of its keys, relative to the reference exponent m:
-// sum of weights l and the weighted sum of values (head_dim binary32), kept in the workspace.
+// sum of weights l and the weighted sum of values (head_dim binary32), kept in the workspace.  l is the
+// sum that belongs to the weighted one, of weights as they were rounded; `exact`, for lse, that of the
+// unrounded ones.
 struct Partial {
-  float m, l;
+  float m, l, exact;
 };
 
 constexpr int kMaxSplits = 64;
 
 // Which sequences a launch takes.  A call whose sequences may bring many rows to a key/value head goes
 // through two sets of kernels: those of k_attn_chunk.hip for sequences with more than kFewRows rows (any, if
-// it is the only one), and the splitting kernel of k_attn.hip for the others.
+// it is the only one), and the splitting kernel of k_attn.hip for the others.  Its grid has room for kFewRows rows of
+// every sequence, so more of them cost calls in which most bring one (48 single tokens beside 200 of one
+// prompt, 32 heads over 8 of 128: 139 us, 180 with 64 rows, 265 with 128) and gain little elsewhere (the ragged
+// batch of 9: 69, 71, 73).
 enum Rows : int { kAllRows = 0, kFewOnly = 1, kManyRows = 2 };
 constexpr int kFewRows = 32;
 

@@ -193,7 +193,7 @@ struct KvAttendArgs {
   void* workspace;
 };
 // Bytes of workspace the launch needs (no device is touched beyond its CU count).
-size_t kv_attend_workspace(const KvAttendArgs& a, int table_size);
+size_t kv_attend_workspace(const KvAttendArgs& a, int dtype);
 int launch_kv_attend(const KvAttendArgs& a, int dtype, const DequantArgs& da, void* stream);
 // Joins the partial results of splits of the keys (k_attn_merge.hip): [0] those of sequences with few
 // rows, [1] with many; nsplit <= 1: nothing to join.  Not both: every sequence is of `kind`.

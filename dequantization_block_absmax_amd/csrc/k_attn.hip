@@ -12,14 +12,16 @@
 // so no cached value is formed: a code byte indexes a table in LDS that holds its two binary16
 // entries side by side.  Rounded to 16 bits are: c (2^-12 relative), the weights p a' (2^-12 relative
 // to the largest of their row), q' where it falls 2^-14 below its row's largest element, and the
-// result.  e_i is the exponent of the row's largest |q|.  Weights are kept in range by the reference
+// result.  With q in binary16, whose result keeps three more bits than a bfloat16's, c enters in two parts and
+// the weights, where registers allow, too (Operand).  e_i is the exponent of the row's largest |q|.  Weights are kept in range by the reference
 //   M_i = max_j (log2-domain s_ij + E_j),   E_j the exponent of token j's largest value maximum,
 // in place of the plain running maximum: the weights p a' = 2^(s - M) a' then stay below 2^14 whatever
 // the size of the values, and sum and weighted sum carry the same factor, which cancels.
 //
 // Decomposition.  Work is split over (16 RT rows: new token x query head of one key/value head) x
-// (key/value head) x (sequence) x (splits of the keys).  A workgroup's four waves take groups of 32
-// keys in turn, each on its own, and join their sums through LDS at the end; with more than one split
+// (key/value head) x (sequence) x (splits of the keys).  A workgroup's eight waves (four for 256-wide heads in
+// blocks of 32, whose block maxima fill the registers) take groups of 32 keys in turn, each on its own, and
+// join their sums through LDS at the end; with more than one split
 // the partial sums go to the workspace and k_attn_merge.hip joins them.  For one group of 32 keys, with
 // lane l = 16 g + m:
 //   scores  S^T = K Q^T: A = K, lane (m, g) decodes 8 codes of key m per step of 32 d; the result's lane
@@ -30,8 +32,21 @@
 //           neither operand passes through LDS.
 // With several blocks to a head (NB > 1) an A tile must hold d's of one block only; lanes exchange
 // halves of their bytes (spread) so that each holds some d's of every block.
+//
+// What bounds it.  For single tokens and drafts the bytes of codes and maxima; beside them the lookups (a permute and an
+// LDS read per code byte and use) and the exchange keep the vector units and LDS about as busy, so that the
+// kernels take 1.1 to 1.3 times what loads alone take with the same schedule.  On MI355X, median of a call's kernels:
+//   64 sequences of up to 8192 keys, 32 heads over 8 of 128, 4-bit, B = 64, bf16: 91 us, 4.1 TB/s (loads alone 71)
+//   3 of up to 131072 keys, 16 over 2 of 128, 8-bit, B = 128, f16: 39 us + join 4.7,  4.7 TB/s (loads alone 31)
+//   24 x 6 tokens, window 4000, 20 over 5 of 64, 8-bit, B = 32, f16: 26 us + join 5,  2.3 TB/s (loads alone 23.5)
+//   1 of 1000 keys, 32 over 8 of 128, 4-bit, B = 64, bf16: 7.5 us + join 3.3: the chain of loads from the arguments to
+//   the sequence, its pages and its keys, each about 1 us, and two launches
+// Eight waves of a workgroup share one table in LDS (four: 114 us in the first case, 43 in the second; sixteen: 98
+// and 43).  Workgroups that each take an equal share of all keys, whatever the sequence, gained nothing (84 us
+// against 83, and a longer join) over the splits below.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "bq_attn.h"
@@ -705,7 +720,7 @@ __global__ __launch_bounds__((64 * Occupancy<D, NB, RT>::kWaves), (Occupancy<D, 
 #pragma unroll
   for (int t = 0; t < RT; ++t) {
     sum[t] = rows_sum(sum[t]);
-    if (g == 0) s_part[wave][t * 16 + m] = {ref[t], sum[t]};
+    if (g == 0) s_part[wave][t * 16 + m] = {ref[t], sum[t], sum[t]};
   }
   __syncthreads();  // also: every lookup is done, the table's memory is free
   float* s_sum = reinterpret_cast<float*>(s_mem);
@@ -751,7 +766,7 @@ __global__ __launch_bounds__((64 * Occupancy<D, NB, RT>::kWaves), (Occupancy<D, 
       } else {
         const int64_t part = (token * aa.heads + head) * nsplit + split;
         *reinterpret_cast<f32x4*>(partial + part * D + d) = o;
-        if (d == 0) reinterpret_cast<Partial*>(partial + aa.tokens * aa.heads * nsplit * D)[part] = {m_all, l_all};
+        if (d == 0) reinterpret_cast<Partial*>(partial + aa.tokens * aa.heads * nsplit * D)[part] = {m_all, l_all, l_all};
       }
     }
     if (t + 1 < RT) __syncthreads();
@@ -791,13 +806,21 @@ static int64_t choose_splits(int64_t base, int64_t slots, int64_t keys, int num_
   return n < 1 ? 1 : n;
 }
 
-static Plan make_plan(const KvAttendArgs& a) {
+// Rows of a key/value head (new tokens x its query heads) up to which the splitting kernel alone is the
+// faster way, codes decoded anew for every 32 rows against an expanded copy written and read (us, 8 sequences of
+// 8192 keys, 4 heads, this kernel / the expanding ones):
+//   bf16, 128 wide, 4-bit: 256 rows 75 / 88, 384 119 / 108; 64 wide: 256 50 / 63, 384 73 / 71
+//   f16 (entries in two parts), 128 wide, 4-bit: 128 60 / 77, 256 103 / 90, one sequence of 16000 keys 36 / 36
+//   256 wide (16 rows to a workgroup), 8-bit: 64 96 / 159, 128 174 / 147, one sequence of 16000 keys 43 / 54
+static int64_t most_few_rows(int64_t head_dim, int dtype) { return head_dim == 256 ? 128 : dtype == F16 ? 256 : 384; }
+
+static Plan make_plan(const KvAttendArgs& a, int dtype) {
   Plan p = {};
   const int64_t group = a.heads / a.cache.kv_heads, D = a.cache.head_dim, cus = cu_count();
   int64_t rows = a.max_q_len * group;
   const int64_t ntiles = ((int64_t)a.max_kv_len + 63) / 64;
   const int64_t per_tile = (int64_t)a.cache.kv_heads * a.num_seqs * 64 * D * 4;  // at most 2^52
-  p.many = rows > 2 * kFewRows && ntiles > 0 && ntiles <= kMaxExpanded / per_tile;
+  p.many = rows > most_few_rows(D, dtype) && ntiles > 0 && ntiles <= kMaxExpanded / per_tile;
   const int64_t expanded = p.many ? ntiles * per_tile : 0;
   p.few = !p.many || a.num_seqs > 1;
   if (p.many) {
@@ -820,7 +843,7 @@ static Plan make_plan(const KvAttendArgs& a) {
     }
     c.info_at = (size_t)expanded;
     c.partial_at = (c.info_at + (size_t)(ntiles * a.cache.kv_heads * a.num_seqs) * 16 + 255) & ~(size_t)255;
-    c.end = c.partial_at + (c.nsplit > 1 ? (size_t)a.tokens * a.heads * c.nsplit * (D + 2) * 4 : 0);
+    c.end = c.partial_at + (c.nsplit > 1 ? (size_t)a.tokens * a.heads * c.nsplit * (D + 3) * 4 : 0);
     p.partial_at = (c.end + 255) & ~(size_t)255;
     rows = kFewRows;  // the splitting kernel's sequences
   }
@@ -828,7 +851,9 @@ static Plan make_plan(const KvAttendArgs& a) {
   if (!p.few) return p;
   p.rt = rows > 16 && D <= 128 ? 2 : 1;
   p.tiles = (int)((rows + 16 * p.rt - 1) / (16 * p.rt));
-  const int64_t base = (int64_t)p.tiles * a.cache.kv_heads * a.num_seqs;
+  // tiles with rows in them: sequences may bring fewer tokens than the longest
+  const int64_t rows_all = a.tokens * group / (16 * p.rt) + a.num_seqs;
+  const int64_t base = a.cache.kv_heads * std::min((int64_t)p.tiles * a.num_seqs, rows_all);
   const int nb = a.cache.head_dim >> a.cache.log2b;
   const int64_t slots = cus * (D == 256 || nb == 4 || (p.rt == 2 && D == 128) ? 1 : 2);
   // the workspace is asked for without a window, and holds for any
@@ -838,11 +863,11 @@ static Plan make_plan(const KvAttendArgs& a) {
     n = k < n ? k : n;
   }
   p.nsplit = (int)n;
-  if (n > 1) p.bytes += (size_t)a.tokens * a.heads * n * (D + 2) * 4;
+  if (n > 1) p.bytes += (size_t)a.tokens * a.heads * n * (D + 3) * 4;
   return p;
 }
 
-size_t kv_attend_workspace(const KvAttendArgs& a, int) { return make_plan(a).bytes; }
+size_t kv_attend_workspace(const KvAttendArgs& a, int dtype) { return make_plan(a, dtype).bytes; }
 
 namespace {
 
@@ -884,7 +909,7 @@ hipError_t launch_few(const KvAttendArgs& a, const Plan& p, int dtype, const Deq
 }  // namespace
 
 int launch_kv_attend(const KvAttendArgs& a, int dtype, const DequantArgs& da, void* stream) {
-  const Plan p = make_plan(a);
+  const Plan p = make_plan(a, dtype);
   // workgroups along x (the launch itself counts threads), grid rows
   if ((p.few && (int64_t)p.tiles * p.nsplit > INT32_MAX) || a.cache.kv_heads > 32767 ||
       (p.many && (int64_t)a.cache.kv_heads * p.chunk.nsplit * p.chunk.blocks > INT32_MAX)) {

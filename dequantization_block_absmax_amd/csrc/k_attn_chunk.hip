@@ -19,6 +19,18 @@
 //                  8 (v / 4) + 4 g + v % 4 of each 32 (element v)
 //   O^T = V'^T P^T B = P^T: 8 keys per lane and step, taken in just that order, so the weights stay where
 //                  they were computed; V' is stored with its keys in the same order.
+//
+// Why once rounded.  A cached value is rounded to binary16 here as bq_kv_read in that type gives it: with q and
+// out in binary16 the result is within 4 parts in 2^12 of the exact sums.  Two parts of each operand, as in k_attn.hip,
+// would double the products and the LDS that bound this kernel.
+//
+// What bounds it.  Each product of a wave reads 1 KB of LDS per 32 cycles, and four such waves are all
+// that LDS delivers: matrix cores and LDS have the same least time, and neither is reached while the exponentials and
+// the barrier stand between.  On MI355X (the largest library product of this type: 1189 TFLOP/s):
+//   2048 tokens over 18432 keys, 32 heads over 8 of 128, bf16: 613-650 us (900-950 TFLOP/s), expansion 23 us
+//   777 over 6000, 8 heads over 1 of 256, bf16: 56 us (640 TFLOP/s, 245 workgroups: about 13 us are start and end of
+//   a workgroup, not its tiles), expansion 6, join 7.6
+//   9 sequences of up to 700 over up to 5000, 16 over 4 of 64, f16: 39 us (510 TFLOP/s), expansion 10
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
@@ -192,7 +204,7 @@ __global__ __launch_bounds__(256) void expand_kernel(KvAttendArgs aa, DequantArg
 template <int D>
 constexpr int kChunkPerCu = D == 64 ? 3 : D == 128 ? 2 : 1;
 
-template <int D>
+template <int D, bool LSE>
 __global__ __launch_bounds__(256, kChunkPerCu<D>) void chunk_kernel(KvAttendArgs aa, int ntiles, const u32x4* tiles,
                                                                     const TileInfo* infos, int nblocks, int nsplit,
                                                                     float* partial, int bf16) {
@@ -296,7 +308,7 @@ __global__ __launch_bounds__(256, kChunkPerCu<D>) void chunk_kernel(KvAttendArgs
     scale = __builtin_ldexpf(fabsf(aa.scale) * 1.44269504088896341f, ex);
   }
 
-  float ref = -INFINITY, sum = 0.0f;
+  float ref = -INFINITY, sum = 0.0f, exact = 0.0f;
   f32x16 acc[kBlocks];
 #pragma unroll
   for (int i = 0; i < kBlocks; ++i)
@@ -355,17 +367,19 @@ __global__ __launch_bounds__(256, kChunkPerCu<D>) void chunk_kernel(KvAttendArgs
     }
     // at least 2^-126: a hidden key's -infinity stays what it is
     const float f = fmaxf(__builtin_ldexpf(scale, ek - kTopBit), 0x1p-126f);
-    const float sum_before = sum;
+    const float sum_before = sum, exact_before = exact;
     float top = -INFINITY, p = 0.0f;
     u32x4 x[2];
     // Weights of scores v .. v + 1 relative to the reference, and their sum.  The sum takes the weights as
-    // rounded: a row that one key fills gives that key's value.
+    // rounded: a row that one key fills gives that key's value.  Where lse is asked for, `exact` takes them
+    // unrounded: the rounded ones would move it by up to 2^-12.
     auto weigh = [&](int v, float safe) {
       const float e = exp2_hw(fmaf(s[v], f, -safe));
       if (v & 1) {
         uint32_t pair = pack_f16(p, e);
         asm volatile("" : "+v"(pair));  // here, beside the products, and not on the side of the branch below
         sum = __builtin_amdgcn_fdot2(__builtin_bit_cast(f16x2, pair), (f16x2){(_Float16)1.0f, (_Float16)1.0f}, sum, false);
+        if constexpr (LSE) exact += p + e;
         x[v >> 3][(v & 7) >> 1] = pair;
       } else {
         p = e;
@@ -402,6 +416,7 @@ __global__ __launch_bounds__(256, kChunkPerCu<D>) void chunk_kernel(KvAttendArgs
       const float down = ref == -INFINITY ? 0.0f : exp2_hw(ref - up);
       ref = up;
       sum = sum_before * down;
+      if constexpr (LSE) exact = exact_before * down;
       const float units = ev > e_all ? __builtin_ldexpf(down, max(e_all - ev, -1000)) : down;
       e_all = max(ev, e_all);
 #pragma unroll
@@ -440,9 +455,9 @@ __global__ __launch_bounds__(256, kChunkPerCu<D>) void chunk_kernel(KvAttendArgs
       const int b = (t - t_first) & 1;
       const TileInfo info_next = find(min(t + 1, t_end - 1));
       // The next tile's keys and this one's values go from registers to LDS, and those that follow them are
-      // asked for, one piece at a time beside the products (all at once between the half steps:
-      // 657 -> 613 us for 2048 tokens over 18432 keys, 32 heads of 128; 65.3 -> 57.2 for 777 over 6000, 8 of 256).  The buffers written were last read before the previous
-      // barrier.
+      // asked for, one piece at a time beside the products (613 us for 2048 tokens over 18432 keys, 32 heads of
+      // 128, and 57.2 for 777 over 6000, 8 of 256; all at once between the half steps 657 and 65.3).  The buffers
+      // written were last read before the previous barrier.
       const u32x4* src_k = source(min(t + 2, t_end - 1), 0);
       const u32x4* src_v = source(min(t + 1, t_end - 1), 1);
       half_step(std::integral_constant<int, 0>(), t, info, s_key[b], s_value[b ^ 1], [&](int k) {
@@ -458,9 +473,13 @@ __global__ __launch_bounds__(256, kChunkPerCu<D>) void chunk_kernel(KvAttendArgs
     add_values(1, s_value[(t_end - 1 - t_first) & 1]);
   }
 
-  const float unit = e_all > -1000 ? __builtin_ldexpf(1.0f, e_all - kTopBit) : 0.0f;
   const u32x2 o2 = __builtin_amdgcn_permlane32_swap(f32_bits(sum), f32_bits(sum), false, false);
+  const float unit = e_all > -1000 ? __builtin_ldexpf(1.0f, e_all - kTopBit) : 0.0f;
   const float l = bits_f32(o2.x) + bits_f32(o2.y);
+  if constexpr (LSE) {
+    const u32x2 o3 = __builtin_amdgcn_permlane32_swap(f32_bits(exact), f32_bits(exact), false, false);
+    exact = bits_f32(o3.x) + bits_f32(o3.y);
+  }
   if (!live) return;
   const int64_t part = (token * aa.heads + head) * nsplit + split;
   const float inv = nsplit > 1 ? unit : (l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l)) * unit;
@@ -478,8 +497,8 @@ __global__ __launch_bounds__(256, kChunkPerCu<D>) void chunk_kernel(KvAttendArgs
       }
     }
   if (g == 0) {
-    if (nsplit > 1) reinterpret_cast<Partial*>(partial + aa.tokens * aa.heads * nsplit * D)[part] = {ref, l};
-    else if (aa.lse != nullptr) aa.lse[token * aa.heads + head] = log_sum(ref, l);
+    if (nsplit > 1) reinterpret_cast<Partial*>(partial + aa.tokens * aa.heads * nsplit * D)[part] = {ref, l, exact};
+    else if constexpr (LSE) aa.lse[token * aa.heads + head] = log_sum(ref, exact);
   }
 }
 
@@ -493,7 +512,8 @@ hipError_t launch_chunk(const KvAttendArgs& a, const ChunkPlan& p, int bf16, con
                             : launch_kernel(expand_kernel<D, 8>, grid, dim3(256), s, a, da, p.ntiles, tiles, infos);
   if (e != hipSuccess) return e;
   const dim3 grid2((unsigned)(a.cache.kv_heads * p.nsplit * p.blocks), 1u, (unsigned)a.num_seqs);
-  return launch_kernel(chunk_kernel<D>, grid2, dim3(256), s, a, p.ntiles, tiles, infos, p.blocks, p.nsplit, partial, bf16);
+  return launch_kernel(a.lse != nullptr ? chunk_kernel<D, true> : chunk_kernel<D, false>, grid2, dim3(256), s, a, p.ntiles, tiles,
+                       infos, p.blocks, p.nsplit, partial, bf16);
 }
 
 }  // namespace

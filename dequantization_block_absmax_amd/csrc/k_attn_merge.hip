@@ -5,8 +5,9 @@
 //
 // Few splits (up to 16): D / 4 lanes take a row, 4 / (D / 64) rows to a wave.  More: four waves take a row, wave
 // w its splits w, w + 4, ..., lane by lane over head_dim, eight loads in flight (64 splits of one row
-// one after another took 20 us, 4.5 us so).  Bound by latency: a call's partial sums are a small part of its
-// cache.
+// one after another took 20 us, 4.5 us so).  Bound by latency where few rows were split (3 to
+// 5 us); by the partial sums' bytes where many were: 6216 rows of 256 over 5 splits (32 MB, written and read once) take
+// 7.6 us here, 4.2 TB/s, and about 6 us of the kernel before.
 #include <hip/hip_runtime.h>
 
 #include "bq_attn.h"
@@ -88,7 +89,7 @@ __global__ __launch_bounds__(64 * kWaves) void merge_few_kernel(KvAttendArgs aa,
   float top = -INFINITY;
 #pragma unroll 4
   for (int s = 0; s < src.nsplit; ++s) top = fmaxf(top, src.parts[s].m);
-  float l = 0.0f;
+  float l = 0.0f, exact = 0.0f;
   f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 4
   for (int s = 0; s < src.nsplit; ++s) {
@@ -96,6 +97,7 @@ __global__ __launch_bounds__(64 * kWaves) void merge_few_kernel(KvAttendArgs aa,
     const f32x4 x = *reinterpret_cast<const f32x4*>(src.sums + (int64_t)s * D + d);
     const float f = p.m == -INFINITY ? 0.0f : exp2_hw(p.m - top);
     l = fmaf(f, p.l, l);
+    exact = fmaf(f, p.exact, exact);
 #pragma unroll
     for (int k = 0; k < 4; ++k) v[k] = fmaf(f, x[k], v[k]);
   }
@@ -103,7 +105,7 @@ __global__ __launch_bounds__(64 * kWaves) void merge_few_kernel(KvAttendArgs aa,
   const int64_t head = at - mine * aa.heads;
   const u32x2 o = {pack16(v[0] * inv, v[1] * inv, bf16), pack16(v[2] * inv, v[3] * inv, bf16)};
   *reinterpret_cast<u32x2*>(static_cast<char*>(aa.out) + (mine * aa.out_stride + head * D + d) * 2) = o;
-  if (aa.lse != nullptr && d == 0) aa.lse[at] = log_sum(top, l);
+  if (aa.lse != nullptr && d == 0) aa.lse[at] = log_sum(top, exact);
 }
 
 template <int D>
@@ -118,14 +120,17 @@ __global__ __launch_bounds__(64 * kWaves) void merge_kernel(KvAttendArgs aa, Mer
   tokens_beside(aa, token, lane, nq);
   const Source src = source<D>(aa, ma, at, nq[0]);
   if (src.nsplit == 0) return;
-  const Partial mine = lane < src.nsplit ? src.parts[lane] : Partial{-INFINITY, 0.0f};
+  const Partial mine = lane < src.nsplit ? src.parts[lane] : Partial{-INFINITY, 0.0f, 0.0f};
   float top = mine.m;
 #pragma unroll
   for (int x = 1; x < 64; x <<= 1) top = fmaxf(top, __shfl_xor(top, x));
   const float f = mine.m == -INFINITY ? 0.0f : exp2_hw(mine.m - top);
-  float l = f * mine.l;
+  float l = f * mine.l, exact = f * mine.exact;
 #pragma unroll
-  for (int x = 1; x < 64; x <<= 1) l += __shfl_xor(l, x);
+  for (int x = 1; x < 64; x <<= 1) {
+    l += __shfl_xor(l, x);
+    exact += __shfl_xor(exact, x);
+  }
   float v[kPer];
 #pragma unroll
   for (int k = 0; k < kPer; ++k) v[k] = 0.0f;
@@ -165,7 +170,7 @@ __global__ __launch_bounds__(64 * kWaves) void merge_kernel(KvAttendArgs aa, Mer
 #pragma unroll
     for (int k = 0; k < kPer; k += 2) reinterpret_cast<uint32_t*>(out)[k / 2] = pack16(v[k] * inv, v[k + 1] * inv, bf16);
   }
-  if (aa.lse != nullptr && lane == 0) aa.lse[at] = log_sum(top, l);
+  if (aa.lse != nullptr && lane == 0) aa.lse[at] = log_sum(top, exact);
 }
 
 template <int D>

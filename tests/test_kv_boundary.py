@@ -148,4 +148,4 @@ def test_attention_sizes_beyond_int32():
     c = cache(kv_heads=1 << 19, num_pages=1, page_size=16, head_dim=128, blocksize=128)
     b = batch(num_seqs=65535, tokens=2047, max_q_len=2047, max_kv_len=1 << 30, table_stride=1 << 26)
     need = bq.bq_kv_attention_workspace_bytes(c, b, bq.BQ_BF16, 1 << 20)
-    assert need <= (2047 << 20) * 64 * (128 + 2) * 4 + 256
+    assert need <= (2047 << 20) * 64 * (128 + 3) * 4 + 256
