@@ -27,7 +27,7 @@
 // What bounds it.  Each product of a wave reads 1 KB of LDS per 32 cycles, and four such waves are all
 // that LDS delivers: matrix cores and LDS have the same least time, and neither is reached while the exponentials and
 // the barrier stand between.  On MI355X (the largest library product of this type: 1189 TFLOP/s):
-//   2048 tokens over 18432 keys, 32 heads over 8 of 128, bf16: 613-650 us (900-950 TFLOP/s), expansion 23 us
+//   2048 tokens over 18432 keys, 32 heads over 8 of 128, bf16: 611-635 us (920-950 TFLOP/s), expansion 23 us
 //   777 over 6000, 8 heads over 1 of 256, bf16: 56 us (640 TFLOP/s, 245 workgroups: about 13 us are start and end of
 //   a workgroup, not its tiles), expansion 6, join 7.6
 //   9 sequences of up to 700 over up to 5000, 16 over 4 of 64, f16: 39 us (510 TFLOP/s), expansion 10
