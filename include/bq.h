@@ -392,7 +392,8 @@ size_t bq_kv_attention_workspace_bytes(const bq_kv_cache* cache, const bq_kv_bat
  *   lse        [device] out, or NULL: tokens x heads binary32, the natural logarithm of
  *              sum_j exp(scale * (q_i . k_j)).
  *   workspace  [device] bq_kv_attention_workspace_bytes bytes, 256-byte aligned (NULL if that is 0).
- * Products are summed in binary32; see k_attn.hip for what is rounded to 16 bits on the way.
+ * Products are summed in binary32; k_attn.hip (few rows) and k_attn_chunk.hip (many) say what is rounded
+ * to 16 bits on the way.
  * Results are the same on every call on one device.  Block maxima of keys that are seen must be
  * finite and at most 2^100.
  * Errors: BQ_ERR_DTYPE; BQ_ERR_SIZE (a negative count or length, num_seqs > 65535, heads, tokens * heads
