@@ -794,7 +794,7 @@ constexpr int64_t kMaxExpanded = (int64_t)4 << 30;
 // 89.3, 4 splits 92.5).  With several sequences, whose lengths may differ, a workgroup takes 8192 keys at most.
 static int64_t choose_splits(int64_t base, int64_t slots, int64_t keys, int num_seqs) {
   const int64_t steps = (keys + 255) / 256;
-  const int64_t least = num_seqs > 1 ? (steps + 31) / 32 : 1;
+  const int64_t least = num_seqs > 1 ? std::max((steps + 31) / 32, (int64_t)1) : 1;  // one without any keys
   int64_t best = INT64_MAX, n = 1;
   for (int64_t k = least < kMaxSplits ? least : kMaxSplits; k <= kMaxSplits && (k <= steps || k <= 1); ++k) {
     const int64_t cost = (base * k + slots - 1) / slots * ((steps + k - 1) / k + 3);
@@ -803,7 +803,7 @@ static int64_t choose_splits(int64_t base, int64_t slots, int64_t keys, int num_
       n = k;
     }
   }
-  return n < 1 ? 1 : n;
+  return n;
 }
 
 // Rows of a key/value head (new tokens x its query heads) up to which the splitting kernel alone is the

@@ -1,0 +1,34 @@
+"""bq_kv_attention where a batch has next to nothing in it: no keys, no tokens, rows of no sequence."""
+import numpy as np
+import pytest
+import torch
+
+import dequantization_block_absmax_amd as bq
+import synth
+from kv_helpers import Batch, Pool, queries, run_attention
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def dev():
+    assert torch.cuda.is_available(), "GPU tests need a ROCm device"
+    return torch.device("cuda:0")
+
+
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
+@pytest.mark.parametrize("lens", [[(1, 0)], [(1, 0), (1, 0), (3, 0)], [(600, 0), (0, 0), (2, 0)]],
+                         ids=["one", "few", "many"])
+@pytest.mark.parametrize("by", ["length", "table"])
+def test_no_sequence_has_a_key(dev, lens, dtype, by):
+    """Zeros, and -infinity in lse, for every row."""
+    rng = np.random.default_rng(1)
+    pool = Pool(dev, synth.table16(), 2, 16, 2, 64, 64)
+    batch = Batch(dev, pool, lens, rng)
+    if by == "table":  # room for keys, but no table to find them by
+        batch.dev[1].fill_(40)
+        batch.batch = bq.kv_batch(*batch.dev, batch.tokens, batch.max_q, 40, table_stride=0)
+    q = queries(dev, rng, batch.tokens, 4, 64, dtype)
+    out, lse = run_attention(dev, pool, batch, q, dtype, 0.125)
+    torch.cuda.synchronize()
+    assert bool((out == 0).all()) and bool(torch.isneginf(lse).all())
