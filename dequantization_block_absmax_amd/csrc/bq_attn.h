@@ -74,13 +74,16 @@ struct Sequence {
   int kv;      // keys
 };
 
+// An entry of q_start as a row that q and out have, or their end (the difference of two is then in range too).
+__device__ __forceinline__ int row_number(const KvAttendArgs& aa, int row) {
+  return max((int)min((int64_t)row, aa.tokens), 0);
+}
+
 __device__ __forceinline__ Sequence sequence(const KvAttendArgs& aa, int seq) {
   Sequence s;
-  const int first = max(__builtin_amdgcn_readfirstlane(aa.q_start[seq]), 0);
-  const int last = (int)min((int64_t)__builtin_amdgcn_readfirstlane(aa.q_start[seq + 1]), aa.tokens);
-  s.q0 = first;
+  s.q0 = row_number(aa, __builtin_amdgcn_readfirstlane(aa.q_start[seq]));
   // positions count all new tokens; rows past max_q_len are left out by the grid
-  s.nq = max(last - first, 0);
+  s.nq = max(row_number(aa, __builtin_amdgcn_readfirstlane(aa.q_start[seq + 1])) - s.q0, 0);
   s.kv = max(min(__builtin_amdgcn_readfirstlane(aa.kv_len[seq]), aa.max_kv_len), 0);
   return s;
 }

@@ -27,9 +27,8 @@ __device__ __forceinline__ void tokens_beside(const KvAttendArgs& aa, const int6
   for (int k = 0; k < N; ++k) count[k] = 0;
   for (int s0 = 0; s0 < aa.num_seqs; s0 += 64) {
     const int s = min(s0 + lane, aa.num_seqs - 1);
-    const int first = max(aa.q_start[s], 0);
-    const int last = (int)min((int64_t)aa.q_start[s + 1], aa.tokens);
-    const int nq = min(last - first, aa.max_q_len);
+    const int first = row_number(aa, aa.q_start[s]);
+    const int nq = min(row_number(aa, aa.q_start[s + 1]) - first, aa.max_q_len);
     bool all = true;
 #pragma unroll
     for (int k = 0; k < N; ++k) {

@@ -32,3 +32,23 @@ def test_no_sequence_has_a_key(dev, lens, dtype, by):
     out, lse = run_attention(dev, pool, batch, q, dtype, 0.125)
     torch.cuda.synchronize()
     assert bool((out == 0).all()) and bool(torch.isneginf(lse).all())
+
+
+@pytest.mark.parametrize("lens", [[(2, 40), (3, 30), (1, 20)], [(500, 600), (3, 30), (1, 20)]], ids=["few", "many"])
+def test_row_numbers_out_of_range(dev, lens):
+    """Entries of q_start below zero count as zero and those past the last row as its end, however far
+    out: what lies between two of them is never taken for rows."""
+    rng = np.random.default_rng(2)
+    pool = Pool(dev, synth.table16(), 60, 16, 2, 64, 64)
+    pool.fill(rng)
+    batch = Batch(dev, pool, lens, rng)
+    q = queries(dev, rng, batch.tokens, 4, 64, "bfloat16")
+    want, want_lse = run_attention(dev, pool, batch, q, "bfloat16", 0.125)
+    n = lens[0][0]
+    for starts, kept in (([-2 ** 31, n, -2 ** 31, -2 ** 31], n), ([-7, n, -2 ** 31, -1], n), ([0, n, -5, -9], n),
+                         ([0, n, n + 3, 2 ** 31 - 1], n + 4), ([2 ** 31 - 1, -2 ** 31, -2 ** 31 + 1, -1], 0)):
+        batch.dev[0].copy_(torch.tensor(starts, dtype=torch.int32))
+        out, lse = run_attention(dev, pool, batch, q, "bfloat16", 0.125)
+        torch.cuda.synchronize()
+        assert torch.equal(out[:kept], want[:kept]) and torch.equal(lse[:kept], want_lse[:kept]), starts
+        assert bool((out[kept:] == 77.0).all()) and bool((lse[kept:] == 77.0).all()), starts
