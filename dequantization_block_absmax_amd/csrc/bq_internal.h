@@ -207,8 +207,9 @@ int launch_kv_merge(const KvAttendArgs& a, int dtype, const MergeArgs& m, void* 
 // its parts of the workspace begin (bytes).
 struct ChunkPlan {
   int ntiles, blocks, nsplit;
-  size_t info_at, partial_at, end;
+  size_t info_at, exponents_at, partial_at, end;
 };
+constexpr int kTileInfoBytes = 16;
 constexpr int kChunkRows = 128;
 int chunk_slots(int head_dim);  // workgroups of that kernel the device holds at once
 int launch_kv_chunk(const KvAttendArgs& a, int dtype, const ChunkPlan& p, const DequantArgs& da, void* stream);

@@ -842,7 +842,9 @@ static Plan make_plan(const KvAttendArgs& a, int dtype) {
       }
     }
     c.info_at = (size_t)expanded;
-    c.partial_at = (c.info_at + (size_t)(ntiles * a.cache.kv_heads * a.num_seqs) * 16 + 255) & ~(size_t)255;
+    const size_t tiles = (size_t)(ntiles * a.cache.kv_heads * a.num_seqs);
+    c.exponents_at = c.info_at + tiles * kTileInfoBytes;
+    c.partial_at = (c.exponents_at + tiles * 2 * 64 + 255) & ~(size_t)255;
     c.end = c.partial_at + (c.nsplit > 1 ? (size_t)a.tokens * a.heads * c.nsplit * (D + 3) * 4 : 0);
     p.partial_at = (c.end + 255) & ~(size_t)255;
     rows = kFewRows;  // the splitting kernel's sequences

@@ -5,12 +5,16 @@
 // many rows are first expanded once into the workspace (expand_kernel), as binary16 in the order in which
 // the matrix cores take them, and chunk_kernel multiplies from there:
 //   K' = RN16(fl32(c a) 2^(14-ek)), V' = RN16(fl32(c a) 2^(14-ev)), per tile of 64 keys of a head
-// with 2^ek, 2^ev powers of two at least as large as the tile's largest maximum: every cached value
-// keeps 11 bits, whatever the type of q and the size of the values (down to 2^-28 of the power of two).
-// ek joins the scale of the scores.  ev is a multiple of 8, so that one sequence's tiles nearly always
-// share it; sums are kept relative to the largest ev so far (E), and for a tile with a smaller one the
-// weights are scaled by 2^(ev - E) before the product (what that rounds away is below 2^-25 of the
-// largest values).
+// with 2^ek, 2^ev powers of two above the tile's largest maximum.  Where the keys of a tile are of very different
+// size (kKeySpread, kValueSpread) each key has powers of its own, so that every cached value keeps 11 bits,
+// whatever the type of q and the size of the values beside it (down to 2^-16 of the largest of its key).  ek joins
+// the scale of the scores.  ev joins the softmax: weights are taken relative to
+//   M_i = max_j (log2-domain s_ij + ev_j)   as   w_ij = 2^(s_ij + ev_j - M_i + 3),
+// so that w V' has the same unit, 2^(M - 17), in every tile, and a weight is rounded relative to the largest
+// weight times value of its row and not to the largest weight.  The denominator is sum_j w_ij 2^-ev_j.
+// Exponents of their own, and denominators of unrounded weights, cost where they occur: 2048 tokens over 18432 keys
+// take 622 us as a rule, 898 where every tile's values are apart, 736 where the first tile's values are 2^9
+// times the others' and matter to the rows.
 //
 // chunk_kernel: a workgroup of four waves takes 128 rows (new token x query head of one key/value
 // head) and walks the tiles of 64 keys with the running maximum and sum of the softmax.  A wave takes
@@ -45,12 +49,21 @@ namespace {
 constexpr int kTile = 64;   // keys
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef short s16x2 __attribute__((ext_vector_type(2)));
 
-// What a tile's expansion leaves beside its values: exponents, and which of its keys some row sees.
+// What a tile's expansion leaves beside its values: exponents, whether its keys have exponents of their own (in
+// an array of bytes, keys then values, tile after tile), and which of its keys some row sees.
 struct TileInfo {
-  int32_t ek, ev;
+  int16_t ek, k_apart, ev, v_apart;
   uint64_t keys;
 };
+
+// Exponents of a tile's keys may differ by this much before each has its own.  A value 2^n below its tile's
+// power of two has 11 bits while n <= 28, so keys have room to spare; a weight is rounded relative to the
+// tile's largest value, 2^n too coarsely.
+constexpr int kKeySpread = 12, kValueSpread = 4;
+// Least exponents; a tile's zeros have it.  Sums of 2^30 weights 2^(s - M + 3) <= 2^(15 - ev) stay in range.
+constexpr int kLeastKey = -100, kLeastValue = -80;
 
 // ---- expansion ----------------------------------------------------------------------------
 //
@@ -59,11 +72,11 @@ struct TileInfo {
 //   V' piece ((db * 4 + ks) * 64 + 32 g + n):   d = 32 db + n, keys 16 ks + 8 (e / 4) + 4 g + e % 4, e = 0 .. 7
 template <int D, int KB>
 __global__ __launch_bounds__(256) void expand_kernel(KvAttendArgs aa, DequantArgs da, int ntiles, u32x4* tiles,
-                                                     TileInfo* infos) {
+                                                     TileInfo* infos, int8_t* exponents) {
   __shared__ float s_c[256];
   __shared__ float s_a[kTile * 8];       // block maxima of the tile's keys or values; zero (theirs may be NaN) where no row sees the key
   __shared__ int64_t s_row[kTile];       // pool row of each key
-  __shared__ uint32_t s_top[4];
+  __shared__ float s_factor[kTile];      // 2^(14 - exponent) of each key, where they are apart
   __shared__ uint32_t s_listed[2];
   __shared__ u32x4 s_out[kTile * D / 8]; // values' pieces, in their order
   const int tid = threadIdx.x, lane = tid & 63;
@@ -127,28 +140,39 @@ __global__ __launch_bounds__(256) void expand_kernel(KvAttendArgs aa, DequantArg
         value_code[k][e] = KB == 4 ? *reinterpret_cast<const uint16_t*>(src) : *reinterpret_cast<const uint32_t*>(src);
       }
   }
-  uint32_t top = 0;
   for (int e = tid; e < kTile << log2nb; e += 256) {
     const int64_t row = s_row[e >> log2nb];
-    const float a = row >= 0 ? aa.cache.absmax[side][(row << log2nb) + (e & (nb - 1))] : 0.0f;
-    s_a[e] = a;
-    top = max(top, f32_bits(a) & 0x7fffffffu);
+    s_a[e] = row >= 0 ? aa.cache.absmax[side][(row << log2nb) + (e & (nb - 1))] : 0.0f;
   }
-#pragma unroll
-  for (int x = 1; x < 64; x <<= 1) top = max(top, (uint32_t)__shfl_xor((int)top, x));
-  if (lane == 0) s_top[wave] = top;
   __syncthreads();
-  // exponent: |a| < 2^e (zeros: the least); the values' is a multiple of 8
-  top = max(max(s_top[0], s_top[1]), max(s_top[2], s_top[3]));
-  const int least = min(max((int)(top >> 23) - 126, -100), 120);
-  const int ex = side == 0 ? least : (least + 127) / 8 * 8 - 120;
+  // Exponents, |a| < 2^e: lane l of every wave takes key l.  Keys that no row sees have no say, nor do zero
+  // keys, whose scores are zero at any scale (zero values have: their weights count).
+  uint32_t top = 0;
+  for (int b = 0; b < nb; ++b) top = max(top, f32_bits(s_a[(lane << log2nb) + b]) & 0x7fffffffu);
+  const int least = side == 0 ? kLeastKey : kLeastValue;
+  int own = min(max((int)(top >> 23) - 126, least), 120);
+  const bool counts = s_row[lane] >= 0 && (side == 1 || top != 0);
+  s16x2 ends = counts ? (s16x2){(short)own, (short)-own} : (s16x2){-128, -128};
+#pragma unroll
+  for (int x = 1; x < 64; x <<= 1)
+    ends = __builtin_elementwise_max(ends, __builtin_bit_cast(s16x2, __shfl_xor(__builtin_bit_cast(int, ends), x)));
+  const int ex = __builtin_amdgcn_readfirstlane(max((int)ends.x, least));
+  // the same in every wave; false if no key counts
+  const bool apart = __builtin_amdgcn_readfirstlane(ends.x + ends.y > (side == 0 ? kKeySpread : kValueSpread));
   const float f = __builtin_ldexpf(1.0f, kTopBit - ex);
   const int64_t at = ((int64_t)seq * aa.cache.kv_heads + kvh) * ntiles + tile;
+  if (!apart || !counts) own = ex;
+  if (wave == 0) exponents[(2 * at + side) * kTile + lane] = (int8_t)own;
   if (tid == 0) {
-    if (side == 0) infos[at].ek = ex;
-    else infos[at].ev = ex;
+    if (side == 0) infos[at].ek = (int16_t)ex, infos[at].k_apart = apart;
+    else infos[at].ev = (int16_t)ex, infos[at].v_apart = apart;
     if (side == 0) infos[at].keys = s_listed[0] | (uint64_t)s_listed[1] << 32;
   }
+  if (apart) {
+    if (wave == 0) s_factor[lane] = __builtin_ldexpf(1.0f, kTopBit - own);
+    __syncthreads();
+  }
+  auto factor = [&](int key) { return apart ? s_factor[key] : f; };
   u32x4* const out = tiles + at * (2 * kTile * D / 8) + side * (kTile * D / 8);
 
   if (side == 0) {
@@ -156,14 +180,14 @@ __global__ __launch_bounds__(256) void expand_kernel(KvAttendArgs aa, DequantArg
     for (int k = 0; k < kKeyUnits; ++k) {
       int key, d8;
       key_unit(256 * k + tid, key, d8);
-      const float a = s_a[(key << log2nb) + (d8 * 8 >> aa.cache.log2b)];
+      const float a = s_a[(key << log2nb) + (d8 * 8 >> aa.cache.log2b)], to = factor(key);
       const u32x2 c = key_code[k];
       u32x4 w;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const uint32_t q0 = KB == 4 ? (c.x >> (8 * i + 4)) & 15u : ((i < 2 ? c.x : c.y) >> (16 * (i & 1))) & 255u;
         const uint32_t q1 = KB == 4 ? (c.x >> (8 * i)) & 15u : ((i < 2 ? c.x : c.y) >> (16 * (i & 1) + 8)) & 255u;
-        w[i] = pack_f16((s_c[q0] * a) * f, (s_c[q1] * a) * f);
+        w[i] = pack_f16((s_c[q0] * a) * to, (s_c[q1] * a) * to);
       }
       out[256 * k + tid] = w;
     }
@@ -178,12 +202,12 @@ __global__ __launch_bounds__(256) void expand_kernel(KvAttendArgs aa, DequantArg
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       value_unit(p, e, key, d4);
-      const float a = s_a[(key << log2nb) + (d4 * 4 >> aa.cache.log2b)];
+      const float a = s_a[(key << log2nb) + (d4 * 4 >> aa.cache.log2b)], to = factor(key);
       const uint32_t c = value_code[k][e];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const uint32_t q = KB == 4 ? (c >> (8 * (i >> 1) + ((i & 1) ? 0 : 4))) & 15u : (c >> (8 * i)) & 255u;
-        v[e][i] = (s_c[q] * a) * f;
+        v[e][i] = (s_c[q] * a) * to;
       }
     }
     const int d = d4 * 4, oct = p / (D / 4);
@@ -204,10 +228,14 @@ __global__ __launch_bounds__(256) void expand_kernel(KvAttendArgs aa, DequantArg
 template <int D>
 constexpr int kChunkPerCu = D == 64 ? 3 : D == 128 ? 2 : 1;
 
+// Weights begin at 2^kHead and grow to 2^(kHead + kSlack), the last power of two below binary16's largest: as far
+// above its least step, 2^-24, as they can be.
+constexpr float kHead = 3.0f;
+
 template <int D, bool LSE>
 __global__ __launch_bounds__(256, kChunkPerCu<D>) void chunk_kernel(KvAttendArgs aa, int ntiles, const u32x4* tiles,
-                                                                    const TileInfo* infos, int nblocks, int nsplit,
-                                                                    float* partial, int bf16) {
+                                                                    const TileInfo* infos, const int8_t* exponents,
+                                                                    int nblocks, int nsplit, float* partial, int bf16) {
   constexpr int kSteps = D / 16, kBlocks = D / 32;
   constexpr int kPieces = kTile * D / 8;          // of keys, and of values, in a tile
   constexpr int kStage = kPieces / 256;           // pieces of each that a thread stages
@@ -247,15 +275,16 @@ __global__ __launch_bounds__(256, kChunkPerCu<D>) void chunk_kernel(KvAttendArgs
   };
   // a tile ahead and by scalar loads: waiting for them does not wait for the tiles on their way
   typedef const __attribute__((address_space(4))) uint32_t* ScalarWords;
+  struct Info {
+    int ek, ev;
+    bool apart;
+    uint64_t keys;
+  };
   auto find = [&](int t) {
     const ScalarWords src = (ScalarWords)(uintptr_t)(infos + head_at + t);
-    TileInfo i;
-    i.ek = (int32_t)src[0];
-    i.ev = (int32_t)src[1];
-    i.keys = src[2] | (uint64_t)src[3] << 32;
-    return i;
+    return Info{(int16_t)src[0], (int16_t)src[1], (src[0] | src[1]) >> 16 != 0, src[2] | (uint64_t)src[3] << 32};
   };
-  TileInfo info = {0, 0, 0};
+  Info info = {0, 0, false, 0};
   if (t_first < t_end) {  // on their way while the queries are set up
     fetch(stage_k, t_first, 0);
     fetch(stage_v, t_first, 1);
@@ -308,13 +337,13 @@ __global__ __launch_bounds__(256, kChunkPerCu<D>) void chunk_kernel(KvAttendArgs
     scale = __builtin_ldexpf(fabsf(aa.scale) * 1.44269504088896341f, ex);
   }
 
+  // M of the row; sums of its weights as rounded and unrounded (this lane's keys, in units of 2^(M - 3))
   float ref = -INFINITY, sum = 0.0f, exact = 0.0f;
   f32x16 acc[kBlocks];
 #pragma unroll
   for (int i = 0; i < kBlocks; ++i)
 #pragma unroll
     for (int v = 0; v < 16; ++v) acc[i][v] = 0.0f;
-  int e_all = -1000;  // exponent of the sums
 
   // Half steps of 32 keys, so that each has independent work for the matrix cores and the vector units:
   // while half h's weights are computed from its scores, the scores of half h + 1 and the sums with
@@ -341,9 +370,9 @@ __global__ __launch_bounds__(256, kChunkPerCu<D>) void chunk_kernel(KvAttendArgs
   };
   // The half step of half `half` of tile t: next = the tile (and half) whose scores follow, prev = the
   // tile whose values the other half's weights belong to; beside every second product, move(k) passes a piece on.
-  auto half_step = [&](auto half_c, int t, const TileInfo& info, const u32x4* next, const u32x4* prev, auto move) {
+  auto half_step = [&](auto half_c, int t, const Info& info, const u32x4* next, const u32x4* prev, auto move) {
     constexpr int half = half_c.value;
-    const int ek = info.ek, ev = info.ev;
+    const float ev = (float)info.ev;
     const int j0 = t * kTile + 32 * half;
     const uint32_t keys = half ? (uint32_t)(info.keys >> 32) : (uint32_t)info.keys;
     f32x16& s = sc[half];
@@ -357,6 +386,23 @@ __global__ __launch_bounds__(256, kChunkPerCu<D>) void chunk_kernel(KvAttendArgs
 #pragma unroll
     for (int z = 0; z < kAhead; ++z) a[z] = operand(z);
     __builtin_amdgcn_sched_barrier(0);
+    // at least 2^-100: a hidden key's -infinity stays what it is
+    const float f = fmaxf(__builtin_ldexpf(scale, info.ek - kTopBit), 0x1p-100f);
+    // the exponents of the lane's keys 8 i + 4 g .. + 3, a byte each, where they are apart (side 0: keys)
+    auto own = [&](int side, int i) {
+      return reinterpret_cast<const uint32_t*>(exponents)[(2 * (head_at + t) + side) * (kTile / 4) + 8 * half + 2 * i + g];
+    };
+    auto byte_of = [](uint32_t x, int e) { return (int)(int8_t)(x >> (8 * e)); };
+    if (info.apart) {  // rare: the scores to the tile's units, the values' exponents beside them
+      const float inv = 1.0f / f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t xk = own(0, i), xv = own(1, i);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          s[4 * i + e] = fmaf((float)(byte_of(xv, e) - info.ev), inv, __builtin_ldexpf(s[4 * i + e], byte_of(xk, e) - info.ek));
+      }
+    }
     if (!(j0 >= lo_all && j0 + 32 <= hi_all && keys == ~0u)) {  // some key hidden from some row
 #pragma unroll
       for (int v = 0; v < 16; ++v) {
@@ -365,27 +411,26 @@ __global__ __launch_bounds__(256, kChunkPerCu<D>) void chunk_kernel(KvAttendArgs
         s[v] = hide | (uint32_t)(j < lo) | (uint32_t)(j >= hi) ? -INFINITY : s[v];
       }
     }
-    // at least 2^-126: a hidden key's -infinity stays what it is
-    const float f = fmaxf(__builtin_ldexpf(scale, ek - kTopBit), 0x1p-126f);
-    const float sum_before = sum, exact_before = exact;
     float top = -INFINITY, p = 0.0f;
     u32x4 x[2];
-    // Weights of scores v .. v + 1 relative to the reference, and their sum.  The sum takes the weights as
-    // rounded: a row that one key fills gives that key's value.  Where lse is asked for, `exact` takes them
-    // unrounded: the rounded ones would move it by up to 2^-12.
-    auto weigh = [&](int v, float safe) {
-      const float e = exp2_hw(fmaf(s[v], f, -safe));
+    // Weights of scores v .. v + 1 as 2^(score f + c), and their sums in this half step.  `part` takes the weights
+    // as rounded: a row that one key fills gives that key's value.  Where lse is asked for, `whole` takes them
+    // unrounded: the rounded ones would move it by up to 2^-11.
+    float part = 0.0f, whole = 0.0f;
+    auto weigh = [&](int v, float c) {
+      const float e = exp2_hw(fmaf(s[v], f, c));
       if (v & 1) {
         uint32_t pair = pack_f16(p, e);
         asm volatile("" : "+v"(pair));  // here, beside the products, and not on the side of the branch below
-        sum = __builtin_amdgcn_fdot2(__builtin_bit_cast(f16x2, pair), (f16x2){(_Float16)1.0f, (_Float16)1.0f}, sum, false);
-        if constexpr (LSE) exact += p + e;
+        part = __builtin_amdgcn_fdot2(__builtin_bit_cast(f16x2, pair), (f16x2){(_Float16)1.0f, (_Float16)1.0f}, part, false);
+        if constexpr (LSE) whole += p + e;
         x[v >> 3][(v & 7) >> 1] = pair;
       } else {
         p = e;
       }
     };
-    const float safe = fmaxf(ref, -0x1p120f);
+    auto offset = [&]() { return (ev + kHead) - fmaxf(ref, -0x1p120f); };  // no key yet: -infinity stays
+    float c = offset();
     f32x16& z_next = sc[half ^ 1];
 #pragma unroll
     for (int v = 0; v < 16; ++v) z_next[v] = 0.0f;
@@ -402,43 +447,50 @@ __global__ __launch_bounds__(256, kChunkPerCu<D>) void chunk_kernel(KvAttendArgs
       if (z & 1) move(z >> 1);
 #pragma unroll
       for (int v = z * 16 / kMul; v < (z + 1) * 16 / kMul; ++v) {
-        weigh(v, safe);
+        weigh(v, c);
         if (v & 1) top = max3_hw(top, s[v - 1], s[v]);
       }
       __builtin_amdgcn_sched_barrier(0);
     }
-    top *= f;
-    if (ev > e_all || __any(top > ref + kSlack)) {
-      // Rare after the first tiles: larger units or a larger reference.  The sums so far move to them, and
-      // the weights are taken again.
+    top = fmaf(top, f, ev);
+    if (__any(top > ref + kSlack)) {
+      // Rare after the first tiles: a larger reference.  The sums so far move to it, and the weights are taken
+      // again.  It may rise by more than 2^126, from values of the least exponent to large ones: in two halves.
       const u32x2 o = __builtin_amdgcn_permlane32_swap(f32_bits(top), f32_bits(top), false, false);
       const float up = fmaxf(ref, fmaxf(bits_f32(o.x), bits_f32(o.y)));
-      const float down = ref == -INFINITY ? 0.0f : exp2_hw(ref - up);
+      const float down = ref == -INFINITY ? 0.0f : exp2_hw(0.5f * (ref - up));
       ref = up;
-      sum = sum_before * down;
-      if constexpr (LSE) exact = exact_before * down;
-      const float units = ev > e_all ? __builtin_ldexpf(down, max(e_all - ev, -1000)) : down;
-      e_all = max(ev, e_all);
+      sum = (sum * down) * down;
+      if constexpr (LSE) exact = (exact * down) * down;
 #pragma unroll
       for (int i = 0; i < kBlocks; ++i)
 #pragma unroll
-        for (int v = 0; v < 16; ++v) acc[i][v] *= units;
-      const float again = fmaxf(ref, -0x1p120f);
+        for (int v = 0; v < 16; ++v) acc[i][v] *= down * down;
+      part = whole = 0.0f;
+      c = offset();
 #pragma unroll
-      for (int v = 0; v < 16; ++v) weigh(v, again);
+      for (int v = 0; v < 16; ++v) weigh(v, c);
     }
     w[half][0] = x[0];
     w[half][1] = x[1];
-    if (ev < e_all) {  // uniform, rare: the tile's values are in smaller units, so its weights shrink
-      const _Float16 f1 = (_Float16)__builtin_ldexpf(1.0f, max(ev - e_all, -24));
-      const f16x2 f2 = {f1, f1};
+    // The denominator.  In units of 2^(M - 3 - ev) a rounded weight is off by up to 2^-25 at the least, which
+    // is nothing beside a sum of one.  Where the row's reference comes from values more than 2^3 times
+    // as large as this tile's, or the keys have exponents of their own, it takes weights that are not rounded.
+    const float with = sum + __builtin_ldexpf(part, -info.ev);
+    const u32x2 o = __builtin_amdgcn_permlane32_swap(f32_bits(with), f32_bits(with), false, false);
+    if (info.apart || __any(ref != -INFINITY && __builtin_ldexpf(bits_f32(o.x) + bits_f32(o.y), info.ev) < 1.0f)) {
+      float more = 0.0f;
 #pragma unroll
-      for (int ks = 0; ks < 2; ++ks)
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t xv = own(1, i);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint32_t x = w[half][ks][k];
-          w[half][ks][k] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, x) * f2);
-        }
+        for (int e = 0; e < 4; ++e) more += exp2_hw(fmaf(s[4 * i + e], f, c) - (float)byte_of(xv, e));
+      }
+      sum += more;
+      if constexpr (LSE) exact += more;
+    } else {
+      sum = with;
+      if constexpr (LSE) exact += __builtin_ldexpf(whole, -info.ev);
     }
   };
 
@@ -453,7 +505,7 @@ __global__ __launch_bounds__(256, kChunkPerCu<D>) void chunk_kernel(KvAttendArgs
     sc[0] = multiply_keys(0, s_key[0]);
     for (int t = t_first; t < t_end; ++t) {
       const int b = (t - t_first) & 1;
-      const TileInfo info_next = find(min(t + 1, t_end - 1));
+      const Info info_next = find(min(t + 1, t_end - 1));
       // The next tile's keys and this one's values go from registers to LDS, and those that follow them are
       // asked for, one piece at a time beside the products (613 us for 2048 tokens over 18432 keys, 32 heads of
       // 128, and 57.2 for 777 over 6000, 8 of 256; all at once between the half steps 657 and 65.3).  The buffers
@@ -474,7 +526,7 @@ __global__ __launch_bounds__(256, kChunkPerCu<D>) void chunk_kernel(KvAttendArgs
   }
 
   const u32x2 o2 = __builtin_amdgcn_permlane32_swap(f32_bits(sum), f32_bits(sum), false, false);
-  const float unit = e_all > -1000 ? __builtin_ldexpf(1.0f, e_all - kTopBit) : 0.0f;
+  const float unit = __builtin_ldexpf(1.0f, -kTopBit);  // of the sums beside those of the weights
   const float l = bits_f32(o2.x) + bits_f32(o2.y);
   if constexpr (LSE) {
     const u32x2 o3 = __builtin_amdgcn_permlane32_swap(f32_bits(exact), f32_bits(exact), false, false);
@@ -497,8 +549,8 @@ __global__ __launch_bounds__(256, kChunkPerCu<D>) void chunk_kernel(KvAttendArgs
       }
     }
   if (g == 0) {
-    if (nsplit > 1) reinterpret_cast<Partial*>(partial + aa.tokens * aa.heads * nsplit * D)[part] = {ref, l, exact};
-    else if constexpr (LSE) aa.lse[token * aa.heads + head] = log_sum(ref, exact);
+    if (nsplit > 1) reinterpret_cast<Partial*>(partial + aa.tokens * aa.heads * nsplit * D)[part] = {ref - kHead, l, exact};
+    else if constexpr (LSE) aa.lse[token * aa.heads + head] = log_sum(ref - kHead, exact);
   }
 }
 
@@ -506,14 +558,15 @@ template <int D>
 hipError_t launch_chunk(const KvAttendArgs& a, const ChunkPlan& p, int bf16, const DequantArgs& da, hipStream_t s) {
   u32x4* tiles = static_cast<u32x4*>(a.workspace);
   TileInfo* infos = reinterpret_cast<TileInfo*>(static_cast<char*>(a.workspace) + p.info_at);
+  int8_t* exponents = static_cast<int8_t*>(a.workspace) + p.exponents_at;
   float* partial = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + p.partial_at);
   const dim3 grid((unsigned)p.ntiles, (unsigned)a.cache.kv_heads * 2, (unsigned)a.num_seqs);
-  hipError_t e = da.K == 16 ? launch_kernel(expand_kernel<D, 4>, grid, dim3(256), s, a, da, p.ntiles, tiles, infos)
-                            : launch_kernel(expand_kernel<D, 8>, grid, dim3(256), s, a, da, p.ntiles, tiles, infos);
+  hipError_t e = da.K == 16 ? launch_kernel(expand_kernel<D, 4>, grid, dim3(256), s, a, da, p.ntiles, tiles, infos, exponents)
+                            : launch_kernel(expand_kernel<D, 8>, grid, dim3(256), s, a, da, p.ntiles, tiles, infos, exponents);
   if (e != hipSuccess) return e;
   const dim3 grid2((unsigned)(a.cache.kv_heads * p.nsplit * p.blocks), 1u, (unsigned)a.num_seqs);
   return launch_kernel(a.lse != nullptr ? chunk_kernel<D, true> : chunk_kernel<D, false>, grid2, dim3(256), s, a, p.ntiles, tiles,
-                       infos, p.blocks, p.nsplit, partial, bf16);
+                       infos, exponents, p.blocks, p.nsplit, partial, bf16);
 }
 
 }  // namespace
@@ -523,7 +576,7 @@ int chunk_slots(int head_dim) {
   return cu_count() * (head_dim == 64 ? kChunkPerCu<64> : head_dim == 128 ? kChunkPerCu<128> : kChunkPerCu<256>);
 }
 
-static_assert(sizeof(TileInfo) == 16, "workspace layout");
+static_assert(sizeof(TileInfo) == kTileInfoBytes && kTile == 64, "workspace layout");
 
 int launch_kv_chunk(const KvAttendArgs& a, int dtype, const ChunkPlan& p, const DequantArgs& da, void* stream) {
   hipStream_t s = static_cast<hipStream_t>(stream);
