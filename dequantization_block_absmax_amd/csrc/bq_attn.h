@@ -21,6 +21,15 @@ typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
 __device__ __forceinline__ float log2_hw(float x) { return __builtin_amdgcn_logf(x); }
 
+// A sum of weights relative to the reference `from`, relative to the larger one `to`.  In units of one reference the
+// weights of zero values may be 2^99 and those of the largest values 2^-101: the sums stay in range where
+// 2^(from - to), below 2^-126, does not, so it is taken in two halves.  No reference yet: the sum is zero, or
+// NaN from q.
+__device__ __forceinline__ float lower(float sum, float from, float to) {
+  const float h = exp2_hw(0.5f * (from - to));
+  return from == -INFINITY ? sum : (sum * h) * h;
+}
+
 // Maximum and sum over the four 16-lane rows of a wave (lanes l, l ^ 16, l ^ 32, l ^ 48), in every lane.
 __device__ __forceinline__ float rows_max(float v) {
   u32x2 s = __builtin_amdgcn_permlane32_swap(f32_bits(v), f32_bits(v), false, false);

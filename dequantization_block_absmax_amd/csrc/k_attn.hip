@@ -618,8 +618,8 @@ __global__ __launch_bounds__((64 * Occupancy<D, NB, RT>::kWaves), (Occupancy<D, 
       if (__any(top > ref[t] + kSlack)) {  // rare after the first groups: raise the reference
         const float up = fmaxf(ref[t], rows_max(top));
         const float f = ref[t] == -INFINITY ? 0.0f : exp2_hw(ref[t] - up);
+        sum[t] = lower(sum[t], ref[t], up);
         ref[t] = up;
-        sum[t] *= f;
 #pragma unroll
         for (int i = 0; i < S::kTiles; ++i)
 #pragma unroll
@@ -753,7 +753,7 @@ __global__ __launch_bounds__((64 * Occupancy<D, NB, RT>::kWaves), (Occupancy<D, 
 #pragma unroll
       for (int v = 0; v < W; ++v) {
         const Partial p = s_part[v][t * 16 + row];
-        l_all += p.m == -INFINITY ? p.l : p.l * exp2_hw(p.m - m_all);  // no reference: zero, or NaN from q
+        l_all += lower(p.l, p.m, m_all);
       }
       f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll

@@ -455,17 +455,17 @@ __global__ __launch_bounds__(256, kChunkPerCu<D>) void chunk_kernel(KvAttendArgs
     top = fmaf(top, f, ev);
     if (__any(top > ref + kSlack)) {
       // Rare after the first tiles: a larger reference.  The sums so far move to it, and the weights are taken
-      // again.  It may rise by more than 2^126, from values of the least exponent to large ones: in two halves.
+      // again.
       const u32x2 o = __builtin_amdgcn_permlane32_swap(f32_bits(top), f32_bits(top), false, false);
       const float up = fmaxf(ref, fmaxf(bits_f32(o.x), bits_f32(o.y)));
-      const float down = ref == -INFINITY ? 0.0f : exp2_hw(0.5f * (ref - up));
+      const float down = ref == -INFINITY ? 0.0f : exp2_hw(ref - up);
+      sum = lower(sum, ref, up);
+      if constexpr (LSE) exact = lower(exact, ref, up);
       ref = up;
-      sum = (sum * down) * down;
-      if constexpr (LSE) exact = (exact * down) * down;
 #pragma unroll
       for (int i = 0; i < kBlocks; ++i)
 #pragma unroll
-        for (int v = 0; v < 16; ++v) acc[i][v] *= down * down;
+        for (int v = 0; v < 16; ++v) acc[i][v] *= down;
       part = whole = 0.0f;
       c = offset();
 #pragma unroll

@@ -95,8 +95,8 @@ __global__ __launch_bounds__(64 * kWaves) void merge_few_kernel(KvAttendArgs aa,
     const Partial p = src.parts[s];
     const f32x4 x = *reinterpret_cast<const f32x4*>(src.sums + (int64_t)s * D + d);
     const float f = p.m == -INFINITY ? 0.0f : exp2_hw(p.m - top);
-    l = fmaf(f, p.l, l);
-    exact = fmaf(f, p.exact, exact);
+    l += lower(p.l, p.m, top);
+    exact += lower(p.exact, p.m, top);
 #pragma unroll
     for (int k = 0; k < 4; ++k) v[k] = fmaf(f, x[k], v[k]);
   }
@@ -124,7 +124,7 @@ __global__ __launch_bounds__(64 * kWaves) void merge_kernel(KvAttendArgs aa, Mer
 #pragma unroll
   for (int x = 1; x < 64; x <<= 1) top = fmaxf(top, __shfl_xor(top, x));
   const float f = mine.m == -INFINITY ? 0.0f : exp2_hw(mine.m - top);
-  float l = f * mine.l, exact = f * mine.exact;
+  float l = lower(mine.l, mine.m, top), exact = lower(mine.exact, mine.m, top);
 #pragma unroll
   for (int x = 1; x < 64; x <<= 1) {
     l += __shfl_xor(l, x);

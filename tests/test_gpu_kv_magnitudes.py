@@ -182,6 +182,17 @@ def sink(gain, k):
     return plan
 
 
+def zeros_beside(k, first):
+    """Half of the keys hold zeros and weigh e^6 times as much as the other half, whose values are 2^k: they
+    count in the denominator only."""
+    def plan(rng, n):
+        t, x = mild(rng, n), np.full(n, float(k))
+        at = np.arange(n) < n // 2 if first else np.arange(n) >= n // 2
+        t[at], x[at] = t[at] + 6.0, -np.inf
+        return t, x
+    return plan
+
+
 def key_spikes(k):
     """Single keys of 2^k, whose scores are far below all others."""
     def plan(rng, n):
@@ -197,6 +208,9 @@ PLANS = {
     "first tile 16": (700, first_tile(16)), "first tile 24": (700, first_tile(24)),
     "first tile 40": (700, first_tile(40)), "up": (700, steps(True, 0.0)), "down": (700, steps(False, 0.0)),
     "up, level": (700, steps(True, np.log(2.0))), "down, level": (700, steps(False, np.log(2.0))),
+    "zeros, then 20": (700, zeros_beside(20, True)), "zeros, then 60": (700, zeros_beside(60, True)),
+    "zeros, then 99": (700, zeros_beside(99, True)), "60, then zeros": (700, zeros_beside(60, False)),
+    "99, then zeros": (5000, zeros_beside(99, False)), "zeros, then 99, long": (5000, zeros_beside(99, True)),
     "key spikes 12": (700, key_spikes(12)),
     "key spikes 24": (700, key_spikes(24)), "key spikes 40": (700, key_spikes(40)),
 }
