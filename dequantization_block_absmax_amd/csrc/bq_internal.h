@@ -203,6 +203,7 @@ struct MergeArgs {
   int both, kind;
 };
 int launch_kv_merge(const KvAttendArgs& a, int dtype, const MergeArgs& m, void* stream);
+bool kv_merge_fits(const KvAttendArgs& a);  // the rows' launch counts its threads in 32 bits
 // How k_attn_chunk.hip goes about a call: expanded tiles of keys, rows per workgroup, splits, and where
 // its parts of the workspace begin (bytes).
 struct ChunkPlan {

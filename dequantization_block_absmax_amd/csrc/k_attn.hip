@@ -912,9 +912,12 @@ hipError_t launch_few(const KvAttendArgs& a, const Plan& p, int dtype, const Deq
 
 int launch_kv_attend(const KvAttendArgs& a, int dtype, const DequantArgs& da, void* stream) {
   const Plan p = make_plan(a, dtype);
-  // workgroups along x (the launch itself counts threads), grid rows
-  if ((p.few && (int64_t)p.tiles * p.nsplit > INT32_MAX) || a.cache.kv_heads > 32767 ||
-      (p.many && (int64_t)a.cache.kv_heads * p.chunk.nsplit * p.chunk.blocks > INT32_MAX)) {
+  // Every launch fits before the first is enqueued: threads along x in 32 bits, grid rows in 16.
+  const bool join = (p.few && p.nsplit > 1) || (p.many && p.chunk.nsplit > 1);
+  const int few_threads = 64 * (a.cache.head_dim == 256 && a.cache.log2b == 5 ? Occupancy<256, 8, 1>::kWaves : 8);
+  if ((p.few && (int64_t)p.tiles * p.nsplit * few_threads > UINT32_MAX) || a.cache.kv_heads > 32767 ||
+      (p.many && (int64_t)a.cache.kv_heads * p.chunk.nsplit * p.chunk.blocks > UINT32_MAX / 256) ||
+      (p.many && p.chunk.ntiles > (int64_t)UINT32_MAX / 256) || (join && !kv_merge_fits(a))) {
     g_launch_refused_for_size = true;
     return (int)hipErrorInvalidConfiguration;
   }
@@ -925,7 +928,7 @@ int launch_kv_attend(const KvAttendArgs& a, int dtype, const DequantArgs& da, vo
                        p.many};
   int e = p.many ? launch_kv_chunk(a, dtype, p.chunk, da, stream) : 0;
   if (e == 0 && p.few) e = (int)launch_few(a, p, dtype, da, static_cast<hipStream_t>(stream));
-  if (e != 0 || (m.nsplit[0] <= 1 && m.nsplit[1] <= 1)) return e;
+  if (e != 0 || !join) return e;
   return launch_kv_merge(a, dtype, m, stream);
 }
 

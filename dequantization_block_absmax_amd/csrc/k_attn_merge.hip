@@ -172,16 +172,26 @@ __global__ __launch_bounds__(64 * kWaves) void merge_kernel(KvAttendArgs aa, Mer
   if (aa.lse != nullptr && lane == 0) aa.lse[at] = log_sum(top, exact);
 }
 
+// A launch counts threads in 32 bits.
+constexpr int64_t kMostWorkgroups = (int64_t)UINT32_MAX / (64 * kWaves);
+
+// Workgroups of merge_few_kernel.
+int64_t few_workgroups(const KvAttendArgs& a) {
+  const int64_t per = kWaves * (64 / (a.cache.head_dim / 4));
+  return (a.tokens * a.heads + per - 1) / per;
+}
+
 template <int D>
 hipError_t launch_dim(const KvAttendArgs& a, const MergeArgs& m, int bf16, hipStream_t s) {
   const int64_t rows = a.tokens * a.heads;
-  if ((m.nsplit[0] > 16 || m.nsplit[1] > 16) && rows <= 1 << 24)  // a launch counts threads in 32 bits
+  if ((m.nsplit[0] > 16 || m.nsplit[1] > 16) && rows <= kMostWorkgroups)
     return launch_kernel(merge_kernel<D>, dim3((unsigned)rows), dim3(64 * kWaves), s, a, m, bf16);
-  const int64_t per = kWaves * (64 / (D / 4));
-  return launch_kernel(merge_few_kernel<D>, dim3((unsigned)((rows + per - 1) / per)), dim3(64 * kWaves), s, a, m, bf16);
+  return launch_kernel(merge_few_kernel<D>, dim3((unsigned)few_workgroups(a)), dim3(64 * kWaves), s, a, m, bf16);
 }
 
 }  // namespace
+
+bool kv_merge_fits(const KvAttendArgs& a) { return few_workgroups(a) <= kMostWorkgroups; }
 
 int launch_kv_merge(const KvAttendArgs& a, int dtype, const MergeArgs& m, void* stream) {
   hipStream_t s = static_cast<hipStream_t>(stream);

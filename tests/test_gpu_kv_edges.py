@@ -52,3 +52,39 @@ def test_row_numbers_out_of_range(dev, lens):
         torch.cuda.synchronize()
         assert torch.equal(out[:kept], want[:kept]) and torch.equal(lse[:kept], want_lse[:kept]), starts
         assert bool((out[kept:] == 77.0).all()) and bool((lse[kept:] == 77.0).all()), starts
+
+
+@pytest.mark.parametrize("tokens", [4095, 4096])
+def test_many_splits_of_two_to_the_24_rows(dev, tokens):
+    """4096 tokens of 4096 heads, all but two of them in no sequence, over room for more than 16 splits: the
+    joining kernel for many splits ends one row short of this."""
+    heads, kv_heads, dim, page = 4096, 64, 64, 16
+    rng = np.random.default_rng(3)
+    pool = Pool(dev, synth.table16(), 12, page, kv_heads, dim, 64)
+    pool.fill(rng)
+    small = Batch(dev, pool, [(1, 70), (1, 55)], rng)
+    q = queries(dev, rng, 2, heads, dim, "bfloat16")
+    want, want_lse = run_attention(dev, pool, small, q, "bfloat16", 0.125)
+
+    wide = torch.full((2, 17 * 8192 // page), -1, dtype=torch.int32, device=dev)
+    wide[:, :small.dev[2].shape[1]] = small.dev[2]
+    b = bq.kv_batch(small.dev[0], small.dev[1], wide, tokens, 1, 17 * 8192)
+    size = bq.bq_kv_attention_workspace_bytes(pool.cache, b, bq.BQ_BF16, heads)
+    assert size >= 17 * tokens * heads * (dim + 3) * 4
+    if torch.cuda.mem_get_info()[0] < size + (8 << 30):
+        pytest.skip("not enough memory free")
+    ws = torch.empty(size, dtype=torch.uint8, device=dev)
+    long_q = torch.zeros(tokens, heads, dim, dtype=torch.bfloat16, device=dev)
+    long_q[:2] = q
+    out = torch.full((tokens, heads, dim), 7.0, dtype=torch.bfloat16, device=dev)
+    lse = torch.full((tokens, heads), 7.0, device=dev)
+    bq.check(bq.bq_kv_attention(pool.cache, b, bq.BQ_BF16, long_q, heads * dim, heads, 0.125, 1, 0, out, heads * dim,
+                                lse, ws, size), "attention")
+    torch.cuda.synchronize()
+    assert bool((out[2:] == 7.0).all()) and bool((lse[2:] == 7.0).all())
+    # other splits of the same keys: both within one rounding of the weights (2^-11 of sum p |v|) and of the result
+    most = float(np.nanmax(np.abs(pool.values(1))))
+    assert bool(((out[:2].float() - want.float()).abs() <= 2 * (2.0 ** -8 * want.float().abs() + 2.0 ** -11 * most)).all())
+    assert bool(((lse[:2] - want_lse).abs() <= 2.0 ** -19 * (1 + want_lse.abs())).all())
+    del ws
+    torch.cuda.empty_cache()

@@ -3,7 +3,7 @@ before any HIP call."""
 import pytest
 
 import dequantization_block_absmax_amd as bq
-from test_kv_boundary import batch, cache
+from test_kv_boundary import attend, batch, cache
 
 
 @pytest.mark.parametrize("kw", [dict(max_kv_len=0), dict(table_stride=0), dict(max_kv_len=0, max_q_len=3),
@@ -13,3 +13,14 @@ from test_kv_boundary import batch, cache
 def test_a_batch_without_keys_is_planned(kw, heads):
     """A call whose sequences have no key is planned like another: nothing to split or to join."""
     assert bq.bq_kv_attention_workspace_bytes(cache(), batch(**kw), bq.BQ_BF16, heads) == 0
+
+
+@pytest.mark.parametrize("dim,over", [(256, 1 << 26), (128, 1 << 27), (64, 1 << 28)])
+def test_a_join_that_is_too_large_is_refused_before_any_work(dim, over):
+    """Splits of the keys are joined by a launch of their own, 256 threads for 1024 / dim rows; where that counts
+    more than 2^32 - 1 threads nothing at all is enqueued."""
+    c = cache(head_dim=dim, blocksize=64, kv_heads=64)
+    b = batch(num_seqs=2, tokens=over // 4096 + 1, max_q_len=1, max_kv_len=20000, table_stride=2000)
+    assert bq.bq_kv_attention_workspace_bytes(c, b, bq.BQ_BF16, 4096) > 2 * over * dim * 4
+    row = 4096 * dim
+    assert attend(c, b, heads=4096, q_stride=row, out_stride=row) == bq.BQ_ERR_SIZE
