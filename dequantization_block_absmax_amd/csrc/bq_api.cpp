@@ -16,6 +16,7 @@
 #include "bq.h"
 #include "bq_debug.h"
 #include "bq_internal.h"
+#include "bq_kv.h"
 
 namespace {
 

@@ -3,7 +3,7 @@
 
 #include <hip/hip_runtime.h>
 
-#include "bq_internal.h"
+#include "bq_kv.h"
 
 namespace bq {
 

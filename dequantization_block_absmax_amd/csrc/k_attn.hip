@@ -50,7 +50,7 @@
 #include <type_traits>
 
 #include "bq_attn.h"
-#include "bq_internal.h"
+#include "bq_kv.h"
 #include "bq_launch.h"
 
 namespace bq {

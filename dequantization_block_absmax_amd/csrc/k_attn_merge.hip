@@ -11,7 +11,7 @@
 #include <hip/hip_runtime.h>
 
 #include "bq_attn.h"
-#include "bq_internal.h"
+#include "bq_kv.h"
 #include "bq_launch.h"
 
 namespace bq {

@@ -20,7 +20,7 @@
 #include <hip/hip_runtime.h>
 
 #include "bq_device.h"
-#include "bq_internal.h"
+#include "bq_kv.h"
 #include "bq_launch.h"
 
 namespace bq {
