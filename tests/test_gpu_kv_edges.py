@@ -1,11 +1,12 @@
-"""bq_kv_attention where a batch has next to nothing in it: no keys, no tokens, rows of no sequence."""
+"""bq_kv_attention at the edges of its arguments: no keys, rows of no sequence, row numbers out of range, scales of
+either sign and zero, the largest joins."""
 import numpy as np
 import pytest
 import torch
 
 import dequantization_block_absmax_amd as bq
 import synth
-from kv_helpers import Batch, Pool, queries, run_attention
+from kv_helpers import Batch, Pool, check_attention, hide_unused, queries, run_attention
 
 pytestmark = pytest.mark.gpu
 
@@ -88,3 +89,22 @@ def test_many_splits_of_two_to_the_24_rows(dev, tokens):
     assert bool(((lse[:2] - want_lse).abs() <= 2.0 ** -19 * (1 + want_lse.abs())).all())
     del ws
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
+@pytest.mark.parametrize("scale", [-0.09, 0.0, -0.0, 1e-40, -1e-30])
+@pytest.mark.parametrize("lens", [[(1, 5), (1, 300), (2, 130)], [(40, 300)], [(50, 60), (200, 450), (3, 3)]],
+                         ids=["few", "many", "chunk"])
+@pytest.mark.parametrize("causal,window", [(1, 0), (1, 40), (0, 0)])
+def test_scales_of_either_sign_and_zero(dev, causal, window, lens, scale, dtype):
+    """A negative scale turns the order of the keys round; with zero every key that a row sees weighs the same, and
+    the hidden ones nothing."""
+    rng = np.random.default_rng(4)
+    pool = Pool(dev, synth.table256(), sum(-(-kv // 16) for _, kv in lens) + 2, 16, 2, 128, 64)
+    pool.fill(rng)
+    batch = Batch(dev, pool, lens, rng)
+    hide_unused(pool, batch)
+    batch.table[0, 0] = -1  # a page that is not there
+    batch.dev[2].copy_(torch.from_numpy(batch.table))
+    q = queries(dev, rng, batch.tokens, 6, 128, dtype)
+    check_attention(dev, pool, batch, q, dtype, scale, causal, window)
