@@ -53,11 +53,12 @@ bool kv_merge_fits(const KvAttendArgs& a);  // the rows' launch counts its threa
 // its parts of the workspace begin (bytes).
 struct ChunkPlan {
   int ntiles, blocks, nsplit;
-  size_t info_at, exponents_at, partial_at, end;
+  size_t rest_at, info_at, exponents_at, partial_at, end;
 };
 constexpr int kTileInfoBytes = 16;
 constexpr int kChunkRows = 128;
-int chunk_slots(int head_dim);  // workgroups of that kernel the device holds at once
+int chunk_slots(int head_dim, int dtype);  // workgroups of that kernel the device holds at once
+int64_t chunk_rest_bytes(int head_dim, int dtype);
 int launch_kv_chunk(const KvAttendArgs& a, int dtype, const ChunkPlan& p, const DequantArgs& da, void* stream);
 
 }  // namespace bq

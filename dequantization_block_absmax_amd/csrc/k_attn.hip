@@ -809,9 +809,11 @@ static int64_t choose_splits(int64_t base, int64_t slots, int64_t keys, int num_
 // Rows of a key/value head (new tokens x its query heads) up to which the splitting kernel alone is the
 // faster way, codes decoded anew for every 32 rows against an expanded copy written and read (us, 8 sequences of
 // 8192 keys, 4 heads, this kernel / the expanding ones):
-//   bf16, 128 wide, 4-bit: 256 rows 75 / 88, 384 119 / 108; 64 wide: 256 50 / 63, 384 73 / 71
-//   f16 (entries in two parts), 128 wide, 4-bit: 128 60 / 77, 256 103 / 90, one sequence of 16000 keys 36 / 36
-//   256 wide (16 rows to a workgroup), 8-bit: 64 96 / 159, 128 174 / 147, one sequence of 16000 keys 43 / 54
+//   bf16, 128 wide, 4-bit: 256 rows 75 / 91, 384 121 / 111; 64 wide: 256 50 / 63, 384 74 / 74
+//   f16 (operands in two parts), 128 wide, 4-bit: 192 107 / 125, 256 121 / 117, 384 189 / 152, one sequence of 16000
+//   keys 256 39 / 44, 384 53 / 55; 64 wide: 256 72 / 76, 384 105 / 95
+//   256 wide (16 rows to a workgroup), 8-bit, bf16: 96 118 / 169, 128 166 / 148, one sequence of 16000 keys 43 / 57;
+//   f16: 128 184 / 203, 256 341 / 261
 static int64_t most_few_rows(int64_t head_dim, int dtype) { return head_dim == 256 ? 128 : dtype == F16 ? 256 : 384; }
 
 static Plan make_plan(const KvAttendArgs& a, int dtype) {
@@ -819,7 +821,8 @@ static Plan make_plan(const KvAttendArgs& a, int dtype) {
   const int64_t group = a.heads / a.cache.kv_heads, D = a.cache.head_dim, cus = cu_count();
   int64_t rows = a.max_q_len * group;
   const int64_t ntiles = ((int64_t)a.max_kv_len + 63) / 64;
-  const int64_t per_tile = (int64_t)a.cache.kv_heads * a.num_seqs * 64 * D * 4;  // at most 2^52
+  const int64_t heads_all = (int64_t)a.cache.kv_heads * a.num_seqs, rest = chunk_rest_bytes(a.cache.head_dim, dtype);
+  const int64_t per_tile = heads_all * (64 * D * 4 + rest);  // less than 2^53
   p.many = rows > most_few_rows(D, dtype) && ntiles > 0 && ntiles <= kMaxExpanded / per_tile;
   const int64_t expanded = p.many ? ntiles * per_tile : 0;
   p.few = !p.many || a.num_seqs > 1;
@@ -831,7 +834,7 @@ static Plan make_plan(const KvAttendArgs& a, int dtype) {
     // the one whose rounds of resident workgroups take the least time, a workgroup costing its tiles and
     // about 6 more (start, end, and its part of the join).
     const int64_t base = a.cache.kv_heads * ((a.tokens * group + kChunkRows - 1) / kChunkRows);
-    const int64_t slots = chunk_slots(a.cache.head_dim);
+    const int64_t slots = chunk_slots(a.cache.head_dim, dtype);
     int64_t best = INT64_MAX;
     c.nsplit = 1;
     for (int64_t n = 1; n <= 32 && (n == 1 || n * 4 <= ntiles); ++n) {
@@ -841,8 +844,9 @@ static Plan make_plan(const KvAttendArgs& a, int dtype) {
         c.nsplit = (int)n;
       }
     }
+    const size_t tiles = (size_t)(ntiles * heads_all);
+    c.rest_at = tiles * 64 * D * 4;
     c.info_at = (size_t)expanded;
-    const size_t tiles = (size_t)(ntiles * a.cache.kv_heads * a.num_seqs);
     c.exponents_at = c.info_at + tiles * kTileInfoBytes;
     c.partial_at = (c.exponents_at + tiles * 2 * 64 + 255) & ~(size_t)255;
     c.end = c.partial_at + (c.nsplit > 1 ? (size_t)a.tokens * a.heads * c.nsplit * (D + 3) * 4 : 0);

@@ -24,9 +24,13 @@
 //   O^T = V'^T P^T B = P^T: 8 keys per lane and step, taken in just that order, so the weights stay where
 //                  they were computed; V' is stored with its keys in the same order.
 //
-// Why once rounded.  A cached value is rounded to binary16 here as bq_kv_read in that type gives it: with q and
-// out in binary16 the result is within 4 parts in 2^12 of the exact sums.  Two parts of each operand, as in k_attn.hip,
-// would double the products and the LDS that bound this kernel.
+// What is rounded.  K', V' and the weights to binary16, each 2^-11 at most; with q in bfloat16 that is a fraction of the
+// result's own rounding.  With q in binary16 (kFine) it would be four times that rounding (8.5e-4 of the result's
+// norm against 2.1e-4), the keys most of it, and a sequence's bits would depend on whether a long piece stands
+// beside it in the call, since k_attn.hip keeps two parts of its operands.  So what rounding left of K'
+// follows in 6 bits, multiplied with q in 6 bits by v_mfma_scale_f32_32x32x64_f8f6f4 (an eighth more time on the
+// matrix cores, 3/8 more key bytes), and what it left of the weights as a second binary16 product with the same V'.  V' stays
+// once rounded, as bq_kv_read in that type gives it: 3.0e-4, sqrt(2) times the result's own rounding.
 //
 // What bounds it.  Each product of a wave reads 1 KB of LDS per 32 cycles, and four such waves are all
 // that LDS delivers: matrix cores and LDS have the same least time, and neither is reached while the exponentials and
@@ -50,6 +54,9 @@ constexpr int kTile = 64;   // keys
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef short s16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x32 __attribute__((ext_vector_type(32)));
+typedef int i32x6 __attribute__((ext_vector_type(6)));
+typedef int i32x8 __attribute__((ext_vector_type(8)));
 
 // What a tile's expansion leaves beside its values: exponents, whether its keys have exponents of their own (in
 // an array of bytes, keys then values, tile after tile), and which of its keys some row sees.
@@ -70,9 +77,14 @@ constexpr int kLeastKey = -100, kLeastValue = -80;
 // Workgroup: the keys or the values of one tile of one head.  Fragment order of a tile (16-byte pieces of 8 binary16):
 //   K' piece ((kb * D/16 + s) * 64 + 32 g + n): key 32 kb + n, d = 16 s + 8 g + 0 .. 7
 //   V' piece ((db * 4 + ks) * 64 + 32 g + n):   d = 32 db + n, keys 16 ks + 8 (e / 4) + 4 g + e % 4, e = 0 .. 7
-template <int D, int KB>
+// FINE adds what rounding left of K', in 6 bits (2 of exponent, 3 of mantissa; at most 4 in magnitude): 24 bytes for
+// the 32 d = 64 S + 16 i + 8 g + 0 .. 7, i = 0 .. 3, of key 32 kb + n, the first 16 of each lane before the last 8
+//   words ((S * 2 + kb) * 64) * 6 + 4 (32 g + n) .. + 3 and ((S * 2 + kb) * 64) * 6 + 256 + 2 (32 g + n) .. + 1
+constexpr int kRestWords(int head_dim) { return 12 * head_dim; }  // of a tile
+
+template <int D, int KB, bool FINE>
 __global__ __launch_bounds__(256) void expand_kernel(KvAttendArgs aa, DequantArgs da, int ntiles, u32x4* tiles,
-                                                     TileInfo* infos, int8_t* exponents) {
+                                                     TileInfo* infos, int8_t* exponents, uint32_t* rests) {
   __shared__ float s_c[256];
   __shared__ float s_a[kTile * 8];       // block maxima of the tile's keys or values; zero (theirs may be NaN) where no row sees the key
   __shared__ int64_t s_row[kTile];       // pool row of each key
@@ -191,6 +203,34 @@ __global__ __launch_bounds__(256) void expand_kernel(KvAttendArgs aa, DequantArg
       }
       out[256 * k + tid] = w;
     }
+    if constexpr (FINE) {
+#pragma unroll 1
+      for (int u = tid; u < 2 * D; u += 256) {  // whole waves: 64 lanes of one (S, kb)
+        const int key = (u >> 6 & 1) * 32 + (u & 31), g = u >> 5 & 1, S = u >> 7;
+        const float to = factor(key);
+        f16x32 left;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int d8 = 8 * S + 2 * i + g;
+          const float a = s_a[(key << log2nb) + (d8 * 8 >> aa.cache.log2b)];
+          const uint8_t* src = packed + max(s_row[key], (int64_t)0) * kRow + d8 * KB;
+          u32x2 c;
+          if constexpr (KB == 4) c = (u32x2){*reinterpret_cast<const uint32_t*>(src), 0u};
+          else c = *reinterpret_cast<const u32x2*>(src);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const uint32_t q = KB == 4 ? (c.x >> (8 * (e >> 1) + ((e & 1) ? 0 : 4))) & 15u
+                                       : ((e < 4 ? c.x : c.y) >> (8 * (e & 3))) & 255u;
+            const float v = (s_c[q] * a) * to;
+            left[8 * i + e] = (_Float16)(v - (float)(_Float16)v);
+          }
+        }
+        const i32x6 w = __builtin_amdgcn_cvt_scalef32_pk32_fp6_f16(left, 1.0f);
+        uint32_t* const dst = rests + at * kRestWords(D) + (u >> 6) * 384;
+        *reinterpret_cast<u32x4*>(dst + 4 * (u & 63)) = (u32x4){(uint32_t)w[0], (uint32_t)w[1], (uint32_t)w[2], (uint32_t)w[3]};
+        *reinterpret_cast<u32x2*>(dst + 256 + 2 * (u & 63)) = (u32x2){(uint32_t)w[4], (uint32_t)w[5]};
+      }
+    }
     return;
   }
 #pragma unroll
@@ -224,23 +264,30 @@ __global__ __launch_bounds__(256) void expand_kernel(KvAttendArgs aa, DequantArg
 
 // ---- attention ----------------------------------------------------------------------------
 
+// How the products are taken: kFine with q in binary16 (below); else as rounded, with or without lse.
+enum Form : int { kPlain, kLse, kFine };
+
 // Workgroups per CU (= waves per SIMD) by registers and LDS.
-template <int D>
-constexpr int kChunkPerCu = D == 64 ? 3 : D == 128 ? 2 : 1;
+template <int D, bool FINE>
+constexpr int kChunkPerCu = D == 64 ? (FINE ? 2 : 3) : D == 128 ? 2 : 1;
 
 // Weights begin at 2^kHead and grow to 2^(kHead + kSlack), the last power of two below binary16's largest: as far
 // above its least step, 2^-24, as they can be.
 constexpr float kHead = 3.0f;
 
-template <int D, bool LSE>
-__global__ __launch_bounds__(256, kChunkPerCu<D>) void chunk_kernel(KvAttendArgs aa, int ntiles, const u32x4* tiles,
-                                                                    const TileInfo* infos, const int8_t* exponents,
-                                                                    int nblocks, int nsplit, float* partial, int bf16) {
+template <int D, int FORM>
+__global__ __launch_bounds__(256, (kChunkPerCu<D, FORM == kFine>)) void chunk_kernel(
+    KvAttendArgs aa, int ntiles, const u32x4* tiles, const TileInfo* infos, const int8_t* exponents, const uint32_t* rests,
+    int nblocks, int nsplit, float* partial) {
+  constexpr bool LSE = FORM == kLse, FINE = FORM == kFine, bf16 = !FINE;
   constexpr int kSteps = D / 16, kBlocks = D / 32;
   constexpr int kPieces = kTile * D / 8;          // of keys, and of values, in a tile
   constexpr int kStage = kPieces / 256;           // pieces of each that a thread stages
   __shared__ u32x4 s_key[2][kPieces];
   __shared__ u32x4 s_value[2][kPieces];
+  constexpr int kRest = kRestWords(D) / 3 / 256;  // words of the rests that a thread stages at a time
+  typedef uint32_t RestWords __attribute__((ext_vector_type(kRest)));
+  __shared__ __attribute__((aligned(16))) uint32_t s_rest[2][FINE ? kRestWords(D) : 4];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int n = lane & 31, g = lane >> 5;
@@ -284,10 +331,26 @@ __global__ __launch_bounds__(256, kChunkPerCu<D>) void chunk_kernel(KvAttendArgs
     const ScalarWords src = (ScalarWords)(uintptr_t)(infos + head_at + t);
     return Info{(int16_t)src[0], (int16_t)src[1], (src[0] | src[1]) >> 16 != 0, src[2] | (uint64_t)src[3] << 32};
   };
+  RestWords stage_r[3];
+  auto rest_source = [&](int t) { return reinterpret_cast<const RestWords*>(rests + (head_at + t) * kRestWords(D)) + tid; };
+  auto fetch_rests = [&](int t) {
+    if constexpr (FINE) {
+      const RestWords* src = rest_source(t);
+#pragma unroll
+      for (int k = 0; k < 3; ++k) stage_r[k] = src[256 * k];
+    }
+  };
+  auto put_rests = [&](int b) {
+    if constexpr (FINE) {
+#pragma unroll
+      for (int k = 0; k < 3; ++k) reinterpret_cast<RestWords*>(s_rest[b])[256 * k + tid] = stage_r[k];
+    }
+  };
   Info info = {0, 0, false, 0};
   if (t_first < t_end) {  // on their way while the queries are set up
     fetch(stage_k, t_first, 0);
     fetch(stage_v, t_first, 1);
+    fetch_rests(t_first);
     info = find(t_first);
   }
 
@@ -300,6 +363,7 @@ __global__ __launch_bounds__(256, kChunkPerCu<D>) void chunk_kernel(KvAttendArgs
   const int lo = live ? first_key(aa, sq, row_i) : 0, hi = live ? end_key(aa, sq, row_i) : 0;
   float scale;
   f16x8 q[kSteps];
+  i32x8 q_rest[FINE ? D / 64 : 1];  // four times q, in 6 bits
   {
     const char* src = static_cast<const char*>(aa.q) + (token * aa.q_stride + (int64_t)head * D + 8 * g) * 2;
     u32x4 w[kSteps];
@@ -334,6 +398,16 @@ __global__ __launch_bounds__(256, kChunkPerCu<D>) void chunk_kernel(KvAttendArgs
     }
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) q[s] = __builtin_bit_cast(f16x8, w[s]);
+    if constexpr (FINE) {
+#pragma unroll
+      for (int S = 0; S < D / 64; ++S) {
+        f16x32 x;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) x[i] = q[4 * S + i / 8][i % 8] * (_Float16)4.0f;
+        const i32x6 y = __builtin_amdgcn_cvt_scalef32_pk32_fp6_f16(x, 1.0f);
+        q_rest[S] = (i32x8){y[0], y[1], y[2], y[3], y[4], y[5], 0, 0};
+      }
+    }
     scale = __builtin_ldexpf(fabsf(aa.scale) * 1.44269504088896341f, ex);
   }
 
@@ -351,13 +425,28 @@ __global__ __launch_bounds__(256, kChunkPerCu<D>) void chunk_kernel(KvAttendArgs
   f32x16 sc[2];            // scores of the tile's two halves
   u32x4 w[2][2];           // weights of the halves, 16 keys each
   w[1][0] = w[1][1] = (u32x4){0, 0, 0, 0};
-  auto multiply_keys = [&](int half, const u32x4* tile) {
+  u32x4 left[2][FINE ? 2 : 1];  // what rounding left of them
+  left[1][0] = left[1][FINE ? 1 : 0] = (u32x4){0, 0, 0, 0};
+  // Adds the products with the rests of 64 d of the keys of half a tile.
+  auto add_rest = [&](int half, int S, const uint32_t* rest, f32x16 z) {
+    const uint32_t* src = rest + (S * 2 + half) * 384;
+    const u32x4 lo = *reinterpret_cast<const u32x4*>(src + 4 * lane);
+    const u32x2 hi = *reinterpret_cast<const u32x2*>(src + 256 + 2 * lane);
+    const i32x8 a = {(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, 0, 0};
+    constexpr int kFp6 = 2, kOne = 127, kQuarter = 125;  // the type (2 + 3 bits), and scales 2^(x - 127)
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, q_rest[S], z, kFp6, kFp6, 0, kOne, 0, kQuarter);
+  };
+  auto multiply_keys = [&](int half, const u32x4* tile, const uint32_t* rest) {
     const f16x8* kp = reinterpret_cast<const f16x8*>(tile) + lane + half * kSteps * 64;
     f32x16 z;
 #pragma unroll
     for (int v = 0; v < 16; ++v) z[v] = 0.0f;
 #pragma unroll
     for (int k = 0; k < kSteps; ++k) z = __builtin_amdgcn_mfma_f32_32x32x16_f16(kp[k * 64], q[k], z, 0, 0, 0);
+    if constexpr (FINE) {
+#pragma unroll
+      for (int S = 0; S < D / 64; ++S) z = add_rest(half, S, rest, z);
+    }
     return z;
   };
   auto add_values = [&](int half, const u32x4* tile) {
@@ -365,12 +454,16 @@ __global__ __launch_bounds__(256, kChunkPerCu<D>) void chunk_kernel(KvAttendArgs
 #pragma unroll
     for (int i = 0; i < kBlocks; ++i)
 #pragma unroll
-      for (int ks = 0; ks < 2; ++ks)
+      for (int ks = 0; ks < 2; ++ks) {
         acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vp[(i * 4 + ks) * 64], __builtin_bit_cast(f16x8, w[half][ks]), acc[i], 0, 0, 0);
+        if constexpr (FINE)
+          acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vp[(i * 4 + ks) * 64], __builtin_bit_cast(f16x8, left[half][ks]), acc[i], 0, 0, 0);
+      }
   };
   // The half step of half `half` of tile t: next = the tile (and half) whose scores follow, prev = the
   // tile whose values the other half's weights belong to; beside every second product, move(k) passes a piece on.
-  auto half_step = [&](auto half_c, int t, const Info& info, const u32x4* next, const u32x4* prev, auto move) {
+  auto half_step = [&](auto half_c, int t, const Info& info, const u32x4* next, const uint32_t* next_rest,
+                       const u32x4* prev, auto move) {
     constexpr int half = half_c.value;
     const float ev = (float)info.ev;
     const int j0 = t * kTile + 32 * half;
@@ -412,7 +505,7 @@ __global__ __launch_bounds__(256, kChunkPerCu<D>) void chunk_kernel(KvAttendArgs
       }
     }
     float top = -INFINITY, p = 0.0f;
-    u32x4 x[2];
+    u32x4 x[2], y[2];
     // Weights of scores v .. v + 1 as 2^(score f + c), and their sums in this half step.  `part` takes the weights
     // as rounded: a row that one key fills gives that key's value.  Where lse is asked for, `whole` takes them
     // unrounded: the rounded ones would move it by up to 2^-11.
@@ -422,8 +515,13 @@ __global__ __launch_bounds__(256, kChunkPerCu<D>) void chunk_kernel(KvAttendArgs
       if (v & 1) {
         uint32_t pair = pack_f16(p, e);
         asm volatile("" : "+v"(pair));  // here, beside the products, and not on the side of the branch below
-        part = __builtin_amdgcn_fdot2(__builtin_bit_cast(f16x2, pair), (f16x2){(_Float16)1.0f, (_Float16)1.0f}, part, false);
+        const f16x2 h = __builtin_bit_cast(f16x2, pair);
+        if constexpr (!FINE) part = __builtin_amdgcn_fdot2(h, (f16x2){(_Float16)1.0f, (_Float16)1.0f}, part, false);
         if constexpr (LSE) whole += p + e;
+        if constexpr (FINE) {
+          part += p + e;
+          y[v >> 3][(v & 7) >> 1] = pack_f16(fmaf((float)h.x, -1.0f, p), fmaf((float)h.y, -1.0f, e));
+        }
         x[v >> 3][(v & 7) >> 1] = pair;
       } else {
         p = e;
@@ -431,6 +529,10 @@ __global__ __launch_bounds__(256, kChunkPerCu<D>) void chunk_kernel(KvAttendArgs
     };
     auto offset = [&]() { return (ev + kHead) - fmaxf(ref, -0x1p120f); };  // no key yet: -infinity stays
     float c = offset();
+    auto add_left = [&](int z) {
+      const int i = (z >> 1) % kBlocks, ks = (z >> 1) / kBlocks;
+      acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a[z], __builtin_bit_cast(f16x8, left[half ^ 1][ks]), acc[i], 0, 0, 0);
+    };
     f32x16& z_next = sc[half ^ 1];
 #pragma unroll
     for (int v = 0; v < 16; ++v) z_next[v] = 0.0f;
@@ -442,6 +544,10 @@ __global__ __launch_bounds__(256, kChunkPerCu<D>) void chunk_kernel(KvAttendArgs
         acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a[z], __builtin_bit_cast(f16x8, w[half ^ 1][ks]), acc[i], 0, 0, 0);
       } else {
         z_next = __builtin_amdgcn_mfma_f32_32x32x16_f16(a[z], q[z >> 1], z_next, 0, 0, 0);
+      }
+      if constexpr (FINE) {
+        if (z % 8 == 7) z_next = add_rest(half ^ 1, z / 8, next_rest, z_next);
+        if (z & 1) add_left(z);
       }
       if (z + kAhead < kMul) a[z + kAhead] = operand(z + kAhead);
       if (z & 1) move(z >> 1);
@@ -471,8 +577,11 @@ __global__ __launch_bounds__(256, kChunkPerCu<D>) void chunk_kernel(KvAttendArgs
 #pragma unroll
       for (int v = 0; v < 16; ++v) weigh(v, c);
     }
-    w[half][0] = x[0];
-    w[half][1] = x[1];
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {
+      w[half][ks] = x[ks];
+      if constexpr (FINE) left[half][ks] = y[ks];
+    }
     // The denominator.  In units of 2^(M - 3 - ev) a rounded weight is off by up to 2^-25 at the least, which
     // is nothing beside a sum of one.  Where the row's reference comes from values more than 2^3 times
     // as large as this tile's, or the keys have exponents of their own, it takes weights that are not rounded.
@@ -500,9 +609,11 @@ __global__ __launch_bounds__(256, kChunkPerCu<D>) void chunk_kernel(KvAttendArgs
       s_key[0][256 * k + tid] = stage_k[k];
       s_value[1][256 * k + tid] = (u32x4){0, 0, 0, 0};  // no weights wait at first
     }
+    put_rests(0);
     fetch(stage_k, min(t_first + 1, t_end - 1), 0);
+    fetch_rests(min(t_first + 1, t_end - 1));
     __syncthreads();
-    sc[0] = multiply_keys(0, s_key[0]);
+    sc[0] = multiply_keys(0, s_key[0], s_rest[0]);
     for (int t = t_first; t < t_end; ++t) {
       const int b = (t - t_first) & 1;
       const Info info_next = find(min(t + 1, t_end - 1));
@@ -512,14 +623,22 @@ __global__ __launch_bounds__(256, kChunkPerCu<D>) void chunk_kernel(KvAttendArgs
       // written were last read before the previous barrier.
       const u32x4* src_k = source(min(t + 2, t_end - 1), 0);
       const u32x4* src_v = source(min(t + 1, t_end - 1), 1);
-      half_step(std::integral_constant<int, 0>(), t, info, s_key[b], s_value[b ^ 1], [&](int k) {
+      auto ask = [&](int k) {
+        u32x4& piece = k < kStage ? stage_k[k] : stage_v[k - kStage];
+        piece = k < kStage ? src_k[256 * k] : src_v[256 * (k - kStage)];
+      };
+      put_rests(b ^ 1);
+      half_step(std::integral_constant<int, 0>(), t, info, s_key[b], s_rest[b], s_value[b ^ 1], [&](int k) {
         u32x4& piece = k < kStage ? stage_k[k] : stage_v[k - kStage];
         u32x4* dst = k < kStage ? s_key[b ^ 1] + 256 * k : s_value[b] + 256 * (k - kStage);
         dst[tid] = piece;
-        piece = k < kStage ? src_k[256 * k] : src_v[256 * (k - kStage)];
+        if constexpr (!FINE) ask(k);
       });
       __syncthreads();
-      half_step(std::integral_constant<int, 1>(), t, info, s_key[b ^ 1], s_value[b], [](int) {});
+      fetch_rests(min(t + 2, t_end - 1));
+      half_step(std::integral_constant<int, 1>(), t, info, s_key[b ^ 1], s_rest[b ^ 1], s_value[b], [&](int k) {
+        if constexpr (FINE) ask(k);
+      });
       info = info_next;
     }
     add_values(1, s_value[(t_end - 1 - t_first) & 1]);
@@ -549,41 +668,54 @@ __global__ __launch_bounds__(256, kChunkPerCu<D>) void chunk_kernel(KvAttendArgs
       }
     }
   if (g == 0) {
-    if (nsplit > 1) reinterpret_cast<Partial*>(partial + aa.tokens * aa.heads * nsplit * D)[part] = {ref - kHead, l, exact};
-    else if constexpr (LSE) aa.lse[token * aa.heads + head] = log_sum(ref - kHead, exact);
+    if (nsplit > 1) reinterpret_cast<Partial*>(partial + aa.tokens * aa.heads * nsplit * D)[part] = {ref - kHead, l, FINE ? l : exact};
+    else if (LSE || (FINE && aa.lse != nullptr)) aa.lse[token * aa.heads + head] = log_sum(ref - kHead, FINE ? l : exact);
   }
 }
 
-template <int D>
-hipError_t launch_chunk(const KvAttendArgs& a, const ChunkPlan& p, int bf16, const DequantArgs& da, hipStream_t s) {
-  u32x4* tiles = static_cast<u32x4*>(a.workspace);
-  TileInfo* infos = reinterpret_cast<TileInfo*>(static_cast<char*>(a.workspace) + p.info_at);
-  int8_t* exponents = static_cast<int8_t*>(a.workspace) + p.exponents_at;
-  float* partial = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + p.partial_at);
+template <int D, int KB>
+hipError_t launch_expand(const KvAttendArgs& a, const ChunkPlan& p, bool fine, const DequantArgs& da, hipStream_t s) {
+  char* const ws = static_cast<char*>(a.workspace);
   const dim3 grid((unsigned)p.ntiles, (unsigned)a.cache.kv_heads * 2, (unsigned)a.num_seqs);
-  hipError_t e = da.K == 16 ? launch_kernel(expand_kernel<D, 4>, grid, dim3(256), s, a, da, p.ntiles, tiles, infos, exponents)
-                            : launch_kernel(expand_kernel<D, 8>, grid, dim3(256), s, a, da, p.ntiles, tiles, infos, exponents);
+  return launch_kernel(fine ? expand_kernel<D, KB, true> : expand_kernel<D, KB, false>, grid, dim3(256), s, a, da, p.ntiles,
+                       reinterpret_cast<u32x4*>(ws), reinterpret_cast<TileInfo*>(ws + p.info_at),
+                       reinterpret_cast<int8_t*>(ws + p.exponents_at), reinterpret_cast<uint32_t*>(ws + p.rest_at));
+}
+
+template <int D>
+hipError_t launch_chunk(const KvAttendArgs& a, const ChunkPlan& p, bool fine, const DequantArgs& da, hipStream_t s) {
+  const hipError_t e = da.K == 16 ? launch_expand<D, 4>(a, p, fine, da, s) : launch_expand<D, 8>(a, p, fine, da, s);
   if (e != hipSuccess) return e;
-  const dim3 grid2((unsigned)(a.cache.kv_heads * p.nsplit * p.blocks), 1u, (unsigned)a.num_seqs);
-  return launch_kernel(a.lse != nullptr ? chunk_kernel<D, true> : chunk_kernel<D, false>, grid2, dim3(256), s, a, p.ntiles, tiles,
-                       infos, exponents, p.blocks, p.nsplit, partial, bf16);
+  char* const ws = static_cast<char*>(a.workspace);
+  const dim3 grid((unsigned)(a.cache.kv_heads * p.nsplit * p.blocks), 1u, (unsigned)a.num_seqs);
+  const auto kernel = fine ? chunk_kernel<D, kFine> : a.lse != nullptr ? chunk_kernel<D, kLse> : chunk_kernel<D, kPlain>;
+  return launch_kernel(kernel, grid, dim3(256), s, a, p.ntiles, reinterpret_cast<const u32x4*>(ws),
+                       reinterpret_cast<const TileInfo*>(ws + p.info_at), reinterpret_cast<const int8_t*>(ws + p.exponents_at),
+                       reinterpret_cast<const uint32_t*>(ws + p.rest_at), p.blocks, p.nsplit,
+                       reinterpret_cast<float*>(ws + p.partial_at));
+}
+
+template <bool FINE>
+int slots(int head_dim) {
+  return cu_count() * (head_dim == 64 ? kChunkPerCu<64, FINE> : head_dim == 128 ? kChunkPerCu<128, FINE> : kChunkPerCu<256, FINE>);
 }
 
 }  // namespace
 
 // Workgroups of the attention kernel that the device holds at once.
-int chunk_slots(int head_dim) {
-  return cu_count() * (head_dim == 64 ? kChunkPerCu<64> : head_dim == 128 ? kChunkPerCu<128> : kChunkPerCu<256>);
-}
+int chunk_slots(int head_dim, int dtype) { return dtype == F16 ? slots<true>(head_dim) : slots<false>(head_dim); }
+
+// Bytes of a tile beside its 256 head_dim: the rests.
+int64_t chunk_rest_bytes(int head_dim, int dtype) { return dtype == F16 ? 4 * kRestWords(head_dim) : 0; }
 
 static_assert(sizeof(TileInfo) == kTileInfoBytes && kTile == 64, "workspace layout");
 
 int launch_kv_chunk(const KvAttendArgs& a, int dtype, const ChunkPlan& p, const DequantArgs& da, void* stream) {
   hipStream_t s = static_cast<hipStream_t>(stream);
-  const int bf16 = dtype == BF16;
-  if (a.cache.head_dim == 64) return (int)launch_chunk<64>(a, p, bf16, da, s);
-  if (a.cache.head_dim == 128) return (int)launch_chunk<128>(a, p, bf16, da, s);
-  return (int)launch_chunk<256>(a, p, bf16, da, s);
+  const bool fine = dtype == F16;
+  if (a.cache.head_dim == 64) return (int)launch_chunk<64>(a, p, fine, da, s);
+  if (a.cache.head_dim == 128) return (int)launch_chunk<128>(a, p, fine, da, s);
+  return (int)launch_chunk<256>(a, p, fine, da, s);
 }
 
 }  // namespace bq
