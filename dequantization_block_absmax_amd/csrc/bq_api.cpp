@@ -475,6 +475,7 @@ static bq_status check_attention_shape(const bq_kv_cache* cache, const bq_kv_bat
   a->max_kv_len = held < b->max_kv_len ? (int32_t)held : b->max_kv_len;
   if (a->max_kv_len > 1 << 30) return BQ_ERR_SIZE;
   a->heads = heads;
+  a->bits = t->K == 16 ? 4 : 8;
   return BQ_OK;
 }
 

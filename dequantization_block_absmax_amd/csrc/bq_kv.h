@@ -34,6 +34,7 @@ struct KvAttendArgs {
   int64_t out_stride;
   float* lse;        // or NULL
   int32_t heads, causal, window;
+  int32_t bits;      // of a code
   float scale;
   void* workspace;
 };

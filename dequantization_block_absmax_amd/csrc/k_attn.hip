@@ -302,22 +302,29 @@ __device__ __forceinline__ void load_fence() {
   __builtin_amdgcn_sched_barrier(0);
 }
 
-// Waves per workgroup and per SIMD: what the registers of each form allow without spilling (the table
-// and sums in LDS leave room for two workgroups of eight waves).
-template <int D, int NB, int RT>
+// Waves per workgroup and per SIMD.  Four per SIMD, two workgroups to a CU, where 128 registers hold a form; else one
+// workgroup: among the forms at the limit 64 wide with 32 rows and two blocks (24 x 6 tokens, 8-bit, windows of 4000, buffers
+// in turn: 38.1 us at four with 12 to 15 registers spilled, 35.9 at two with the weights' rests besides; bf16
+// 33.5 and 29.4) and 128 wide in 8 bits with two blocks (64 single tokens over up to 4096 keys, bf16: 100 us with 7
+// spilled, 90).  Of the others <128, 4, 8, 2> with q in binary16 spills one register.
+constexpr bool wide_form(int head_dim, int nb, int bits, int rt) {
+  return nb == 2 && rt * head_dim == 128 && (head_dim == 64 || bits == 8);
+}
+
+template <int D, int NB, int KB, int RT>
 struct Occupancy {
   static constexpr int kWaves = D == 256 && NB == 8 ? 4 : 8;
-  static constexpr int kPerSimd = D == 256 && NB == 8 ? 1 : RT * D <= 128 && NB <= 2 ? 4 : 2;
-  // room for the weights' rests too (q in binary16; without them the weights are rounded once, 2^-12)
+  static constexpr int kPerSimd = D == 256 && NB == 8 ? 1 : RT * D <= 128 && NB <= 2 && !wide_form(D, NB, KB, RT) ? 4 : 2;
+  // room for the weights' rests too (q in binary16; without them the weights are rounded once, 2^-11)
   static constexpr bool kRests = kPerSimd == 4 ? RT * NB * D <= 128 : kPerSimd == 2 && (NB <= 2 || RT * D == 128);
 };
 
 template <int D, int NB, int KB, int RT, bool HL>
-__global__ __launch_bounds__((64 * Occupancy<D, NB, RT>::kWaves), (Occupancy<D, NB, RT>::kPerSimd)) void attend_kernel(
+__global__ __launch_bounds__((64 * Occupancy<D, NB, KB, RT>::kWaves), (Occupancy<D, NB, KB, RT>::kPerSimd)) void attend_kernel(
     KvAttendArgs aa, DequantArgs da, int nsplit, float* partial, int rows) {
   using O = Operand<KB, HL>;
   constexpr bool bf16 = !HL;  // the type of q and out
-  constexpr int W = Occupancy<D, NB, RT>::kWaves;
+  constexpr int W = Occupancy<D, NB, KB, RT>::kWaves;
   using S = Shape<D, NB, KB>;
   constexpr int kThreads = 64 * W;
   constexpr int kRows = 16 * RT;
@@ -576,7 +583,7 @@ __global__ __launch_bounds__((64 * Occupancy<D, NB, RT>::kWaves), (Occupancy<D, 
   };
 
   // Weights of the lane's 8 keys, block by block, as pairs of binary16.
-  constexpr bool kRests = HL && Occupancy<D, NB, RT>::kRests;
+  constexpr bool kRests = HL && Occupancy<D, NB, KB, RT>::kRests;
   u32x4 w[RT][NB], rest[RT][kRests ? NB : 1];  // and what rounding them left
   auto weights = [&](int j0, const Pages& p, const Values<D, NB, KB>& x) {
     float va[2][4][NB];
@@ -861,7 +868,7 @@ static Plan make_plan(const KvAttendArgs& a, int dtype) {
   const int64_t rows_all = a.tokens * group / (16 * p.rt) + a.num_seqs;
   const int64_t base = a.cache.kv_heads * std::min((int64_t)p.tiles * a.num_seqs, rows_all);
   const int nb = a.cache.head_dim >> a.cache.log2b;
-  const int64_t slots = cus * (D == 256 || nb == 4 || (p.rt == 2 && D == 128) ? 1 : 2);
+  const int64_t slots = cus * (D == 256 || nb == 4 || (p.rt == 2 && D == 128) || wide_form((int)D, nb, a.bits, p.rt) ? 1 : 2);
   // the workspace is asked for without a window, and holds for any
   int64_t n = choose_splits(base, slots, a.max_kv_len, a.num_seqs);
   if (a.window > 0 && (int64_t)a.window + a.max_q_len < a.max_kv_len) {
@@ -881,7 +888,7 @@ template <int D, int NB, int KB, int RT, bool HL>
 hipError_t launch_type(const KvAttendArgs& a, const Plan& p, const DequantArgs& da, hipStream_t s) {
   const dim3 grid((unsigned)(p.tiles * p.nsplit), (unsigned)a.cache.kv_heads, (unsigned)a.num_seqs);
   float* partial = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + p.partial_at);
-  return launch_kernel(attend_kernel<D, NB, KB, RT, HL>, grid, dim3(64 * Occupancy<D, NB, RT>::kWaves), s, a, da, p.nsplit,
+  return launch_kernel(attend_kernel<D, NB, KB, RT, HL>, grid, dim3(64 * Occupancy<D, NB, KB, RT>::kWaves), s, a, da, p.nsplit,
                        partial, p.many ? kFewOnly : kAllRows);
 }
 
@@ -918,7 +925,7 @@ int launch_kv_attend(const KvAttendArgs& a, int dtype, const DequantArgs& da, vo
   const Plan p = make_plan(a, dtype);
   // Every launch fits before the first is enqueued: threads along x in 32 bits, grid rows in 16.
   const bool join = (p.few && p.nsplit > 1) || (p.many && p.chunk.nsplit > 1);
-  const int few_threads = 64 * (a.cache.head_dim == 256 && a.cache.log2b == 5 ? Occupancy<256, 8, 1>::kWaves : 8);
+  const int few_threads = 64 * (a.cache.head_dim == 256 && a.cache.log2b == 5 ? Occupancy<256, 8, 4, 1>::kWaves : 8);
   if ((p.few && (int64_t)p.tiles * p.nsplit * few_threads > UINT32_MAX) || a.cache.kv_heads > 32767 ||
       (p.many && (int64_t)a.cache.kv_heads * p.chunk.nsplit * p.chunk.blocks > UINT32_MAX / 256) ||
       (p.many && p.chunk.ntiles > (int64_t)UINT32_MAX / 256) || (join && !kv_merge_fits(a))) {

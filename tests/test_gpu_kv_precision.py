@@ -47,3 +47,19 @@ def test_error_in_units_of_the_results_rounding(dev, dtype, name, dim, B, bits):
             continue  # single rows: what one key holds is not averaged
         rows = slice(batch.starts[s], batch.starts[s] + n)
         assert error[rows].norm() <= 1.75 * rounding[rows].norm(), (s, float(error[rows].norm() / rounding[rows].norm()))
+
+
+@pytest.mark.parametrize("dim,B,bits,lens", [(64, 32, 4, [(6, 3000), (5, 900)]), (64, 32, 8, [(6, 3000), (5, 900)]),
+                                             (128, 64, 8, [(1, 3000), (1, 900)]), (128, 64, 8, [(6, 3000), (5, 900)]),
+                                             (64, 64, 4, [(6, 3000), (1, 900)])])
+def test_few_rows_with_weights_in_two_parts(dev, dim, B, bits, lens):
+    """binary16, forms whose registers hold the weights' rests: table entries and weights in two parts (2^-22), so that
+    the result's own rounding is nearly all: 1.2 units."""
+    rng = np.random.default_rng(dim + B + bits)
+    pool = Pool(dev, synth.table16() if bits == 4 else synth.table256(), sum(-(-kv // 32) for _, kv in lens) + 1, 32, 2, dim, B)
+    pool.fill(rng)
+    batch = Batch(dev, pool, lens, rng)
+    q = queries(dev, rng, batch.tokens, 8, dim, "float16", 2.0)
+    want = torch.from_numpy(reference(pool, batch, q, "float16", dim ** -0.5)[0])
+    out, _ = run_attention(dev, pool, batch, q, "float16", dim ** -0.5)
+    assert (out.double().cpu() - want).norm() <= 1.2 * (want.half().double() - want).norm()
