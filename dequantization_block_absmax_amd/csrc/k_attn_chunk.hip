@@ -13,8 +13,8 @@
 // so that w V' has the same unit, 2^(M - 17), in every tile, and a weight is rounded relative to the largest
 // weight times value of its row and not to the largest weight.  The denominator is sum_j w_ij 2^-ev_j.
 // Exponents of their own, and denominators of unrounded weights, cost where they occur: 2048 tokens over 18432 keys
-// take 622 us as a rule, 898 where every tile's values are apart, 736 where the first tile's values are 2^9
-// times the others' and matter to the rows.
+// take 655 us as a rule, 935 where every tile's values are apart, 789 where the first tile's values are 2^9
+// times the others' and matter to the rows (in one run).
 //
 // chunk_kernel: a workgroup of four waves takes 128 rows (new token x query head of one key/value
 // head) and walks the tiles of 64 keys with the running maximum and sum of the softmax.  A wave takes
@@ -413,6 +413,8 @@ __global__ __launch_bounds__(256, (kChunkPerCu<D, FORM == kFine>)) void chunk_ke
 
   // M of the row; sums of its weights as rounded and unrounded (this lane's keys, in units of 2^(M - 3))
   float ref = -INFINITY, sum = 0.0f, exact = 0.0f;
+  float least_ev = -INFINITY;  // of tiles whose rounded weights are good for the denominator
+  int most_ev = -1000;         // of the tiles so far
   f32x16 acc[kBlocks];
 #pragma unroll
   for (int i = 0; i < kBlocks; ++i)
@@ -567,6 +569,7 @@ __global__ __launch_bounds__(256, (kChunkPerCu<D, FORM == kFine>)) void chunk_ke
       const float down = ref == -INFINITY ? 0.0f : exp2_hw(ref - up);
       sum = lower(sum, ref, up);
       if constexpr (LSE) exact = lower(exact, ref, up);
+      if constexpr (!FINE) least_ev = up > ref ? ev - kHead : least_ev;
       ref = up;
 #pragma unroll
       for (int i = 0; i < kBlocks; ++i)
@@ -582,12 +585,12 @@ __global__ __launch_bounds__(256, (kChunkPerCu<D, FORM == kFine>)) void chunk_ke
       w[half][ks] = x[ks];
       if constexpr (FINE) left[half][ks] = y[ks];
     }
-    // The denominator.  In units of 2^(M - 3 - ev) a rounded weight is off by up to 2^-25 at the least, which
-    // is nothing beside a sum of one.  Where the row's reference comes from values more than 2^3 times
-    // as large as this tile's, or the keys have exponents of their own, it takes weights that are not rounded.
-    const float with = sum + __builtin_ldexpf(part, -info.ev);
-    const u32x2 o = __builtin_amdgcn_permlane32_swap(f32_bits(with), f32_bits(with), false, false);
-    if (info.apart || __any(ref != -INFINITY && __builtin_ldexpf(bits_f32(o.x) + bits_f32(o.y), info.ev) < 1.0f)) {
+    // The denominator.  It is at least 2^(3 - ev) of the tile that M is from, and a rounded weight, times 2^-ev of
+    // its own tile, is off by up to 2^(-25 - ev) at the least: nothing beside it unless the tile's values are more than 2^3 times
+    // smaller.  Then, and where the keys have exponents of their own, it takes weights that are not rounded and
+    // do not hold the exponent.  (kFine sums unrounded weights anyway; these lose what counts below 2^-126 only.)
+    if constexpr (FINE) most_ev = max(most_ev, info.ev);
+    if (info.apart || (FINE ? info.ev < most_ev - 60 : __any(ev < least_ev))) {
       float more = 0.0f;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -598,7 +601,7 @@ __global__ __launch_bounds__(256, (kChunkPerCu<D, FORM == kFine>)) void chunk_ke
       sum += more;
       if constexpr (LSE) exact += more;
     } else {
-      sum = with;
+      sum += __builtin_ldexpf(part, -info.ev);
       if constexpr (LSE) exact += __builtin_ldexpf(whole, -info.ev);
     }
   };
