@@ -791,8 +791,11 @@ struct Plan {
   ChunkPlan chunk;
 };
 
-// The expanded keys and values may take this much of the workspace; a call that would need more is
-// left to the splitting kernel.
+// The expanded keys and values may take this much of the workspace (with q in binary16 3/16 of it more, for the
+// rests); a call that would need more is left to the splitting kernel.  Room is kept for every sequence at the
+// longest length, as their row counts are known on the device only: 2048 tokens beside 63 single ones, 32 heads over 8 of 128,
+// bf16, take 2.1 GiB and 0.60 ms over 8192 keys each, 4.3 GiB and 1.2 ms over 16384, and over 32768, left to the
+// splitting kernel, 7.4 ms.
 constexpr int64_t kMaxExpanded = (int64_t)4 << 30;
 
 // Splits of the keys: those whose rounds of resident workgroups (`slots`; `base` without splits) take the least
@@ -829,9 +832,8 @@ static Plan make_plan(const KvAttendArgs& a, int dtype) {
   int64_t rows = a.max_q_len * group;
   const int64_t ntiles = ((int64_t)a.max_kv_len + 63) / 64;
   const int64_t heads_all = (int64_t)a.cache.kv_heads * a.num_seqs, rest = chunk_rest_bytes(a.cache.head_dim, dtype);
-  const int64_t per_tile = heads_all * (64 * D * 4 + rest);  // less than 2^53
+  const int64_t per_tile = heads_all * 64 * D * 4;  // at most 2^52
   p.many = rows > most_few_rows(D, dtype) && ntiles > 0 && ntiles <= kMaxExpanded / per_tile;
-  const int64_t expanded = p.many ? ntiles * per_tile : 0;
   p.few = !p.many || a.num_seqs > 1;
   if (p.many) {
     ChunkPlan& c = p.chunk;
@@ -853,7 +855,7 @@ static Plan make_plan(const KvAttendArgs& a, int dtype) {
     }
     const size_t tiles = (size_t)(ntiles * heads_all);
     c.rest_at = tiles * 64 * D * 4;
-    c.info_at = (size_t)expanded;
+    c.info_at = c.rest_at + tiles * rest;
     c.exponents_at = c.info_at + tiles * kTileInfoBytes;
     c.partial_at = (c.exponents_at + tiles * 2 * 64 + 255) & ~(size_t)255;
     c.end = c.partial_at + (c.nsplit > 1 ? (size_t)a.tokens * a.heads * c.nsplit * (D + 3) * 4 : 0);

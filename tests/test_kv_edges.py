@@ -24,3 +24,15 @@ def test_a_join_that_is_too_large_is_refused_before_any_work(dim, over):
     assert bq.bq_kv_attention_workspace_bytes(c, b, bq.BQ_BF16, 4096) > 2 * over * dim * 4
     row = 4096 * dim
     assert attend(c, b, heads=4096, q_stride=row, out_stride=row) == bq.BQ_ERR_SIZE
+
+
+@pytest.mark.parametrize("dtype", [bq.BQ_F16, bq.BQ_BF16])
+def test_the_expanded_copy_may_take_four_gib(dtype):
+    """64 sequences of up to 16384 keys, 8 heads of 128, one of them long: 4 GiB of expanded keys and values, in either
+    type; twice as many keys are left to the other kernel, whose workspace is partial sums."""
+    c = cache(kv_heads=8, num_pages=1 << 14, page_size=64)
+    def need(keys):
+        b = batch(num_seqs=64, tokens=2111, max_q_len=2048, max_kv_len=keys, table_stride=keys // 64)
+        return bq.bq_kv_attention_workspace_bytes(c, b, dtype, 32)
+    assert 4 << 30 < need(16384) < (4 << 30) * 5 // 4 + (1 << 29)
+    assert 0 < need(32768) < 1 << 30
