@@ -10,10 +10,11 @@
 //   s_ij = R_i sum_b a_jb (sum_{d in b} q'_id c_jd)   q' = q 2^-e_i exact in binary16, R_i = scale 2^e_i
 //   o_i  = sum_j (p_ij a'_jb) c'_jd                    for d in block b of the values
 // so no cached value is formed: a code byte indexes a table in LDS that holds its two binary16
-// entries side by side.  Rounded to 16 bits are: c (2^-12 relative), the weights p a' (2^-12 relative
-// to the largest of their row), q' where it falls 2^-14 below its row's largest element, and the
-// result.  With q in binary16, whose result keeps three more bits than a bfloat16's, c enters in two parts and
-// the weights, where registers allow, too (Operand).  e_i is the exponent of the row's largest |q|.  Weights are kept in range by the reference
+// entries side by side.  Rounded to 16 bits are: c (2^-11 relative at most), the weights p a' (2^-11, and 2^-25 of the
+// largest of their row), q' where it falls 2^-14 below its row's largest element, and the result.  With q
+// in binary16, whose result keeps three more bits than a bfloat16's, c enters in two parts and the weights, where registers
+// allow, too (Operand, Occupancy): the error is the result's own rounding, or sqrt(2) times that.  e_i is the
+// exponent of the row's largest |q|.  Weights are kept in range by the reference
 //   M_i = max_j (log2-domain s_ij + E_j),   E_j the exponent of token j's largest value maximum,
 // in place of the plain running maximum: the weights p a' = 2^(s - M) a' then stay below 2^14 whatever
 // the size of the values, and sum and weighted sum carry the same factor, which cancels.
@@ -35,11 +36,14 @@
 //
 // What bounds it.  For single tokens and drafts the bytes of codes and maxima; beside them the lookups (a permute and an
 // LDS read per code byte and use) and the exchange keep the vector units and LDS about as busy, so that the
-// kernels take 1.1 to 1.3 times what loads alone take with the same schedule.  On MI355X, median of a call's kernels:
-//   64 sequences of up to 8192 keys, 32 heads over 8 of 128, 4-bit, B = 64, bf16: 91 us, 4.1 TB/s (loads alone 71)
-//   3 of up to 131072 keys, 16 over 2 of 128, 8-bit, B = 128, f16: 39 us + join 4.7,  4.7 TB/s (loads alone 31)
-//   24 x 6 tokens, window 4000, 20 over 5 of 64, 8-bit, B = 32, f16: 26 us + join 5,  2.3 TB/s (loads alone 23.5)
-//   1 of 1000 keys, 32 over 8 of 128, 4-bit, B = 64, bf16: 7.5 us + join 3.3: the chain of loads from the arguments to
+// kernels take 1.1 to 1.3 times what loads alone take with the same schedule (timed with the buffers in the last-level
+// cache: 71 of 91 us, 31 of 39, 23.5 of 26.2 for the first three).  On MI355X, median of a call's kernels, buffers in turn
+// past that cache:
+//   64 sequences of up to 8192 keys, 32 heads over 8 of 128, 4-bit, B = 64, bf16: 94 us, 4.0 TB/s
+//   3 of up to 131072 keys, 16 over 2 of 128, 8-bit, B = 128, f16: 44.5 us + join 4.7, 4.1 TB/s
+//   24 x 6 tokens, window 4000, 20 over 5 of 64, 8-bit, B = 32, f16: 32.3 us + join 4.7, 1.8 TB/s: a wave has one group of
+//   keys in flight and about eight in all
+//   1 of 1000 keys, 32 over 8 of 128, 4-bit, B = 64, bf16: 8.3 us + join 3.5: the chain of loads from the arguments to
 //   the sequence, its pages and its keys, each about 1 us, and two launches
 // Eight waves of a workgroup share one table in LDS (four: 114 us in the first case, 43 in the second; sixteen: 98
 // and 43).  Workgroups that each take an equal share of all keys, whatever the sequence, gained nothing (84 us
@@ -132,9 +136,9 @@ __device__ __forceinline__ uint32_t entry_of(uint32_t w, int b, uint32_t copy) {
   return __builtin_amdgcn_perm(w, copy, 0x0c0c0000u | (uint32_t)(4 + b) << 8);
 }
 
-// How a table entry enters the products.  One part (q in bfloat16): its binary16 rounding, 2^-12 relative, far
+// How a table entry enters the products.  One part (q in bfloat16): its binary16 rounding, 2^-11 relative, far
 // below what the result's rounding leaves.  Two parts (q in binary16): the rounding and, beside it, the
-// rounded rest, 2^-24 relative together; the other operand repeats, and the sum over k adds both.
+// rounded rest, 2^-22 relative together; the other operand repeats, and the sum over k adds both.
 //   entries in LDS, by byte: 4-bit codes the pair (low nibble, high nibble), then the rests' pair; 8-bit codes
 //   one entry, then its rest
 template <int KB, bool HL>

@@ -35,10 +35,12 @@
 // What bounds it.  Each product of a wave reads 1 KB of LDS per 32 cycles, and four such waves are all
 // that LDS delivers: matrix cores and LDS have the same least time, and neither is reached while the exponentials and
 // the barrier stand between.  On MI355X (the largest library product of this type: 1189 TFLOP/s):
-//   2048 tokens over 18432 keys, 32 heads over 8 of 128, bf16: 611-635 us (920-950 TFLOP/s), expansion 23 us
-//   777 over 6000, 8 heads over 1 of 256, bf16: 56 us (640 TFLOP/s, 245 workgroups: about 13 us are start and end of
-//   a workgroup, not its tiles), expansion 6, join 7.6
-//   9 sequences of up to 700 over up to 5000, 16 over 4 of 64, f16: 39 us (510 TFLOP/s), expansion 10
+//   2048 tokens over 18432 keys, 32 heads over 8 of 128, bf16: 600-650 us by the box's clock (900-970 TFLOP/s), matrix
+//   cores busy 52%, expansion 24 us; f16, with the rests, 910-990 us
+//   777 over 6000, 8 heads over 1 of 256, bf16: 59.5 us (600 TFLOP/s, matrix cores 25%; 245 workgroups: about 13 us are
+//   start and end of a workgroup, not its tiles), expansion 7.5, join 8.1; f16 91 us
+//   9 sequences of up to 700 over up to 5000, 16 over 4 of 64, f16: 58 us (340 TFLOP/s, matrix cores 24%, vector units
+//   about 35%: short workgroups of unequal length), expansion 13; bf16 42
 #include <hip/hip_runtime.h>
 
 #include <type_traits>

@@ -11,12 +11,15 @@
 // Work decomposition.  A unit is 8 consecutive elements of one token's head.  Lane `tid` of a
 // 256-lane workgroup handles units (tile * U + u) * 256 + tid, u < U, of the tokens' units in
 // (token, head, d) order; grid row 0 takes the keys, row 1 the values.  A block is B / 8 = 4 .. 32
-// neighbouring lanes, whose maximum is joined by lane permutes.  Both kernels stream and are bound by HBM for
-// long inputs, by their launch for a decoding step (3 us).  On MI355X:
-//   write  one unit per lane, ordinary loads: 16384 tokens of 8 x 128 bf16 into 8-bit codes, B = 128, take 22.0 us
-//          (4.6 TB/s of input and cache); two units 22.4, four 25.0, four with non-temporal loads 27.0
+// neighbouring lanes, whose maximum is joined by lane permutes.  Both kernels stream; a decoding step is bound by the
+// launch (3 us).  On MI355X:
+//   write  one unit per lane, ordinary loads: 16384 tokens of 8 x 128 bf16 into 8-bit codes, B = 128, take 28.8 us from
+//          HBM (3.5 TB/s of input and cache; about 22 vector instructions per element), 22.0 with the input in the last-level
+//          cache; there two units 22.4, four 25.0, four with non-temporal loads 27.0
 //   read   two units per lane where that leaves every CU several workgroups: 32768 tokens of 8 x 128 from
-//          4-bit codes, B = 64, to bf16 take 25.9 us (6.6 TB/s); one unit 32.5, four 27.3, eight 29.9
+//          4-bit codes, B = 64, to bf16 take 28 us by themselves, 42 back to back on buffers in turn (4.1 TB/s,
+//          3/4 of it writes; the codes' lines, two tokens of a head each, are fetched 1.4 times); by themselves, cached,
+//          25.9, one unit 32.5, four 27.3, eight 29.9
 #include <hip/hip_runtime.h>
 
 #include "bq_device.h"

@@ -373,7 +373,10 @@ typedef struct {
 } bq_kv_batch;
 
 /* Bytes of workspace bq_kv_attention needs for this call's shape (the batch's pointers are not
- * read); 0 if an argument is not valid.  It depends on the device's number of compute units. */
+ * read); 0 if an argument is not valid.  It depends on the device's number of compute units.  A call whose
+ * max_q_len is long (above 384 rows, new tokens x query heads of a key/value head; 256 for binary16, 128 for
+ * 256-wide heads) asks for num_seqs x max_kv_len keys and values expanded to 16 bits, 4 GiB (4.75 for binary16) at
+ * most: a call that would need more does without, and is several times slower.  Give max_kv_len as it is. */
 size_t bq_kv_attention_workspace_bytes(const bq_kv_cache* cache, const bq_kv_batch* batch, bq_dtype dtype,
                                        int32_t heads);
 
@@ -392,8 +395,10 @@ size_t bq_kv_attention_workspace_bytes(const bq_kv_cache* cache, const bq_kv_bat
  *   lse        [device] out, or NULL: tokens x heads binary32, the natural logarithm of
  *              sum_j exp(scale * (q_i . k_j)).
  *   workspace  [device] bq_kv_attention_workspace_bytes bytes, 256-byte aligned (NULL if that is 0).
- * Products are summed in binary32; k_attn.hip (few rows) and k_attn_chunk.hip (many) say what is rounded
- * to 16 bits on the way.
+ * Products, maxima and sums are held in binary32; k_attn.hip (few rows) and k_attn_chunk.hip (many) say what is
+ * rounded to 16 bits on the way.  Over many keys the 2-norm of the error is up to 1.2 times that of rounding the
+ * exact result to bfloat16, 1.5 times for binary16; where one key carries a row of binary16, a part in 2^11 more.
+ * Keys and values may differ in size from token to token by any power of two.
  * Results are the same on every call on one device.  Block maxima of keys that are seen must be
  * finite and at most 2^100.
  * Errors: BQ_ERR_DTYPE; BQ_ERR_SIZE (a negative count or length, num_seqs > 65535, heads, tokens * heads
