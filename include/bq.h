@@ -398,9 +398,8 @@ size_t bq_kv_attention_workspace_bytes(const bq_kv_cache* cache, const bq_kv_bat
  * Products, maxima and sums are held in binary32; k_attn.hip (few rows) and k_attn_chunk.hip (many) say what is
  * rounded to 16 bits on the way.  Over many keys the 2-norm of the error is up to 1.2 times that of rounding the
  * exact result to bfloat16, 1.5 times for binary16; where one key carries a row of binary16, a part in 2^11 more.
- * Keys and values may differ in size from token to token by any power of two.
  * Results are the same on every call on one device.  Block maxima of keys that are seen must be
- * finite and at most 2^100.
+ * finite and at most 2^100; from token to token they may differ by any factor (values below 2^-80 lose bits).
  * Errors: BQ_ERR_DTYPE; BQ_ERR_SIZE (a negative count or length, num_seqs > 65535, heads, tokens * heads
  * above INT32_MAX, more than 2^30 keys, a stride, window < 0, a scale that is not finite, kv_heads above
  * 32767, or a launch of more than 2^32 - 1 threads); BQ_ERR_WORKSPACE;

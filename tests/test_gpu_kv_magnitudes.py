@@ -182,6 +182,15 @@ def sink(gain, k):
     return plan
 
 
+def small(k, large):
+    """Values of 2^k, every other key's 2^large with a weight that much smaller."""
+    def plan(rng, n):
+        t, x = mild(rng, n), np.full(n, float(k))
+        t[1::2], x[1::2] = t[1::2] - (large - k) * np.log(2.0), large
+        return t, x
+    return plan
+
+
 def zeros_beside(k, first):
     """Half of the keys hold zeros and weigh e^6 times as much as the other half, whose values are 2^k: they
     count in the denominator only."""
@@ -208,6 +217,7 @@ PLANS = {
     "first tile 16": (700, first_tile(16)), "first tile 24": (700, first_tile(24)),
     "first tile 40": (700, first_tile(40)), "up": (700, steps(True, 0.0)), "down": (700, steps(False, 0.0)),
     "up, level": (700, steps(True, np.log(2.0))), "down, level": (700, steps(False, np.log(2.0))),
+    "small": (700, small(-78, -78)), "small beside large": (700, small(-78, 0)), "small beside 2^99": (700, small(-78, 99)),
     "zeros, then 20": (700, zeros_beside(20, True)), "zeros, then 60": (700, zeros_beside(60, True)),
     "zeros, then 99": (700, zeros_beside(99, True)), "60, then zeros": (700, zeros_beside(60, False)),
     "99, then zeros": (5000, zeros_beside(99, False)), "zeros, then 99, long": (5000, zeros_beside(99, True)),
