@@ -206,8 +206,11 @@ def kv_batch(q_start, kv_len, page_table, tokens: int, max_q_len: int, max_kv_le
     if num_seqs is None:
         num_seqs = kv_len.numel()
     if table_stride is None:
+        rows, width = page_table.shape
+        if width > 1 and page_table.stride(1) != 1 or rows > 1 and page_table.stride(0) < width:
+            raise ValueError("page_table: rows of consecutive entries, one after another (contiguous() makes them so)")
         # a table of one row may carry any stride: its length is what the row holds
-        table_stride = page_table.stride(0) if page_table.shape[0] > 1 else page_table.shape[1]
+        table_stride = page_table.stride(0) if rows > 1 else width
     return bq_kv_batch(_addr(q_start), _addr(kv_len), _addr(page_table), int(table_stride), int(tokens),
                        int(num_seqs), int(max_q_len), int(max_kv_len))
 

@@ -1,6 +1,7 @@
 """CPU tests of the plan of bq_kv_attention at the edges of its sizes: what it asks for and refuses
 before any HIP call."""
 import pytest
+import torch
 
 import dequantization_block_absmax_amd as bq
 from test_kv_boundary import attend, batch, cache
@@ -36,3 +37,20 @@ def test_the_expanded_copy_may_take_four_gib(dtype):
         return bq.bq_kv_attention_workspace_bytes(c, b, dtype, 32)
     assert 4 << 30 < need(16384) < (4 << 30) * 5 // 4 + (1 << 29)
     assert 0 < need(32768) < 1 << 30
+
+
+def test_page_tables_that_no_stride_describes():
+    """kv_batch reads the stride off the table: a transposed or an expanded one has none, and was read wrongly, or as
+    if it were empty."""
+    t = torch.zeros(3, 7, dtype=torch.int32)
+    lens = torch.zeros(3, dtype=torch.int32)
+
+    def stride(table, **kw):
+        return bq.kv_batch(lens, lens, table, 3, 1, 16, **kw).table_stride
+
+    assert stride(t) == 7 and stride(t[:, :4]) == 7 and stride(t[:, 2:]) == 7 and stride(t[::2]) == 14
+    assert stride(t[:1, :4]) == 4 and stride(t[:, :1]) == 7 and stride(t.t().contiguous().t()[:1, :1]) == 1
+    assert stride(t.t(), table_stride=5) == 5
+    for bad in (t.t(), t[:1].expand(3, 7), t[:, ::2]):
+        with pytest.raises(ValueError):
+            stride(bad)
