@@ -26,7 +26,8 @@ EXPORTS = ("bq_quantize_blockwise", "bq_dequantize_blockwise", "bq_quantize_nest
            "bq_iq1s_quantize", "bq_iq1s_dequantize", "bq_nested_workspace_bytes", "bq_status_string",
            "bq_debug_nearest_codes", "bq_last_hip_error", "bq_linear_blockwise", "bq_gemm_blockwise",
            "bq_debug_time_next_kernel", "bq_quantize_nested_noalloc", "bq_kv_write", "bq_kv_read",
-           "bq_kv_attention_workspace_bytes", "bq_kv_attention")
+           "bq_kv_attention_workspace_bytes", "bq_kv_attention", "bq_kv_append",
+           "bq_kv_tree_attention_workspace_bytes", "bq_kv_tree_attention", "bq_kv_tree_accept")
 
 
 class BQError(RuntimeError):
@@ -61,6 +62,11 @@ class bq_kv_batch(ctypes.Structure):
                 ("max_q_len", ctypes.c_int32), ("max_kv_len", ctypes.c_int32)]
 
 
+class bq_rotation(ctypes.Structure):
+    _fields_ = [("cos", ctypes.c_void_p), ("sin", ctypes.c_void_p), ("stride", ctypes.c_int64),
+                ("max_positions", ctypes.c_int64), ("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32)]
+
+
 def _load() -> ctypes.CDLL:
     if not os.path.exists(LIB_PATH):
         raise ImportError("libbq.so is not built (run: python dequantization_block_absmax_amd/build.py)")
@@ -76,6 +82,7 @@ def _load() -> ctypes.CDLL:
     tp = ctypes.POINTER(bq_code_table)
     sp = ctypes.POINTER(bq_nested_stats)
     cp, bp, f32 = ctypes.POINTER(bq_kv_cache), ctypes.POINTER(bq_kv_batch), ctypes.c_float
+    rp = ctypes.POINTER(bq_rotation)
     sig = {
         "bq_quantize_blockwise": [vp, st, i64, i32, tp, vp, vp, vp],
         "bq_dequantize_blockwise": [vp, st, i64, i32, tp, vp, vp, vp],
@@ -92,6 +99,9 @@ def _load() -> ctypes.CDLL:
         "bq_kv_write": [cp, st, vp, vp, i64, i64, i64, vp, vp],
         "bq_kv_read": [cp, st, vp, vp, i64, i64, i64, vp, vp],
         "bq_kv_attention": [cp, bp, st, vp, i64, i32, f32, i32, i32, vp, i64, vp, vp, ctypes.c_size_t, vp],
+        "bq_kv_append": [cp, rp, st, vp, vp, i64, i64, i64, vp, vp, vp, i64, i32, vp, i64, vp],
+        "bq_kv_tree_attention": [cp, bp, vp, st, vp, i64, i32, f32, i32, vp, i64, vp, vp, ctypes.c_size_t, vp],
+        "bq_kv_tree_accept": [cp, bp, vp, i64, vp, vp],
     }
     for name, args in sig.items():
         f = getattr(lib, name)
@@ -99,8 +109,9 @@ def _load() -> ctypes.CDLL:
         f.restype = st
     lib.bq_nested_workspace_bytes.argtypes = [i64, i32, i32]
     lib.bq_nested_workspace_bytes.restype = ctypes.c_size_t
-    lib.bq_kv_attention_workspace_bytes.argtypes = [cp, bp, st, i32]
-    lib.bq_kv_attention_workspace_bytes.restype = ctypes.c_size_t
+    for f in (lib.bq_kv_attention_workspace_bytes, lib.bq_kv_tree_attention_workspace_bytes):
+        f.argtypes = [cp, bp, st, i32]
+        f.restype = ctypes.c_size_t
     lib.bq_debug_nearest_codes.argtypes = [tp, vp, i64, vp, vp, vp]
     lib.bq_debug_nearest_codes.restype = st
     lib.bq_debug_time_next_kernel.argtypes = [vp, vp]
@@ -215,6 +226,24 @@ def kv_batch(q_start, kv_len, page_table, tokens: int, max_q_len: int, max_kv_le
                        int(num_seqs), int(max_q_len), int(max_kv_len))
 
 
+def rotation(cos, sin, rotary_dim: int, interleaved: bool = False, max_positions: int | None = None,
+             stride: int | None = None) -> bq_rotation:
+    """A bq_rotation over the caller's tables of cosines and sines, one row of rotary_dim / 2 for each
+    position; the number of positions and the stride are read off the tensors where not given."""
+    if max_positions is None or stride is None:
+        for t in (cos, sin):
+            if t.dim() != 2 or t.shape != cos.shape or t.shape[1] < rotary_dim // 2 or str(t.dtype) != "torch.float32":
+                raise ValueError("rotation: cos and sin are binary32 tables of positions x at least rotary_dim / 2")
+            if t.shape[1] > 1 and t.stride(1) != 1 or t.shape[0] > 1 and (t.stride(0) < t.shape[1] or
+                                                                          t.stride(0) != cos.stride(0)):
+                raise ValueError("rotation: rows of consecutive entries, with one stride for both tables")
+        if max_positions is None:
+            max_positions = cos.shape[0]
+        if stride is None:  # a table of one row may carry any stride
+            stride = cos.stride(0) if cos.shape[0] > 1 else (cos.shape[1] + 3) // 4 * 4
+    return bq_rotation(_addr(cos), _addr(sin), int(stride), int(max_positions), int(rotary_dim), int(interleaved))
+
+
 # ---- entry points (same names as the C ABI; each returns the bq_status) -----------------
 
 def bq_quantize_blockwise(inp, dtype, n: int, blocksize: int, table, absmax, packed, stream=None) -> int:
@@ -311,6 +340,34 @@ def bq_kv_attention(cache: bq_kv_cache | None, batch: bq_kv_batch | None, dtype,
     return _lib.bq_kv_attention(cache, batch, dtype_code(dtype), _addr(q), int(q_stride),
                                 int(heads), float(scale), int(causal), int(window), _addr(out), int(out_stride),
                                 _addr(lse), _addr(workspace), int(workspace_bytes), _stream(stream))
+
+
+def bq_kv_append(cache: bq_kv_cache | None, rotation: bq_rotation | None, dtype, k, v, tokens: int, k_stride: int,
+                 v_stride: int, positions, slots, q=None, q_stride: int = 0, heads: int = 0, q_out=None,
+                 q_out_stride: int = 0, stream=None) -> int:
+    return _lib.bq_kv_append(cache, rotation, dtype_code(dtype), _addr(k), _addr(v), int(tokens), int(k_stride),
+                             int(v_stride), _addr(positions), _addr(slots), _addr(q), int(q_stride), int(heads),
+                             _addr(q_out), int(q_out_stride), _stream(stream))
+
+
+def bq_kv_tree_attention_workspace_bytes(cache: bq_kv_cache | None, batch: bq_kv_batch | None, dtype, heads: int) -> int:
+    return int(_lib.bq_kv_tree_attention_workspace_bytes(cache, batch, dtype_code(dtype), int(heads)))
+
+
+def bq_kv_tree_attention(cache: bq_kv_cache | None, batch: bq_kv_batch | None, parents, dtype, q, q_stride: int,
+                         heads: int, scale: float, window: int, out, out_stride: int, lse=None, workspace=None,
+                         workspace_bytes: int | None = None, stream=None) -> int:
+    if workspace_bytes is None:
+        workspace_bytes = 0 if workspace is None or isinstance(workspace, int) else \
+            workspace.numel() * workspace.element_size()
+    return _lib.bq_kv_tree_attention(cache, batch, _addr(parents), dtype_code(dtype), _addr(q), int(q_stride),
+                                     int(heads), float(scale), int(window), _addr(out), int(out_stride), _addr(lse),
+                                     _addr(workspace), int(workspace_bytes), _stream(stream))
+
+
+def bq_kv_tree_accept(cache: bq_kv_cache | None, batch: bq_kv_batch | None, path, path_stride: int, path_len,
+                      stream=None) -> int:
+    return _lib.bq_kv_tree_accept(cache, batch, _addr(path), int(path_stride), _addr(path_len), _stream(stream))
 
 
 def bq_nested_workspace_bytes(n: int, blocksize: int, blocksize2: int = 256) -> int:

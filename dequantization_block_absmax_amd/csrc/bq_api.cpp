@@ -127,7 +127,7 @@ const char* bq_status_string(bq_status s) {
     case BQ_ERR_BLOCKSIZE: return "block size must be a power of two in [32, 4096]";
     case BQ_ERR_TABLE: return "invalid code table";
     case BQ_ERR_ALIGNMENT: return "misaligned device pointer";
-    case BQ_ERR_FORMAT: return "unknown block format, row length, page size or head size";
+    case BQ_ERR_FORMAT: return "unknown block format, row length, page size, head size or rotary size";
     case BQ_ERR_WORKSPACE: return "workspace missing or too small";
     case BQ_ERR_HIP: return "HIP launch failed";
   }
@@ -452,6 +452,100 @@ bq_status bq_kv_read(const bq_kv_cache* cache, bq_dtype dtype, void* k, void* v,
   return hip_status(bq::launch_kv_read(ca, dtype, k, v, tokens, k_stride, v_stride, slots, a, stream));
 }
 
+static bq_status check_rotation(const bq_rotation* r, const bq_kv_cache* c) {
+  if (r == nullptr) return BQ_ERR_NULL;
+  if (r->rotary_dim < 16 || r->rotary_dim % 16 != 0 || r->rotary_dim > c->head_dim) return BQ_ERR_FORMAT;
+  // the last row's byte offset fits 62 bits
+  if (r->max_positions < 1 || r->stride < r->rotary_dim / 2 || r->stride > ((int64_t)1 << 59) / r->max_positions)
+    return BQ_ERR_SIZE;
+  return BQ_OK;
+}
+
+bq_status bq_kv_append(const bq_kv_cache* cache, const bq_rotation* rotation, bq_dtype dtype, const void* k,
+                       const void* v, int64_t tokens, int64_t k_stride, int64_t v_stride, const int64_t* positions,
+                       const int64_t* slots, const void* q, int64_t q_stride, int32_t heads, void* q_out,
+                       int64_t q_out_stride, hipStream_t stream) {
+  Tables t;
+  bq::KvAppendArgs a;
+  memset(&a, 0, sizeof(a));
+  bq_status st = check_kv_rows(cache, dtype, k, v, tokens, k_stride, v_stride, slots, &t.data, &a.cache);
+  if (st != BQ_OK) return st;
+  st = check_rotation(rotation, cache);
+  if (st != BQ_OK) return st;
+  const int64_t size = dtype == BQ_F32 ? 4 : 2;
+  if (q != nullptr) {
+    if (heads < 1 || (int64_t)heads * cache->head_dim >= (int64_t)1 << 34) return BQ_ERR_SIZE;
+    const int64_t row = (int64_t)heads * cache->head_dim;
+    if (tokens > (((int64_t)1 << 34) - 1) / row) return BQ_ERR_SIZE;
+    const int64_t most = tokens > 1 ? ((int64_t)1 << 60) / tokens : (int64_t)1 << 60;
+    if (q_stride < row || q_out_stride < row || q_stride > most || q_out_stride > most) return BQ_ERR_SIZE;
+    if (q == q_out && q_stride != q_out_stride) return BQ_ERR_SIZE;  // neither in place nor apart
+  }
+  if (tokens == 0) return BQ_OK;
+  if (positions == nullptr || rotation->cos == nullptr || rotation->sin == nullptr || (q != nullptr && q_out == nullptr))
+    return BQ_ERR_NULL;
+  if (!aligned(positions, 8) || !aligned(rotation->cos, 16) || !aligned(rotation->sin, 16) || rotation->stride % 4 != 0)
+    return BQ_ERR_ALIGNMENT;
+  if (q != nullptr && (!aligned(q, 16) || !aligned(q_out, 16) || (q_stride * size) % 16 != 0 || (q_out_stride * size) % 16 != 0))
+    return BQ_ERR_ALIGNMENT;
+  a.k = k;
+  a.v = v;
+  a.tokens = tokens;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.positions = positions;
+  a.slots = slots;
+  a.cos = rotation->cos;
+  a.sin = rotation->sin;
+  a.angle_stride = rotation->stride;
+  a.max_positions = rotation->max_positions;
+  a.rotary_dim = rotation->rotary_dim;
+  a.interleaved = rotation->interleaved != 0;
+  if (q != nullptr) {
+    a.q = q;
+    a.q_stride = q_stride;
+    a.q_out = q_out;
+    a.q_out_stride = q_out_stride;
+    a.heads = heads;
+  }
+  return hip_status(bq::launch_kv_append(a, dtype, t.data, stream));
+}
+
+bq_status bq_kv_tree_accept(const bq_kv_cache* cache, const bq_kv_batch* b, const int32_t* path, int64_t path_stride,
+                            const int32_t* path_len, hipStream_t stream) {
+  Tables t;
+  bq::KvAcceptArgs a;
+  memset(&a, 0, sizeof(a));
+  const bq_status st = check_cache(cache, &t.data, &a.cache);
+  if (st != BQ_OK) return st;
+  if (b == nullptr) return BQ_ERR_NULL;
+  if (b->num_seqs < 0 || b->num_seqs > 65535 || b->tokens < 0 || b->tokens > INT32_MAX || b->table_stride < 0 ||
+      b->table_stride > INT32_MAX || b->max_q_len < 0 || b->max_kv_len < 0 || path_stride < 0 || path_stride > INT32_MAX ||
+      cache->kv_heads > 1 << 20)
+    return BQ_ERR_SIZE;
+  if (b->num_seqs == 0 || b->tokens == 0) return BQ_OK;
+  const bq_status pt = check_cache_pointers(cache);
+  if (pt == BQ_ERR_NULL || b->q_start == nullptr || b->kv_len == nullptr || b->page_table == nullptr || path == nullptr ||
+      path_len == nullptr)
+    return BQ_ERR_NULL;
+  if (pt != BQ_OK || !aligned(b->q_start, 4) || !aligned(b->kv_len, 4) || !aligned(b->page_table, 4) || !aligned(path, 4) ||
+      !aligned(path_len, 4))
+    return BQ_ERR_ALIGNMENT;
+  a.q_start = b->q_start;
+  a.kv_len = b->kv_len;
+  a.page_table = b->page_table;
+  a.table_stride = b->table_stride;
+  a.tokens = b->tokens;
+  a.num_seqs = b->num_seqs;
+  const int64_t held = b->table_stride * cache->page_size;
+  a.max_kv_len = held < b->max_kv_len ? (int32_t)held : b->max_kv_len;
+  a.path = path;
+  a.path_stride = path_stride;
+  a.path_len = path_len;
+  a.bits = t.data.K == 16 ? 4 : 8;
+  return hip_status(bq::launch_kv_accept(a, stream));
+}
+
 // Shape of an attention call; fills everything of `a` but the data pointers.
 static bq_status check_attention_shape(const bq_kv_cache* cache, const bq_kv_batch* b, bq_dtype dtype, int32_t heads,
                                        bq::PreparedTable* t, bq::KvAttendArgs* a) {
@@ -488,19 +582,18 @@ size_t bq_kv_attention_workspace_bytes(const bq_kv_cache* cache, const bq_kv_bat
   return bq::kv_attend_workspace(a, dtype);
 }
 
-bq_status bq_kv_attention(const bq_kv_cache* cache, const bq_kv_batch* batch, bq_dtype dtype, const void* q,
-                          int64_t q_stride, int32_t heads, float scale, int32_t causal, int32_t window, void* out,
-                          int64_t out_stride, float* lse, void* workspace, size_t workspace_bytes,
-                          hipStream_t stream) {
-  Tables t;
-  bq::KvAttendArgs a;
-  const bq_status st = check_attention_shape(cache, batch, dtype, heads, &t.data, &a);
-  if (st != BQ_OK) return st;
+// What bq_kv_attention and bq_kv_tree_attention check and fill in alike, of a call whose shape is valid.  *done: nothing
+// to enqueue.
+static bq_status check_attention_call(const bq_kv_cache* cache, const bq_kv_batch* batch, const void* q, int64_t q_stride,
+                                      int32_t heads, float scale, int32_t window, void* out, int64_t out_stride, float* lse,
+                                      bq::KvAttendArgs* a, bool* done) {
   const int64_t row = (int64_t)heads * cache->head_dim;
   const int64_t most = (int64_t)1 << 29;  // rows number less than 2^31: byte offsets fit 62 bits
+  *done = false;
   if (q_stride < row || out_stride < row || q_stride > most || out_stride > most || window < 0 || !isfinite(scale))
     return BQ_ERR_SIZE;
-  if (a.tokens == 0 || a.num_seqs == 0 || a.max_q_len == 0) return BQ_OK;
+  *done = a->tokens == 0 || a->num_seqs == 0 || a->max_q_len == 0;
+  if (*done) return BQ_OK;
   const bq_status pt = check_cache_pointers(cache);
   if (pt == BQ_ERR_NULL || q == nullptr || out == nullptr || batch->q_start == nullptr || batch->kv_len == nullptr ||
       batch->page_table == nullptr)
@@ -508,28 +601,83 @@ bq_status bq_kv_attention(const bq_kv_cache* cache, const bq_kv_batch* batch, bq
   if (pt != BQ_OK || !aligned(q, 16) || !aligned(out, 16) || q_stride % 8 != 0 || out_stride % 8 != 0 ||
       !aligned(batch->q_start, 4) || !aligned(batch->kv_len, 4) || !aligned(batch->page_table, 4) || !aligned(lse, 4))
     return BQ_ERR_ALIGNMENT;
-  const size_t need = bq::kv_attend_workspace(a, dtype);
-  if (need > 0) {
-    if (workspace == nullptr || workspace_bytes < need) return BQ_ERR_WORKSPACE;
-    if (!aligned(workspace, 256)) return BQ_ERR_ALIGNMENT;
-  }
-  a.q_start = batch->q_start;
-  a.kv_len = batch->kv_len;
-  a.page_table = batch->page_table;
-  a.q = q;
-  a.q_stride = q_stride;
-  a.out = out;
-  a.out_stride = out_stride;
-  a.lse = lse;
-  a.causal = causal != 0;
-  a.window = window;
-  a.scale = scale;
-  a.workspace = workspace;
+  a->q_start = batch->q_start;
+  a->kv_len = batch->kv_len;
+  a->page_table = batch->page_table;
+  a->q = q;
+  a->q_stride = q_stride;
+  a->out = out;
+  a->out_stride = out_stride;
+  a->lse = lse;
+  a->window = window;
+  a->scale = scale;
+  return BQ_OK;
+}
+
+static bq_status check_workspace(size_t need, void* workspace, size_t workspace_bytes) {
+  if (need == 0) return BQ_OK;
+  if (workspace == nullptr || workspace_bytes < need) return BQ_ERR_WORKSPACE;
+  return aligned(workspace, 256) ? BQ_OK : BQ_ERR_ALIGNMENT;
+}
+
+static bq::DequantArgs dequant_args(const bq::PreparedTable& t) {
   bq::DequantArgs da;
   memset(&da, 0, sizeof(da));
-  memcpy(da.c, t.data.c, sizeof(float) * t.data.K);
-  da.K = t.data.K;
-  return hip_status(bq::launch_kv_attend(a, dtype, da, stream));
+  memcpy(da.c, t.c, sizeof(float) * t.K);
+  da.K = t.K;
+  return da;
+}
+
+bq_status bq_kv_attention(const bq_kv_cache* cache, const bq_kv_batch* batch, bq_dtype dtype, const void* q,
+                          int64_t q_stride, int32_t heads, float scale, int32_t causal, int32_t window, void* out,
+                          int64_t out_stride, float* lse, void* workspace, size_t workspace_bytes,
+                          hipStream_t stream) {
+  Tables t;
+  bq::KvAttendArgs a;
+  bool done;
+  bq_status st = check_attention_shape(cache, batch, dtype, heads, &t.data, &a);
+  if (st != BQ_OK) return st;
+  st = check_attention_call(cache, batch, q, q_stride, heads, scale, window, out, out_stride, lse, &a, &done);
+  if (st != BQ_OK || done) return st;
+  st = check_workspace(bq::kv_attend_workspace(a, dtype), workspace, workspace_bytes);
+  if (st != BQ_OK) return st;
+  a.causal = causal != 0;
+  a.workspace = workspace;
+  return hip_status(bq::launch_kv_attend(a, dtype, dequant_args(t.data), stream));
+}
+
+// A tree's words and its lanes' paths have room for so many tokens.
+static bool tree_fits(const bq_kv_batch* b) { return b->max_q_len <= bq::kMostNodes; }
+
+size_t bq_kv_tree_attention_workspace_bytes(const bq_kv_cache* cache, const bq_kv_batch* batch, bq_dtype dtype,
+                                            int32_t heads) {
+  Tables t;
+  bq::KvAttendArgs a;
+  if (check_attention_shape(cache, batch, dtype, heads, &t.data, &a) != BQ_OK || !tree_fits(batch)) return 0;
+  if (a.tokens == 0 || a.num_seqs == 0 || a.max_q_len == 0) return 0;
+  return bq::kv_tree_workspace(a, dtype);
+}
+
+bq_status bq_kv_tree_attention(const bq_kv_cache* cache, const bq_kv_batch* batch, const int32_t* parents,
+                               bq_dtype dtype, const void* q, int64_t q_stride, int32_t heads, float scale,
+                               int32_t window, void* out, int64_t out_stride, float* lse, void* workspace,
+                               size_t workspace_bytes, hipStream_t stream) {
+  Tables t;
+  bq::KvAttendArgs a;
+  bool done;
+  bq_status st = check_attention_shape(cache, batch, dtype, heads, &t.data, &a);
+  if (st != BQ_OK) return st;
+  if (!tree_fits(batch)) return BQ_ERR_SIZE;
+  st = check_attention_call(cache, batch, q, q_stride, heads, scale, window, out, out_stride, lse, &a, &done);
+  if (st != BQ_OK || done) return st;
+  if (parents == nullptr) return BQ_ERR_NULL;
+  if (!aligned(parents, 4)) return BQ_ERR_ALIGNMENT;
+  st = check_workspace(bq::kv_tree_workspace(a, dtype), workspace, workspace_bytes);
+  if (st != BQ_OK) return st;
+  a.parents = parents;
+  a.causal = 1;
+  a.workspace = workspace;
+  return hip_status(bq::launch_kv_tree(a, dtype, dequant_args(t.data), stream));
 }
 
 }  // extern "C"

@@ -107,6 +107,12 @@ __device__ __forceinline__ int end_key(const KvAttendArgs& aa, const Sequence& s
   return aa.causal ? max(min(s.kv, s.kv - s.nq + i + 1), 0) : s.kv;
 }
 
+// The first key of the context that a new token of a tree at this depth sees.
+__device__ __forceinline__ int node_first(const KvAttendArgs& aa, int context, int depth) {
+  const int pos = context + depth;
+  return aa.window > 0 && pos >= aa.window ? pos - aa.window + 1 : 0;
+}
+
 // Partial results of a row over one split of its keys, relative to the reference exponent m:
 // sum of weights l and the weighted sum of values (head_dim binary32), kept in the workspace.  l is the
 // sum that belongs to the weighted one, of weights as they were rounded; `exact`, for lse, that of the

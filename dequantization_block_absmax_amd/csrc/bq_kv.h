@@ -22,10 +22,42 @@ int launch_kv_write(const KvCacheArgs& c, int dtype, const void* k, const void* 
 int launch_kv_read(const KvCacheArgs& c, int dtype, void* k, void* v, int64_t tokens, int64_t k_stride,
                    int64_t v_stride, const int64_t* slots, const DequantArgs& da, void* stream);
 
+
+// Appending with the rotation by position (k_kv_append.hip).
+struct KvAppendArgs {
+  KvCacheArgs cache;
+  const void *k, *v;
+  int64_t tokens, k_stride, v_stride;  // strides in elements
+  const int64_t *positions, *slots;
+  const float *cos, *sin;
+  int64_t angle_stride, max_positions;
+  int32_t rotary_dim, interleaved;
+  const void* q;  // or NULL
+  int64_t q_stride;
+  void* q_out;
+  int64_t q_out_stride;
+  int32_t heads;
+};
+int launch_kv_append(const KvAppendArgs& a, int dtype, const PreparedTable& t, void* stream);
+
+// Moving the accepted path of a tree of drafted tokens to the front of its draft (k_kv_accept.hip).
+struct KvAcceptArgs {
+  KvCacheArgs cache;
+  const int32_t *q_start, *kv_len, *page_table;
+  int64_t table_stride, tokens;
+  int32_t num_seqs, max_kv_len;
+  const int32_t* path;
+  int64_t path_stride;
+  const int32_t* path_len;
+  int32_t bits;
+};
+int launch_kv_accept(const KvAcceptArgs& a, void* stream);
+
 // Attention over the cache (k_attn.hip).
 struct KvAttendArgs {
   KvCacheArgs cache;
   const int32_t *q_start, *kv_len, *page_table;
+  const int32_t* parents;  // of new tokens that are a tree, else NULL
   int64_t table_stride, tokens;
   int32_t num_seqs, max_q_len, max_kv_len;
   const void* q;
@@ -41,6 +73,10 @@ struct KvAttendArgs {
 // Bytes of workspace the launch needs (no device is touched beyond its CU count).
 size_t kv_attend_workspace(const KvAttendArgs& a, int dtype);
 int launch_kv_attend(const KvAttendArgs& a, int dtype, const DequantArgs& da, void* stream);
+// Attention of a tree of new tokens (k_tree.hip), at most kMostNodes to a sequence.
+constexpr int kMostNodes = 256;
+size_t kv_tree_workspace(const KvAttendArgs& a, int dtype);
+int launch_kv_tree(const KvAttendArgs& a, int dtype, const DequantArgs& da, void* stream);
 // Joins the partial results of splits of the keys (k_attn_merge.hip): [0] those of sequences with few
 // rows, [1] with many; nsplit <= 1: nothing to join.  Not both: every sequence is of `kind`.
 struct MergeArgs {

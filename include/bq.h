@@ -65,9 +65,9 @@ typedef enum {
   BQ_ERR_TABLE = 5,     /* code table: size, order, range or spacing (see bq_code_table) */
   BQ_ERR_ALIGNMENT = 6, /* a device pointer is not aligned as required */
   BQ_ERR_FORMAT = 7,    /* unknown bq_q32_format, row_len not a multiple of 32 (of 256 for
-                           the IQ2_XS- and IQ1_S-style calls), or page_size or head_dim of a cache */
+                           the IQ2_XS- and IQ1_S-style calls), page_size or head_dim of a cache, or rotary_dim */
   BQ_ERR_WORKSPACE = 8, /* workspace missing or smaller than bq_nested_workspace_bytes or
-                           bq_kv_attention_workspace_bytes */
+                           bq_kv_attention_workspace_bytes (bq_kv_tree_attention_workspace_bytes) */
   BQ_ERR_HIP = 9        /* the HIP runtime rejected a launch */
 } bq_status;
 
@@ -395,7 +395,7 @@ size_t bq_kv_attention_workspace_bytes(const bq_kv_cache* cache, const bq_kv_bat
  *   lse        [device] out, or NULL: tokens x heads binary32, the natural logarithm of
  *              sum_j exp(scale * (q_i . k_j)).
  *   workspace  [device] bq_kv_attention_workspace_bytes bytes, 256-byte aligned (NULL if that is 0).
- * Products, maxima and sums are held in binary32; k_attn.hip (few rows) and k_attn_chunk.hip (many) say what is
+ * Products, maxima and sums are held in binary32; bq_attend.h (few rows) and k_attn_chunk.hip (many) say what is
  * rounded to 16 bits on the way.  Over many keys the 2-norm of the error is up to 1.2 times that of rounding the
  * exact result to bfloat16, 1.5 times for binary16; where one key carries a row of binary16, a part in 2^11 more.
  * Results are the same on every call on one device.  Block maxima of keys that are seen must be
@@ -408,6 +408,86 @@ bq_status bq_kv_attention(const bq_kv_cache* cache, const bq_kv_batch* batch, bq
                           int64_t q_stride, int32_t heads, float scale, int32_t causal, int32_t window, void* out,
                           int64_t out_stride, float* lse, void* workspace, size_t workspace_bytes,
                           hipStream_t stream);
+
+/* ---- Drafted tokens over the cache -----------------------------------------------------------
+ *
+ * A server that drafts several continuations of a sequence at once, as a tree, and verifies them in one
+ * step: bq_kv_append puts the draft's keys and values into the cache, keys (and queries) rotated to their
+ * positions; bq_kv_tree_attention attends over context and draft; bq_kv_tree_accept moves the accepted
+ * path to the front of the draft, where the next one follows it. */
+
+/* Rotation by position.  Pair i of a head, i < rotary_dim / 2, of a token at position t is turned by the
+ * angle whose cosine and sine are cos[t * stride + i] and sin[t * stride + i]:
+ *     (x, y) -> (fl32(fl32(x cos) - fl32(y sin)), fl32(fl32(y cos) + fl32(x sin)))
+ * in binary32, every operation rounded once.  Pair i is elements i and i + rotary_dim / 2, or, if
+ * `interleaved` is nonzero, elements 2 i and 2 i + 1; elements from rotary_dim on stay as they are. */
+typedef struct {
+  const float* cos;      /* [device] max_positions rows, 16-byte aligned */
+  const float* sin;      /* [device] likewise */
+  int64_t stride;        /* elements from one position's row to the next: at least rotary_dim / 2, a multiple of 4 */
+  int64_t max_positions;
+  int32_t rotary_dim;    /* a multiple of 16 from 16 to head_dim */
+  int32_t interleaved;
+} bq_rotation;
+
+/* bq_kv_write with the rotation on the way: the codes and maxima of the keys are those of the rotated
+ * binary32 values (not rounded to `dtype` in between), bit for bit; values are written as by bq_kv_write.
+ * In the same launch the tokens' queries are rotated, each element rounded once to `dtype`.
+ *   k, v, k_stride, v_stride, slots
+ *              as in bq_kv_write.
+ *   positions  [device] one position per token, 8-byte aligned, in any order, repeats allowed (tokens of one
+ *              depth of a tree).  A token whose position is outside [0, max_positions) is left out: nothing
+ *              of it is written, to the cache or to q_out.
+ *   q          [device] tokens rows of heads * head_dim elements of `dtype`, 16-byte aligned, or NULL: no
+ *              queries (heads, the strides and q_out are not looked at then).
+ *   heads      at least 1; tokens * heads * head_dim < 2^34.
+ *   q_out      [device] out: rows as in q, with q_out_stride; q itself (with its stride) rotates in place.  A
+ *              token whose slot is outside the pool has its queries rotated all the same.
+ * q_out overlaps none of the inputs but q, and that not in part.
+ * Errors: as bq_kv_write, and BQ_ERR_FORMAT (rotary_dim), BQ_ERR_SIZE (max_positions below 1, a stride too
+ * short, heads, q_out == q with another stride). */
+bq_status bq_kv_append(const bq_kv_cache* cache, const bq_rotation* rotation, bq_dtype dtype, const void* k,
+                       const void* v, int64_t tokens, int64_t k_stride, int64_t v_stride, const int64_t* positions,
+                       const int64_t* slots, const void* q, int64_t q_stride, int32_t heads, void* q_out,
+                       int64_t q_out_stride, hipStream_t stream);
+
+/* Bytes of workspace bq_kv_tree_attention needs for this call's shape (the batch's pointers are not read); 0
+ * if an argument is not valid.  It depends on the device's number of compute units. */
+size_t bq_kv_tree_attention_workspace_bytes(const bq_kv_cache* cache, const bq_kv_batch* batch, bq_dtype dtype,
+                                            int32_t heads);
+
+/* bq_kv_attention for new tokens that are a tree.  New token i of a sequence's n (its key in place
+ * kv_len - n + i, like theirs in bq_kv_attention) has a parent among those before it, or follows the context, the
+ * kv_len - n keys before the draft.  It stands at position kv_len - n + depth, its depth the number of its
+ * ancestors in the draft, and sees the context, its ancestors and itself; of these, if window > 0, those
+ * at positions above its own minus window.
+ *   parents    [device] one per row of q, 4-byte aligned: the number (0 .. i - 1) of the parent among the
+ *              sequence's new tokens, or -1: it follows the context.  Any other number marks an unused place:
+ *              that token and all that descend from it see no key and give zeros, and -infinity in lse.  What
+ *              is cached in an unused place does not matter (it may be NaN).
+ *   batch      max_q_len at most 256.
+ * Everything else, the rounding and the errors are as in bq_kv_attention; the workspace is that of
+ * bq_kv_tree_attention_workspace_bytes. */
+bq_status bq_kv_tree_attention(const bq_kv_cache* cache, const bq_kv_batch* batch, const int32_t* parents,
+                               bq_dtype dtype, const void* q, int64_t q_stride, int32_t heads, float scale,
+                               int32_t window, void* out, int64_t out_stride, float* lse, void* workspace,
+                               size_t workspace_bytes, hipStream_t stream);
+
+/* Keeps the accepted path of each sequence's draft: the cached keys and values of its new token path[i] move to the
+ * place of new token i, codes and maxima as they are (along a path, position and depth agree, so rotated keys stay
+ * right).  With m accepted tokens the sequence's length is then kv_len - n + m: the caller's to set.  Places of
+ * the draft from m on keep what they held.
+ *   batch      as of the tree attention (q_start, kv_len, page_table; any max_q_len).
+ *   path       [device] num_seqs rows of numbers of new tokens, 4-byte aligned, strictly ascending (0 <= path[i] < n);
+ *              at an entry that is not, the row ends.
+ *   path_stride  entries from one row to the next, at least 0 (0: one row for all).
+ *   path_len   [device] num_seqs, 4-byte aligned: entries of each row, read as at most the sequence's new tokens.
+ * A token whose place, old or new, is on a page outside the pool is not moved.  No two sequences share a page of
+ * their drafts.
+ * Errors: as bq_kv_write (of the batch: a negative count or length, num_seqs > 65535, kv_heads above 2^20).  tokens or
+ * num_seqs of 0 enqueue nothing. */
+bq_status bq_kv_tree_accept(const bq_kv_cache* cache, const bq_kv_batch* batch, const int32_t* path,
+                            int64_t path_stride, const int32_t* path_len, hipStream_t stream);
 
 /* The hipError_t (as int) of the most recent launch that failed on the calling thread with
  * BQ_ERR_HIP, or 0 if none has. */
