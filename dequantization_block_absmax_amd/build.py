@@ -27,7 +27,7 @@ DEVICE = ["--offload-arch=" + ARCH, "-Xclang", "-target-feature", "-Xclang", "-p
 SOURCES = ["bq_api.cpp", "bq_table.cpp", "k_quant.hip", "k_dequant.hip", "k_nested.hip", "k_q32.hip",
            "k_linear.hip", "k_gemm.hip", "k_scratch.hip", "k_iq2xs.hip",
            "k_iq1s.hip", "k_kv.hip", "k_attn.hip", "k_attn_merge.hip", "k_attn_chunk.hip", "k_kv_append.hip", "k_kv_accept.hip",
-           "k_tree.hip"]
+           "k_tree.hip", "k_tree_few.hip"]
 
 
 def _cmd(src: str, obj: str) -> list[str]:

@@ -338,6 +338,53 @@ struct TreeShared {
 };
 struct NoTree {};
 
+// Fills the shared tree of a tile with the new tokens i_first .. i_last; `parent` is token tid's.  The last 256 threads, each
+// with a token of its own, follow its path to the root.  Every thread takes part; a barrier has to follow.
+template <int THREADS, int ROWS>
+__device__ __forceinline__ void read_tree(const KvAttendArgs& aa, TreeShared<ROWS>& tree, int parent, int tid, int i_first,
+                                          int i_last) {
+  if (tid < kMostNodes) tree.parent[tid] = (int16_t)(parent >= -1 && parent < tid ? parent : -2);
+  if (tid < kTreeWords) tree.used[tid] = 0;
+  __syncthreads();
+  const int node = tid - (THREADS - kMostNodes);  // whole waves
+  if (node < 0) return;
+  const bool mine = node >= i_first && node <= i_last;
+  uint32_t* const seen = tree.seen[mine ? node - i_first : 0];
+  int at = node, depth = 0, word = node >> 5;
+  uint32_t bits = 0;
+  if (mine)
+    for (int k = 0; k < kTreeWords; ++k) seen[k] = 0;
+  if (node <= i_last)
+    for (int n = 0; n < kMostNodes; ++n) {  // ancestors come in descending order: a word is done when another begins
+      if (at >> 5 != word) {
+        if (mine) seen[word + 1] = bits;
+        word = at >> 5;
+        bits = 0;
+      }
+      if (aa.window == 0 || depth < aa.window) bits |= 1u << (at & 31);
+      at = tree.parent[at];
+      if (at < 0) break;
+      ++depth;
+    }
+  const bool sees = node <= i_last && at == -1;
+  if (mine) {
+    seen[word + 1] = bits;
+    tree.depth[node - i_first] = sees ? depth : -1;
+    if (!sees)
+      for (int k = 0; k < kTreeWords; ++k) seen[k] = 0;
+  }
+  const uint64_t all = __ballot(sees);
+  if ((node & 31) == 0) tree.used[(node >> 5) + 1] = (uint32_t)(all >> (node & 63));
+}
+
+// Whether any of these tokens sees anything (the same in every lane).
+template <int ROWS>
+__device__ __forceinline__ bool any_node(const TreeShared<ROWS>& tree, int i_first, int i_last) {
+  uint32_t any = 0;  // tokens past i_last are not marked
+  for (int k = i_first >> 5; k <= i_last >> 5; ++k) any |= tree.used[k + 1] & (k == i_first >> 5 ? ~0u << (i_first & 31) : ~0u);
+  return __builtin_amdgcn_readfirstlane(any) != 0;
+}
+
 // TREE: the new tokens are a tree (aa.parents).  Token i sees the context (the keys before the new tokens), itself and
 // the tokens on its path from the root, by its depth within the window.  The words are worked out once for a tile, beside
 // the first loads, each token's path by a lane of its own; they are looked at for the groups that reach past the
@@ -495,46 +542,7 @@ __global__ __launch_bounds__((64 * Occupancy<D, NB, KB, RT>::kWaves), (Occupancy
       *reinterpret_cast<u32x4*>(s_mem + tid * kEntryBytes + ((i + tid) & (kEntryBytes / 16 - 1)) * 16) = e4;
   }
   const uint32_t copy = (lane * O::kCopyBytes) & (kEntryBytes - 1);
-  if constexpr (TREE) {
-    if (tid < kMostNodes) s_tree.parent[tid] = (int16_t)(parent >= -1 && parent < tid ? parent : -2);
-    if (tid < kTreeWords) s_tree.used[tid] = 0;
-    __syncthreads();
-    // the last waves, the first have the queries; whole waves
-    const int node = tid - (kThreads - kMostNodes);
-    if (node >= 0) {
-      uint32_t* const seen = s_tree.seen[min(max(node - i_first, 0), kRows - 1)];
-      const bool mine = node >= i_first && node <= i_last;
-      int at = node, depth = 0, word = node >> 5;
-      uint32_t bits = 0;
-      if (mine)
-        for (int k = 0; k < kTreeWords; ++k) seen[k] = 0;
-      if (node <= i_last)
-        while (true) {  // ancestors come in descending order, so that a word is done when another begins
-          if (at >> 5 != word) {
-            if (mine) seen[word + 1] = bits;
-            word = at >> 5;
-            bits = 0;
-          }
-          if (aa.window == 0 || depth < aa.window) bits |= 1u << (at & 31);
-          const int up = s_tree.parent[at];
-          if (up < 0) {
-            at = up;
-            break;
-          }
-          at = up;
-          ++depth;
-        }
-      const bool sees = node <= i_last && at == -1;
-      if (mine) {
-        seen[word + 1] = bits;
-        s_tree.depth[node - i_first] = sees ? depth : -1;
-        if (!sees)
-          for (int k = 0; k < kTreeWords; ++k) seen[k] = 0;
-      }
-      const uint64_t all = __ballot(sees);
-      if ((lane & 31) == 0) s_tree.used[(node >> 5) + 1] = (uint32_t)(all >> lane);
-    }
-  }
+  if constexpr (TREE) read_tree<kThreads, kRows>(aa, s_tree, parent, tid, i_first, i_last);
 
   // Queries: wave t sets up the 16 rows of tile t, as the products' operands and a scale per row.
   f16x8* const s_q = reinterpret_cast<f16x8*>(s_mem + kLut);
@@ -587,11 +595,7 @@ __global__ __launch_bounds__((64 * Occupancy<D, NB, KB, RT>::kWaves), (Occupancy
   }
   __syncthreads();  // table and queries are in place
   if constexpr (TREE) {
-    // no row of the tile sees any key: theirs may hold anything
-    uint32_t any = 0;
-    for (int k = i_first >> 5; k <= i_last >> 5; ++k)
-      any |= s_tree.used[k + 1] & (k == i_first >> 5 ? ~0u << (i_first & 31) : ~0u);
-    if (__builtin_amdgcn_readfirstlane(any) == 0) end = hi_all = 0;
+    if (!any_node(s_tree, i_first, i_last)) end = hi_all = 0;  // no row of the tile sees any key: theirs may hold anything
   }
 
   // Rows of this lane (column m of the products): the keys they see, their scales.

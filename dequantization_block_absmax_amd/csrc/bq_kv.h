@@ -73,8 +73,11 @@ struct KvAttendArgs {
 // Bytes of workspace the launch needs (no device is touched beyond its CU count).
 size_t kv_attend_workspace(const KvAttendArgs& a, int dtype);
 int launch_kv_attend(const KvAttendArgs& a, int dtype, const DequantArgs& da, void* stream);
-// Attention of a tree of new tokens (k_tree.hip), at most kMostNodes to a sequence.
+// Attention of a tree of new tokens (k_tree_few.hip, k_tree.hip), at most kMostNodes to a sequence.
 constexpr int kMostNodes = 256;
+constexpr int kTreeBlockRows = 128;  // of a workgroup of k_tree.hip
+int tree_block_slots(int head_dim, int dtype);  // workgroups of that kernel the device holds at once
+int launch_tree_blocks(const KvAttendArgs& a, int dtype, int blocks, int nsplit, const DequantArgs& da, void* stream);
 size_t kv_tree_workspace(const KvAttendArgs& a, int dtype);
 int launch_kv_tree(const KvAttendArgs& a, int dtype, const DequantArgs& da, void* stream);
 // Joins the partial results of splits of the keys (k_attn_merge.hip): [0] those of sequences with few

@@ -1,10 +1,7 @@
-// k_tree.hip -- attention of a tree of drafted tokens over the cache.
-//
-//   o_i = sum_j p_ij v_j, p_ij = softmax over the keys j that token i sees: the context before the draft, the tokens on
-//   its path from the tree's root, itself
+// k_tree.hip -- attention of a tree of drafted tokens over the cache, for drafts with many rows to a key/value head.
 #include <hip/hip_runtime.h>
 
-#include <algorithm>
+#include <type_traits>
 
 #include "bq_attend.h"
 #include "bq_launch.h"
@@ -12,97 +9,615 @@
 namespace bq {
 namespace {
 
-struct TreePlan {
-  int rt, tiles, nsplit;
-  size_t bytes;
+constexpr int kTile = 64;   // keys
+constexpr int kRows = kTreeBlockRows;  // new token x query head of one key/value head
+constexpr int kCopies = 8;  // of a table entry in LDS, for lanes l % 8
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef _Float16 f16x32 __attribute__((ext_vector_type(32)));
+typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
+typedef int i32x6 __attribute__((ext_vector_type(6)));
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+
+// As in k_attn_chunk.hip.
+constexpr int kKeySpread = 12, kValueSpread = 4;
+constexpr int kLeastKey = -100, kLeastValue = -80;
+constexpr float kHead = 3.0f;
+
+// A thread decodes D / 4 consecutive d of one key: lane = key, wave = quarter of the head.
+template <int D, int KB, bool FINE>
+struct Decode {
+  static constexpr int kPart = D / 4;
+  static constexpr int kPieces = kPart / 8;          // of 8 d, 16 bytes of binary16
+  static constexpr int kRow = D * KB / 8;            // bytes of a key's codes
+  static constexpr int kWords = kPart * KB / 32;     // of a thread's codes
+  static constexpr int kPieceWords = KB / 4;
+  static constexpr int kOwn = D == 256 ? 2 : 1;      // blocks that a thread's d may belong to
+  static constexpr int kBlocks = D / 32;             // most blocks of a head
+  static constexpr int kEntry = FINE && KB == 4 ? 8 : 4;  // bytes of a table entry
+  static constexpr int kTable = 256 * kCopies * kEntry;
+  static constexpr int kLookups = KB == 4 ? 4 : 8;   // of a piece
+  typedef std::conditional_t<FINE && KB == 4, f32x2, uint32_t> Entry;
 };
 
-int64_t choose_splits(int64_t base, int64_t slots, int64_t keys, int num_seqs) {
-  const int64_t steps = (keys + 255) / 256;
-  const int64_t least = num_seqs > 1 ? std::max((steps + 31) / 32, (int64_t)1) : 1;
-  int64_t best = INT64_MAX, n = 1;
-  for (int64_t k = least < kMaxSplits ? least : kMaxSplits; k <= kMaxSplits && (k <= steps || k <= 1); ++k) {
-    const int64_t cost = (base * k + slots - 1) / slots * ((steps + k - 1) / k + 3);
-    if (cost < best) {
-      best = cost;
-      n = k;
+// Codes and block maxima of a thread's key, of one side.
+template <int D, int KB, bool FINE>
+struct Raw {
+  uint32_t code[Decode<D, KB, FINE>::kWords];
+  float a[Decode<D, KB, FINE>::kOwn];     // of its own d
+  float all[Decode<D, KB, FINE>::kBlocks];  // of the whole head
+};
+
+// What there is to know of a tile of one side: 2^e above its largest maximum; its keys' own exponents (of the lane's key)
+// where they are apart.
+struct Scale {
+  int e, own;
+  bool apart;
+};
+
+__device__ __forceinline__ uint32_t wave_max_bits(uint32_t v) {
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, false));
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, false));
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x141, 0xF, 0xF, false));
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x140, 0xF, 0xF, false));
+  u32x2 s = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+  v = max(s.x, s.y);
+  s = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+  return (uint32_t)__builtin_amdgcn_readfirstlane((int)max(s.x, s.y));
+}
+
+__device__ __forceinline__ int exponent(uint32_t bits, int least) { return min(max((int)(bits >> 23) - 126, least), 120); }
+
+template <int D, int KB, bool FINE>
+__global__ __launch_bounds__(256, (D == 256 || FINE ? 1 : 2)) void tree_kernel(KvAttendArgs aa, DequantArgs da, int nsplit,
+                                                                            float* partial) {
+  using C = Decode<D, KB, FINE>;
+  constexpr bool bf16 = !FINE;
+  constexpr int kSteps = D / 16, kBlocks = D / 32;
+  constexpr int kTilePieces = kTile * D / 8;
+  __shared__ u32x4 s_key[2][kTilePieces];
+  __shared__ __attribute__((aligned(16))) char s_value[2][kTilePieces * 16];
+  __shared__ __attribute__((aligned(16))) uint32_t s_rest[2][FINE ? 12 * D : 4];
+  __shared__ __attribute__((aligned(16))) char s_table[C::kTable];
+  __shared__ TreeShared<kRows> s_tree;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int n = lane & 31, g = lane >> 5;
+  const float entry_lo = da.c[KB == 4 ? tid & 15 : tid], entry_hi = da.c[KB == 4 ? tid >> 4 : tid];
+  load_fence();
+  const int kvh = blockIdx.x % aa.cache.kv_heads, rest_x = blockIdx.x / aa.cache.kv_heads;
+  const int split = rest_x % nsplit, block = rest_x / nsplit;
+  const int seq = blockIdx.z;
+  const int group = aa.heads / aa.cache.kv_heads;
+  const Sequence sq = sequence(aa, seq);
+  const int nrows = min(sq.nq, aa.max_q_len) * group;
+  if (block * kRows >= nrows) return;
+
+  const int last_row = min(block * kRows + kRows, nrows) - 1;
+  const int i_first = block * kRows / group, i_last = last_row / group;
+  const int context = sq.kv - sq.nq;
+  const int first = node_first(aa, context, 0);
+  int last = max(min(sq.kv, context + i_last + 1), 0);  // end of the keys that some row may see
+  const int begin = first / kTile, end = (last + kTile - 1) / kTile;
+  const int count = max(end - begin, 0), per = (count + nsplit - 1) / nsplit;
+  const int t_first = begin + split * per, t_end = min(t_first + per, end);
+  const int lo_all = node_first(aa, context, i_last);
+  int hi_all = context;
+
+  const int parent = tid <= i_last ? aa.parents[sq.q0 + tid] : -2;
+  // ---- the cache: rows of the pool, codes and maxima of the thread's key of a tile
+  const int lps = aa.cache.log2_page, log2b = aa.cache.log2b, nb = D >> log2b;
+  const int32_t* const pages = aa.page_table + (int64_t)seq * aa.table_stride;
+  const int last_page = sq.kv > 0 ? (sq.kv - 1) >> lps : 0;
+  auto page_of = [&](int t) { return pages[min((min(t, t_end - 1) * kTile + lane) >> lps, last_page)]; };
+  auto listed = [&](int id) { return (uint32_t)id < (uint32_t)aa.cache.num_pages; };
+  auto row_of = [&](int t, int id) {
+    const int j = min(t, t_end - 1) * kTile + lane;
+    return (((int64_t)(listed(id) ? id : 0) * aa.cache.kv_heads + kvh) << lps) + (j & ((1 << lps) - 1));
+  };
+  auto fetch = [&](Raw<D, KB, FINE>& x, int side, int64_t row) {
+    const uint8_t* src = aa.cache.packed[side] + row * C::kRow + wave * (C::kPart * KB / 8);
+#pragma unroll
+    for (int k = 0; k < C::kWords; k += 4) {
+      const u32x4 v = *reinterpret_cast<const u32x4*>(src + 4 * k);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x.code[k + e] = v[e];
     }
+    const float* a = aa.cache.absmax[side] + row * nb;
+#pragma unroll
+    for (int b = 0; b < C::kOwn; ++b) x.a[b] = a[(wave * C::kPart + 32 * b) >> log2b];
+#pragma unroll
+    for (int b = 0; b < C::kBlocks; ++b) x.all[b] = a[min(b, nb - 1)];
+  };
+  Raw<D, KB, FINE> xk, xv;
+  int id_first = 0, id = 0, id_next = 0;  // pages of the lane's keys of tiles t, t + 1, t + 2
+  if (t_first < t_end) {
+    id_first = page_of(t_first);
+    id = page_of(t_first + 1);
+    id_next = page_of(t_first + 2);
+    const int64_t row = row_of(t_first, id_first);
+    fetch(xk, 0, row);
+    fetch(xv, 1, row);
   }
-  return n;
-}
 
-TreePlan make_plan(const KvAttendArgs& a) {
-  TreePlan p = {};
-  const int64_t group = a.heads / a.cache.kv_heads, D = a.cache.head_dim, cus = cu_count();
-  const int64_t rows = a.max_q_len * group;
-  p.rt = D > 128 || rows <= 16 ? 1 : 2;
-  p.tiles = (int)((rows + 16 * p.rt - 1) / (16 * p.rt));
-  const int64_t rows_all = a.tokens * group / (16 * p.rt) + a.num_seqs;
-  const int64_t base = a.cache.kv_heads * std::min((int64_t)p.tiles * a.num_seqs, rows_all);
-  const int nb = a.cache.head_dim >> a.cache.log2b;
-  const int64_t slots = cus * (D == 256 || nb == 4 || p.rt * D > 128 || wide_form((int)D, nb, a.bits, p.rt) ? 1 : 2);
-  int64_t n = choose_splits(base, slots, a.max_kv_len, a.num_seqs);
-  if (a.window > 0 && (int64_t)a.window + a.max_q_len < a.max_kv_len) {
-    const int64_t k = choose_splits(base, slots, (int64_t)a.window + a.max_q_len, a.num_seqs);
-    n = k < n ? k : n;
+  {  // table
+    const float x0 = __builtin_ldexpf(entry_lo, kTopBit), x1 = __builtin_ldexpf(entry_hi, kTopBit);
+    const uint32_t w = pack_f16(x1, x0);
+    const u32x4 e = FINE && KB == 4 ? (u32x4){f32_bits(x1), f32_bits(x0), f32_bits(x1), f32_bits(x0)}
+                    : FINE          ? (u32x4){f32_bits(x0), f32_bits(x0), f32_bits(x0), f32_bits(x0)}
+                                    : (u32x4){w, w, w, w};
+#pragma unroll
+    for (int i = 0; i < kCopies * C::kEntry / 16; ++i) *reinterpret_cast<u32x4*>(s_table + (tid * kCopies * C::kEntry / 16 + i) * 16) = e;
   }
-  p.nsplit = (int)n;
-  if (n > 1) p.bytes = (size_t)a.tokens * a.heads * n * (D + 3) * 4;
-  return p;
-}
+  const uint32_t copy = (lane & (kCopies - 1)) * C::kEntry;
 
-template <int D, int NB, int KB, int RT, bool HL>
-hipError_t launch_type(const KvAttendArgs& a, const TreePlan& p, const DequantArgs& da, hipStream_t s) {
-  const dim3 grid((unsigned)(p.tiles * p.nsplit), (unsigned)a.cache.kv_heads, (unsigned)a.num_seqs);
-  return launch_kernel(attend_kernel<D, NB, KB, RT, HL, true>, grid, dim3(64 * Occupancy<D, NB, KB, RT>::kWaves), s, a, da,
-                       p.nsplit, static_cast<float*>(a.workspace), (int)kAllRows);
-}
-
-template <int D, int NB, int KB, int RT>
-hipError_t launch_rows(const KvAttendArgs& a, const TreePlan& p, int dtype, const DequantArgs& da, hipStream_t s) {
-  return dtype == F16 ? launch_type<D, NB, KB, RT, true>(a, p, da, s) : launch_type<D, NB, KB, RT, false>(a, p, da, s);
-}
-
-template <int D, int NB, int KB>
-hipError_t launch_bits(const KvAttendArgs& a, const TreePlan& p, int dtype, const DequantArgs& da, hipStream_t s) {
-  if constexpr (D <= 128) {
-    if (p.rt == 2) return launch_rows<D, NB, KB, 2>(a, p, dtype, da, s);
+  // Queries as operands: binary16 relative to a power of two of the row, the scale's sign included.
+  const int r = block * kRows + wave * 32 + n;
+  const bool live = r < nrows;
+  const int row_i = live ? r / group : i_first;
+  const int head = kvh * group + (live ? r - row_i * group : 0);
+  const int64_t token = sq.q0 + row_i;
+  float scale;
+  f16x8 q[kSteps];
+  i32x8 q_rest[FINE ? D / 64 : 1];  // four times q, in 6 bits
+  {
+    // d = 8 (2 s + g) .. + 7 for step s
+    const char* src = static_cast<const char*>(aa.q) + (token * aa.q_stride + (int64_t)head * D + 8 * g) * 2;
+    u32x4 w[kSteps];
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) w[s] = *reinterpret_cast<const u32x4*>(src + 32 * s);
+    uint32_t top = 0;  // magnitudes of 16-bit floats are ordered like their bits
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) top = max(top, max(w[s][k] & 0x7fffu, (w[s][k] >> 16) & 0x7fffu));
+    top = max(top, (uint32_t)__shfl_xor((int)top, 32));
+    if (top >= (bf16 ? 0x7f80u : 0x7c00u)) top = 0;
+    const float tf = bf16 ? bits_f32(top << 16) : (float)__builtin_bit_cast(_Float16, (uint16_t)top);
+    const int ex = tf > 0.0f ? max(__builtin_amdgcn_frexp_expf(tf), -126) : 0;  // |q| < 2^ex
+    const float unit = __builtin_ldexpf(aa.scale < 0.0f ? -1.0f : 1.0f, -ex);
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t x = w[s][k];
+        const f16x2 h = __builtin_bit_cast(f16x2, x);
+        w[s][k] = bf16 ? pack_f16(bits_f32(x << 16) * unit, bits_f32(x & 0xffff0000u) * unit) : pack_f16((float)h.x * unit, (float)h.y * unit);
+      }
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) q[s] = __builtin_bit_cast(f16x8, w[s]);
+    if constexpr (FINE) {
+      // the rests' order: lane g has d = 64 S + 32 g + 0 .. 31, of which the other half lane holds two pieces
+#pragma unroll
+      for (int S = 0; S < D / 64; ++S) {
+        f16x32 x;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {  // piece 8 S + 4 g + i is step 4 S + 2 g + i / 2 of half lane i & 1
+          u32x4 v;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t lo = __shfl((int)w[4 * S + i / 2][e], n + 32 * (i & 1));
+            const uint32_t hi = __shfl((int)w[4 * S + 2 + i / 2][e], n + 32 * (i & 1));
+            v[e] = g ? hi : lo;
+          }
+          const f16x8 p = __builtin_bit_cast(f16x8, v);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[8 * i + e] = p[e] * (_Float16)4.0f;
+        }
+        const i32x6 y = __builtin_amdgcn_cvt_scalef32_pk32_fp6_f16(x, 1.0f);
+        q_rest[S] = (i32x8){y[0], y[1], y[2], y[3], y[4], y[5], 0, 0};
+      }
+    }
+    scale = __builtin_ldexpf(fabsf(aa.scale) * 1.44269504088896341f, ex);
   }
-  return launch_rows<D, NB, KB, 1>(a, p, dtype, da, s);
+  read_tree<256, kRows>(aa, s_tree, parent, tid, i_first, i_last);
+  __syncthreads();  // table and tree are in place
+  if (!any_node(s_tree, i_first, i_last)) last = hi_all = 0;  // no row of the block sees any key: theirs may hold anything
+  const int depth = s_tree.depth[row_i - i_first];
+  const uint32_t* const seen = s_tree.seen[row_i - i_first];
+  const int lo = node_first(aa, context, depth), hi = depth >= 0 ? context : 0;  // of the context
+
+  // Whether some row sees the lane's key of tile t.
+  auto counts = [&](int t, int page) {
+    const int j = t * kTile + lane, node = j - context;
+    const bool used = node < 0 || (node < kMostNodes && (s_tree.used[(node >> 5) + 1] >> (node & 31) & 1));
+    return j >= first && j < last && listed(page) && used;
+  };
+
+  // ---- decoding
+  auto scale_tile = [&](Raw<D, KB, FINE>& x, int side, bool seen_key) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int b = 0; b < C::kBlocks; ++b) top = max(top, f32_bits(x.all[b]) & 0x7fffffffu);
+    top = seen_key ? top : 0u;
+    const bool say = seen_key && (side == 1 || top != 0);  // zero keys, whose scores are zero at any scale, have none
+    const int least = side == 0 ? kLeastKey : kLeastValue;
+    const uint32_t most = wave_max_bits(say ? top : 0u), low = ~wave_max_bits(say ? ~top : 0u);
+    Scale s;
+    s.e = exponent(most, least);
+    s.apart = low <= most && s.e - exponent(low, least) > (side == 0 ? kKeySpread : kValueSpread);
+    s.own = s.apart && say ? exponent(top, least) : s.e;
+#pragma unroll
+    for (int b = 0; b < C::kOwn; ++b) x.a[b] = seen_key ? __builtin_ldexpf(x.a[b], -s.own) : 0.0f;
+    return s;
+  };
+  auto entry_at = [&](uint32_t w, int b) {
+    constexpr int shift = __builtin_ctz(kCopies * C::kEntry);
+    const uint32_t at = ((b == 0 ? w & 255u : b == 3 ? w >> 24 : __builtin_amdgcn_ubfe(w, 8 * b, 8)) << shift) | copy;
+    return *reinterpret_cast<const typename C::Entry*>(s_table + at);
+  };
+  auto look_up = [&](const Raw<D, KB, FINE>& x, int i, typename C::Entry (&e)[C::kLookups]) {
+#pragma unroll
+    for (int k = 0; k < C::kLookups; ++k) e[k] = entry_at(x.code[i * C::kPieceWords + k / 4], k & 3);
+  };
+  // The 8 values of piece i: rounded once to binary16, and what that left (times the tile's power of two).
+  auto products = [&](const Raw<D, KB, FINE>& x, int i, const typename C::Entry (&e)[C::kLookups], f16x8* left) {
+    const float a = x.a[C::kOwn > 1 ? i / 4 : 0];
+    u32x4 h;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if constexpr (FINE) {
+        float v0, v1;
+        if constexpr (KB == 4) {
+          v0 = e[k].x * a;
+          v1 = e[k].y * a;
+        } else {
+          v0 = bits_f32(e[2 * k]) * a;
+          v1 = bits_f32(e[2 * k + 1]) * a;
+        }
+        const uint32_t pair = pack_f16(v0, v1);
+        h[k] = pair;
+        if (left != nullptr) {
+          const f16x2 y = __builtin_bit_cast(f16x2, pair);
+          (*left)[2 * k] = (_Float16)(v0 - (float)y.x);
+          (*left)[2 * k + 1] = (_Float16)(v1 - (float)y.y);
+        }
+      } else {
+        f16x2 c;
+        if constexpr (KB == 4) {
+          const uint32_t x2 = e[k];
+          c = __builtin_bit_cast(f16x2, x2);
+        } else {
+          const uint32_t x0 = e[2 * k], x1 = e[2 * k + 1];
+          c.x = __builtin_bit_cast(f16x2, x0).x;
+          c.y = __builtin_bit_cast(f16x2, x1).x;
+        }
+        // mixed-precision instructions: one rounding, to binary16
+        const f16x2 y = {(_Float16)__builtin_fmaf((float)c.x, a, 0.0f), (_Float16)__builtin_fmaf((float)c.y, a, 0.0f)};
+        h[k] = __builtin_bit_cast(uint32_t, y);
+      }
+    }
+    return h;
+  };
+  u32x4* const key_to[2] = {s_key[0] + ((lane >> 5) * kSteps) * 64 + (lane & 31), s_key[1] + ((lane >> 5) * kSteps) * 64 + (lane & 31)};
+  const int turn = 2 * (lane & 3) + (lane >> 2 & 1);  // see value_at
+  auto put_key = [&](int b, int i, const u32x4& h) {
+    const int d8 = wave * C::kPieces + i;
+    key_to[b][(d8 >> 1) * 64 + 32 * (d8 & 1)] = h;
+  };
+  auto put_value = [&](int b, int i, const u32x4& h) {
+    *reinterpret_cast<u32x4*>(s_value[b] + lane * (2 * D) + ((wave * C::kPieces + i) ^ turn) * 16) = h;
+  };
+  f16x32 left;  // of 32 d of the key
+  auto put_rest = [&](int b, int part) {  // d = 32 part .. of the head
+    if constexpr (FINE) {
+      const i32x6 w = __builtin_amdgcn_cvt_scalef32_pk32_fp6_f16(left, 1.0f);
+      // 24 bytes for lane 32 (part & 1) + n of S = part / 2, half = key / 32; the first 16 of each lane before the last 8
+      const int l = 32 * (part & 1) + (lane & 31);
+      uint32_t* const dst = s_rest[b] + ((part >> 1) * 2 + (lane >> 5)) * 384;
+      *reinterpret_cast<u32x4*>(dst + 4 * l) = (u32x4){(uint32_t)w[0], (uint32_t)w[1], (uint32_t)w[2], (uint32_t)w[3]};
+      *reinterpret_cast<u32x2*>(dst + 256 + 2 * l) = (u32x2){(uint32_t)w[4], (uint32_t)w[5]};
+    }
+  };
+  // Piece i of the keys from its entries, with what rounding left of it.
+  auto finish_key = [&](int b, int i, const typename C::Entry (&e)[C::kLookups]) {
+    f16x8 l;
+    put_key(b, i, products(xk, i, e, FINE ? &l : nullptr));
+    if constexpr (FINE) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) left[8 * (i & 3) + k] = l[k];
+      if (i % 4 == 3) put_rest(b, wave * (C::kPieces / 4) + i / 4);
+    }
+  };
+  // Where a lane reads the values' operands: rows of 16-byte chunks, chunk c of key k at place c ^ (2 (k & 3) + (k >> 2 & 1)), so that
+  // neither the writes (a key to a lane) nor the transposed reads (4 keys x 16 d to 16 lanes) meet in a bank.
+  const int x_of = 2 * (lane >> 4 & 1) + (lane >> 1 & 1), turn_r = 2 * (lane >> 2 & 3) + g;
+  const int value_base = ((lane >> 2 & 3) + 4 * g) * (2 * D) + 8 * (lane & 1);
+  const int value_at[2] = {value_base + (x_of ^ turn_r) * 16, value_base + (x_of ^ turn_r ^ 4) * 16};
+  auto value_operand = [&](int b, int half, int i, int ks) {  // d = 32 i .., keys 32 half + 16 ks ..
+    typedef __attribute__((address_space(3))) s16x4* Local;
+    const char* at = s_value[b] + value_at[i & 1] + (i >> 1) * 128 + (32 * half + 16 * ks) * (2 * D);
+    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Local)at);
+    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Local)(at + 8 * (2 * D)));
+    typedef short s16x8 __attribute__((ext_vector_type(8)));
+    return __builtin_bit_cast(f16x8, (s16x8)__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+  };
+
+  // M of the row; sum of its weights (this lane's keys, in units of 2^(M - 3))
+  float ref = -INFINITY, sum = 0.0f;
+  int most_ev = -1000;  // of the tiles so far
+  f32x16 acc[kBlocks];
+#pragma unroll
+  for (int i = 0; i < kBlocks; ++i)
+#pragma unroll
+    for (int v = 0; v < 16; ++v) acc[i][v] = 0.0f;
+  f32x16 sc[2];
+  u32x4 w[2][2];
+  w[1][0] = w[1][1] = (u32x4){0, 0, 0, 0};
+  u32x4 wl[2][FINE ? 2 : 1];  // what rounding left of them
+  wl[1][0] = wl[1][FINE ? 1 : 0] = (u32x4){0, 0, 0, 0};
+  auto add_rest = [&](int half, int S, const uint32_t* rest, f32x16 z) {
+    const uint32_t* src = rest + (S * 2 + half) * 384;
+    const u32x4 a4 = *reinterpret_cast<const u32x4*>(src + 4 * lane);
+    const u32x2 a2 = *reinterpret_cast<const u32x2*>(src + 256 + 2 * lane);
+    const i32x8 a = {(int)a4.x, (int)a4.y, (int)a4.z, (int)a4.w, (int)a2.x, (int)a2.y, 0, 0};
+    constexpr int kFp6 = 2, kOne = 127, kQuarter = 125;
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, q_rest[S], z, kFp6, kFp6, 0, kOne, 0, kQuarter);
+  };
+  auto multiply_keys = [&](int half, int b) {
+    const f16x8* kp = reinterpret_cast<const f16x8*>(s_key[b]) + lane + half * kSteps * 64;
+    f32x16 z;
+#pragma unroll
+    for (int v = 0; v < 16; ++v) z[v] = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kSteps; ++k) z = __builtin_amdgcn_mfma_f32_32x32x16_f16(kp[k * 64], q[k], z, 0, 0, 0);
+    if constexpr (FINE) {
+#pragma unroll
+      for (int S = 0; S < D / 64; ++S) z = add_rest(half, S, s_rest[b], z);
+    }
+    return z;
+  };
+
+  struct Info {
+    Scale k, v;
+    uint64_t keys;  // that some row sees
+  };
+  // The half step of half `half` of tile t: next_b, prev_b: the buffers of the keys whose scores follow and of the values that
+  // the other half's weights belong to; beside every second product, move(k) decodes a piece.
+  auto half_step = [&](auto half_c, int t, const Info& info, int next_b, int prev_b, auto move) {
+    constexpr int half = half_c.value;
+    const float ev = (float)info.v.e;
+    const int j0 = t * kTile + 32 * half;
+    const uint32_t keys = half ? (uint32_t)(info.keys >> 32) : (uint32_t)info.keys;
+    f32x16& s = sc[half];
+    constexpr int kMul = 2 * kSteps, kAhead = 6;
+    const f16x8* kp = reinterpret_cast<const f16x8*>(s_key[next_b]) + lane + (half ^ 1) * kSteps * 64;
+    auto operand = [&](int z) {
+      return z & 1 ? value_operand(prev_b, half ^ 1, (z >> 1) % kBlocks, (z >> 1) / kBlocks) : kp[(z >> 1) * 64];
+    };
+    f16x8 a[kMul];
+#pragma unroll
+    for (int z = 0; z < kAhead; ++z) a[z] = operand(z);
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_nop 15");  // max3_hw is no instruction that the compiler waits for a matrix product before
+    float f = fmaxf(__builtin_ldexpf(scale, info.k.e - kTopBit), 0x1p-100f);
+    // of the lane's keys 8 i + 4 g + e, element 4 i + e
+    auto own_of = [&](const Scale& x, int v) { return __shfl(x.own, 32 * half + 8 * (v >> 2) + 4 * g + (v & 3)); };
+    if (info.k.apart || info.v.apart) {  // rare: the scores to the tile's units, the values' exponents beside them
+      const float inv = 1.0f / f;
+#pragma unroll
+      for (int v = 0; v < 16; ++v)
+        s[v] = fmaf((float)(own_of(info.v, v) - info.v.e), inv, __builtin_ldexpf(s[v], own_of(info.k, v) - info.k.e));
+    }
+    if (!(j0 >= lo_all && j0 + 32 <= hi_all && keys == ~0u)) {  // some key hidden from some row
+      const int from = j0 - context;
+      uint32_t mine = 0;
+      if (from > -32) {
+        const int word = min((from + 32) >> 5, kTreeWords - 2);
+        mine = __builtin_amdgcn_alignbit(seen[word + 1], seen[word], from & 31);
+      }
+#pragma unroll
+      for (int v = 0; v < 16; ++v) {
+        const int key = 8 * (v >> 2) + (v & 3) + 4 * g, j = j0 + key;
+        const bool no = j >= context ? !(mine >> key & 1) : j < lo || j >= hi;
+        s[v] = no || !(keys >> key & 1) ? -INFINITY : s[v];
+      }
+    }
+    float top = -INFINITY, p = 0.0f;
+    u32x4 x[2], y[2];
+    float part = 0.0f;
+    auto weigh = [&](int v, float c) {
+      const float e = exp2_hw(fmaf(s[v], f, c));
+      if (v & 1) {
+        uint32_t pair = pack_f16(p, e);
+        asm volatile("" : "+v"(pair));  // here, beside the products, and not on the side of the branch below
+        part += p + e;
+        if constexpr (FINE) {
+          const f16x2 h = __builtin_bit_cast(f16x2, pair);
+          y[v >> 3][(v & 7) >> 1] = pack_f16(fmaf((float)h.x, -1.0f, p), fmaf((float)h.y, -1.0f, e));
+        }
+        x[v >> 3][(v & 7) >> 1] = pair;
+      } else {
+        p = e;
+      }
+    };
+    auto offset = [&]() { return (ev + kHead) - fmaxf(ref, -0x1p120f); };  // no key yet: -infinity stays
+    float c = offset();
+    f32x16& z_next = sc[half ^ 1];
+#pragma unroll
+    for (int v = 0; v < 16; ++v) z_next[v] = 0.0f;
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int z = 0; z < kMul; ++z) {  // kept in this order
+      if (z & 1) {
+        const int i = (z >> 1) % kBlocks, ks = (z >> 1) / kBlocks;
+        acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a[z], __builtin_bit_cast(f16x8, w[half ^ 1][ks]), acc[i], 0, 0, 0);
+        if constexpr (FINE)
+          acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a[z], __builtin_bit_cast(f16x8, wl[half ^ 1][ks]), acc[i], 0, 0, 0);
+      } else {
+        z_next = __builtin_amdgcn_mfma_f32_32x32x16_f16(a[z], q[z >> 1], z_next, 0, 0, 0);
+      }
+      if constexpr (FINE) {
+        if (z % 8 == 7) z_next = add_rest(half ^ 1, z / 8, s_rest[next_b], z_next);
+      }
+      if (z + kAhead < kMul) a[z + kAhead] = operand(z + kAhead);
+      if (z & 1) move(z >> 1);
+#pragma unroll
+      for (int v = z * 16 / kMul; v < (z + 1) * 16 / kMul; ++v) {
+        weigh(v, c);
+        if (v & 1) top = max3_hw(top, s[v - 1], s[v]);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    top = fmaf(top, f, ev);
+    const bool far = __any(fabsf(top) > 0x1p14f && top != -INFINITY);
+    if (far || __any(top > ref + kSlack)) {
+      // Rare after the first tiles: a larger reference.  The sums so far move to it, and the weights are taken again.
+      if (far) {  // scores that are rounded by as much as the slack: once, here, and not again beside the reference
+        top = -INFINITY;
+#pragma unroll
+        for (int v = 0; v < 16; ++v) {
+          s[v] *= f;
+          top = fmaxf(top, s[v]);
+        }
+        f = 1.0f;
+        top += ev;
+      }
+      const u32x2 o = __builtin_amdgcn_permlane32_swap(f32_bits(top), f32_bits(top), false, false);
+      const float up = fmaxf(ref, fmaxf(bits_f32(o.x), bits_f32(o.y)));
+      const float down = ref == -INFINITY ? 0.0f : exp2_hw(ref - up);
+      sum = lower(sum, ref, up);
+      ref = up;
+#pragma unroll
+      for (int i = 0; i < kBlocks; ++i)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) acc[i][v] *= down;
+      part = 0.0f;
+      c = offset();
+#pragma unroll
+      for (int v = 0; v < 16; ++v) weigh(v, c);
+    }
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {
+      w[half][ks] = x[ks];
+      if constexpr (FINE) wl[half][ks] = y[ks];
+    }
+    // The denominator, in weights that do not hold the exponent.
+    most_ev = max(most_ev, info.v.e);
+    if (info.v.apart || info.v.e < most_ev - 60) {
+      float more = 0.0f;
+#pragma unroll
+      for (int v = 0; v < 16; ++v) more += exp2_hw(fmaf(s[v], f, c) - (float)own_of(info.v, v));
+      sum += more;
+    } else {
+      sum += __builtin_ldexpf(part, -info.v.e);
+    }
+  };
+
+  if (t_first < t_end) {
+    auto keys_of = [&](int t, int page) { return (uint64_t)__ballot(counts(t, page)); };
+    Info info;
+    info.keys = keys_of(t_first, id_first);
+    info.k = scale_tile(xk, 0, info.keys >> lane & 1);
+    info.v = scale_tile(xv, 1, info.keys >> lane & 1);
+#pragma unroll
+    for (int i = 0; i < C::kPieces; ++i) {
+      typename C::Entry e[C::kLookups];
+      look_up(xk, i, e);
+      finish_key(0, i, e);
+      look_up(xv, i, e);
+      put_value(0, i, products(xv, i, e, nullptr));
+      *reinterpret_cast<u32x4*>(s_value[1] + (i * 256 + tid) * 16) = (u32x4){0, 0, 0, 0};  // no weights wait at first
+    }
+    int64_t row = row_of(t_first + 1, id);
+    fetch(xk, 0, row);
+    fetch(xv, 1, row);
+    __syncthreads();
+    sc[0] = multiply_keys(0, 0);
+    for (int t = t_first; t < t_end; ++t) {
+      const int b = (t - t_first) & 1;
+      Info next;
+      next.keys = keys_of(min(t + 1, t_end - 1), id);
+      const bool seen_key = next.keys >> lane & 1;
+      // Beside the products the next tile is decoded: its keys into the buffer last read before the previous barrier, its
+      // values, past the barrier, into that of the tile before.
+      next.k = scale_tile(xk, 0, seen_key);
+      typename C::Entry e[C::kLookups];
+      half_step(std::integral_constant<int, 0>(), t, info, b, b ^ 1, [&](int k) {
+        if (k % 2 == 0 && k / 2 < C::kPieces) {
+          if (k > 0) finish_key(b ^ 1, k / 2 - 1, e);
+          look_up(xk, k / 2, e);
+        }
+      });
+      finish_key(b ^ 1, C::kPieces - 1, e);
+      id = id_next;
+      id_next = page_of(t + 3);
+      row = row_of(t + 2, id);
+      fetch(xk, 0, row);
+      __syncthreads();
+      next.v = scale_tile(xv, 1, seen_key);
+      half_step(std::integral_constant<int, 1>(), t, info, b ^ 1, b, [&](int k) {
+        if (k % 2 == 0 && k / 2 < C::kPieces) {
+          if (k > 0) put_value(b ^ 1, k / 2 - 1, products(xv, k / 2 - 1, e, nullptr));
+          look_up(xv, k / 2, e);
+        }
+      });
+      put_value(b ^ 1, C::kPieces - 1, products(xv, C::kPieces - 1, e, nullptr));
+      fetch(xv, 1, row);
+      info = next;
+    }
+    // the last half's weights
+    const int b = (t_end - 1 - t_first) & 1;
+#pragma unroll
+    for (int i = 0; i < kBlocks; ++i)
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) {
+        const f16x8 v = value_operand(b, 1, i, ks);
+        acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, __builtin_bit_cast(f16x8, w[1][ks]), acc[i], 0, 0, 0);
+        if constexpr (FINE)
+          acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, __builtin_bit_cast(f16x8, wl[1][ks]), acc[i], 0, 0, 0);
+      }
+  }
+
+  const u32x2 o2 = __builtin_amdgcn_permlane32_swap(f32_bits(sum), f32_bits(sum), false, false);
+  const float unit = __builtin_ldexpf(1.0f, -kTopBit);  // of the sums beside those of the weights
+  const bool sees = depth >= 0;  // a row that sees nothing went along through the context
+  const float l = sees ? bits_f32(o2.x) + bits_f32(o2.y) : 0.0f;
+  if (!live) return;
+  const int64_t part = (token * aa.heads + head) * nsplit + split;
+  const float inv = nsplit > 1 ? unit : (l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l)) * unit;
+#pragma unroll
+  for (int k = 0; k < kBlocks; ++k)
+#pragma unroll
+    for (int v = 0; v < 16; v += 4) {
+      const int d = 32 * k + 2 * v + 4 * g;
+      f32x4 o;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[e] = sees ? acc[k][v + e] * inv : 0.0f;
+      if (nsplit > 1) {
+        *reinterpret_cast<f32x4*>(partial + part * D + d) = o;
+      } else {
+        const u32x2 o16 = {pack16(o[0], o[1], bf16), pack16(o[2], o[3], bf16)};
+        *reinterpret_cast<u32x2*>(static_cast<char*>(aa.out) + (token * aa.out_stride + (int64_t)head * D + d) * 2) = o16;
+      }
+    }
+  if (g == 0) {
+    const float m = sees ? ref - kHead : -INFINITY;
+    if (nsplit > 1) reinterpret_cast<Partial*>(partial + aa.tokens * aa.heads * nsplit * D)[part] = {m, l, l};
+    else if (aa.lse != nullptr) aa.lse[token * aa.heads + head] = log_sum(m, l);
+  }
 }
 
-template <int D, int NB>
-hipError_t launch_blocks(const KvAttendArgs& a, const TreePlan& p, int dtype, const DequantArgs& da, hipStream_t s) {
-  return da.K == 16 ? launch_bits<D, NB, 4>(a, p, dtype, da, s) : launch_bits<D, NB, 8>(a, p, dtype, da, s);
+template <int D, int KB>
+hipError_t launch_bits(const KvAttendArgs& a, int blocks, int nsplit, bool fine, const DequantArgs& da, hipStream_t s) {
+  const dim3 grid((unsigned)(a.cache.kv_heads * nsplit * blocks), 1u, (unsigned)a.num_seqs);
+  if constexpr (D == 128) {
+    if (fine) return launch_kernel(tree_kernel<D, KB, true>, grid, dim3(256), s, a, da, nsplit, static_cast<float*>(a.workspace));
+  }
+  return launch_kernel(tree_kernel<D, KB, false>, grid, dim3(256), s, a, da, nsplit, static_cast<float*>(a.workspace));
 }
 
 }  // namespace
 
-size_t kv_tree_workspace(const KvAttendArgs& a, int dtype) { return make_plan(a).bytes; }
+int tree_block_slots(int head_dim, int dtype) { return cu_count() * (head_dim == 256 || dtype == F16 ? 1 : 2); }
 
-int launch_kv_tree(const KvAttendArgs& a, int dtype, const DequantArgs& da, void* stream) {
-  const TreePlan p = make_plan(a);
+int launch_tree_blocks(const KvAttendArgs& a, int dtype, int blocks, int nsplit, const DequantArgs& da, void* stream) {
   const hipStream_t s = static_cast<hipStream_t>(stream);
-  if ((int64_t)p.tiles * p.nsplit > UINT32_MAX / 512 || a.cache.kv_heads > 32767 || (p.nsplit > 1 && !kv_merge_fits(a))) {
-    g_launch_refused_for_size = true;
-    return (int)hipErrorInvalidConfiguration;
-  }
-  const int nb = a.cache.head_dim >> a.cache.log2b;
-  hipError_t e;
-  if (a.cache.head_dim == 64)
-    e = nb == 1 ? launch_blocks<64, 1>(a, p, dtype, da, s) : launch_blocks<64, 2>(a, p, dtype, da, s);
-  else if (a.cache.head_dim == 128)
-    e = nb == 1   ? launch_blocks<128, 1>(a, p, dtype, da, s)
-        : nb == 2 ? launch_blocks<128, 2>(a, p, dtype, da, s)
-                  : launch_blocks<128, 4>(a, p, dtype, da, s);
-  else
-    e = nb == 1   ? launch_blocks<256, 1>(a, p, dtype, da, s)
-        : nb == 2 ? launch_blocks<256, 2>(a, p, dtype, da, s)
-        : nb == 4 ? launch_blocks<256, 4>(a, p, dtype, da, s)
-                  : launch_blocks<256, 8>(a, p, dtype, da, s);
-  if (e != hipSuccess || p.nsplit <= 1) return (int)e;
-  const MergeArgs m = {{static_cast<float*>(a.workspace), nullptr}, {p.nsplit, 0}, 0, 0};
-  return launch_kv_merge(a, dtype, m, stream);
+  const bool fine = dtype == F16;
+  if (a.cache.head_dim == 128)
+    return (int)(da.K == 16 ? launch_bits<128, 4>(a, blocks, nsplit, fine, da, s) : launch_bits<128, 8>(a, blocks, nsplit, fine, da, s));
+  return (int)(da.K == 16 ? launch_bits<256, 4>(a, blocks, nsplit, fine, da, s) : launch_bits<256, 8>(a, blocks, nsplit, fine, da, s));
 }
 
 }  // namespace bq

@@ -1,0 +1,122 @@
+// k_tree_few.hip -- attention of a tree of drafted tokens over the cache: how a call is divided, and the launches for drafts with
+// few rows to a key/value head (the kernel of bq_attend.h).
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+
+#include "bq_attend.h"
+#include "bq_launch.h"
+
+namespace bq {
+namespace {
+
+struct TreePlan {
+  bool blocks;      // k_tree.hip
+  int rt, tiles, nsplit;
+  size_t bytes;
+};
+
+// The splits of the keys whose rounds of resident workgroups take the least time, a workgroup costing its steps and
+// `more` of them for its start, its end and its part of the join.
+int64_t choose_splits(int64_t base, int64_t slots, int64_t steps, int64_t most_steps, int64_t more) {
+  int64_t best = INT64_MAX, n = 1;
+  const int64_t least = std::max((steps + most_steps - 1) / most_steps, (int64_t)1);
+  for (int64_t k = std::min(least, (int64_t)kMaxSplits); k <= kMaxSplits && (k <= steps || k <= 1); ++k) {
+    const int64_t cost = (base * k + slots - 1) / slots * ((steps + k - 1) / k + more);
+    if (cost < best) {
+      best = cost;
+      n = k;
+    }
+  }
+  return n;
+}
+
+constexpr int64_t kFewRowsOfTree = 32;
+
+TreePlan make_plan(const KvAttendArgs& a, int dtype) {
+  TreePlan p = {};
+  const int64_t group = a.heads / a.cache.kv_heads, D = a.cache.head_dim, cus = cu_count();
+  const int64_t rows = a.max_q_len * group;
+  p.blocks = rows > kFewRowsOfTree && (D == 128 || (D == 256 && dtype != F16));
+  int64_t per, slots;  // rows of a workgroup
+  if (p.blocks) {
+    per = kTreeBlockRows;
+    slots = tree_block_slots(a.cache.head_dim, dtype);
+  } else {
+    p.rt = D > 128 || rows <= 16 ? 1 : rows <= 32 || D == 128 ? 2 : 4;
+    per = 16 * p.rt;
+    const int nb = a.cache.head_dim >> a.cache.log2b;
+    slots = cus * (D == 256 || nb == 4 || p.rt * D > 128 || wide_form((int)D, nb, a.bits, p.rt) ? 1 : 2);
+  }
+  p.tiles = (int)((rows + per - 1) / per);
+  // tiles with rows in them: sequences may bring fewer tokens than the longest
+  const int64_t base = a.cache.kv_heads * std::min((int64_t)p.tiles * a.num_seqs, a.tokens * group / per + a.num_seqs);
+  const int64_t step = p.blocks ? 64 : 256;
+  auto splits = [&](int64_t keys) {
+    return choose_splits(base, slots, (keys + step - 1) / step, a.num_seqs > 1 ? 8192 / step : INT64_MAX / 2, p.blocks ? 8 : 3);
+  };
+  // the workspace is asked for without a window, and holds for any
+  int64_t n = splits(a.max_kv_len);
+  if (a.window > 0 && (int64_t)a.window + a.max_q_len < a.max_kv_len) n = std::min(n, splits((int64_t)a.window + a.max_q_len));
+  p.nsplit = (int)n;
+  if (n > 1) p.bytes = (size_t)a.tokens * a.heads * n * (D + 3) * 4;
+  return p;
+}
+
+template <int D, int NB, int KB, int RT>
+hipError_t launch_rows(const KvAttendArgs& a, const TreePlan& p, int dtype, const DequantArgs& da, hipStream_t s) {
+  const dim3 grid((unsigned)(p.tiles * p.nsplit), (unsigned)a.cache.kv_heads, (unsigned)a.num_seqs);
+  const auto kernel = dtype == F16 ? attend_kernel<D, NB, KB, RT, true, true> : attend_kernel<D, NB, KB, RT, false, true>;
+  return launch_kernel(kernel, grid, dim3(64 * Occupancy<D, NB, KB, RT>::kWaves), s, a, da, p.nsplit,
+                       static_cast<float*>(a.workspace), (int)kAllRows);
+}
+
+template <int D, int NB, int KB>
+hipError_t launch_bits(const KvAttendArgs& a, const TreePlan& p, int dtype, const DequantArgs& da, hipStream_t s) {
+  if constexpr (D == 64) {
+    if (p.rt == 4) return launch_rows<D, NB, KB, 4>(a, p, dtype, da, s);
+  }
+  if constexpr (D <= 128) {
+    if (p.rt == 2) return launch_rows<D, NB, KB, 2>(a, p, dtype, da, s);
+  }
+  return launch_rows<D, NB, KB, 1>(a, p, dtype, da, s);
+}
+
+template <int D, int NB>
+hipError_t launch_blocks(const KvAttendArgs& a, const TreePlan& p, int dtype, const DequantArgs& da, hipStream_t s) {
+  return da.K == 16 ? launch_bits<D, NB, 4>(a, p, dtype, da, s) : launch_bits<D, NB, 8>(a, p, dtype, da, s);
+}
+
+hipError_t launch_few(const KvAttendArgs& a, const TreePlan& p, int dtype, const DequantArgs& da, hipStream_t s) {
+  const int nb = a.cache.head_dim >> a.cache.log2b;
+  if (a.cache.head_dim == 64)
+    return nb == 1 ? launch_blocks<64, 1>(a, p, dtype, da, s) : launch_blocks<64, 2>(a, p, dtype, da, s);
+  if (a.cache.head_dim == 128)
+    return nb == 1   ? launch_blocks<128, 1>(a, p, dtype, da, s)
+           : nb == 2 ? launch_blocks<128, 2>(a, p, dtype, da, s)
+                     : launch_blocks<128, 4>(a, p, dtype, da, s);
+  return nb == 1   ? launch_blocks<256, 1>(a, p, dtype, da, s)
+         : nb == 2 ? launch_blocks<256, 2>(a, p, dtype, da, s)
+         : nb == 4 ? launch_blocks<256, 4>(a, p, dtype, da, s)
+                   : launch_blocks<256, 8>(a, p, dtype, da, s);
+}
+
+}  // namespace
+
+size_t kv_tree_workspace(const KvAttendArgs& a, int dtype) { return make_plan(a, dtype).bytes; }
+
+int launch_kv_tree(const KvAttendArgs& a, int dtype, const DequantArgs& da, void* stream) {
+  const TreePlan p = make_plan(a, dtype);
+  if ((int64_t)p.tiles * p.nsplit > UINT32_MAX / 512 || a.cache.kv_heads > 32767 || (p.nsplit > 1 && !kv_merge_fits(a)) ||
+      (p.blocks && (int64_t)a.cache.kv_heads * p.tiles * p.nsplit > UINT32_MAX / 256)) {
+    g_launch_refused_for_size = true;
+    return (int)hipErrorInvalidConfiguration;
+  }
+  const int e = p.blocks ? launch_tree_blocks(a, dtype, p.tiles, p.nsplit, da, stream)
+                         : (int)launch_few(a, p, dtype, da, static_cast<hipStream_t>(stream));
+  if (e != 0 || p.nsplit <= 1) return e;
+  const MergeArgs m = {{static_cast<float*>(a.workspace), nullptr}, {p.nsplit, 0}, 0, 0};
+  return launch_kv_merge(a, dtype, m, stream);
+}
+
+}  // namespace bq
