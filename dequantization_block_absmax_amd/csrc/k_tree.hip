@@ -290,11 +290,11 @@ __global__ __launch_bounds__(256, (D == 256 || FINE ? 1 : 2)) void tree_kernel(K
     }
     return h;
   };
-  u32x4* const key_to[2] = {s_key[0] + ((lane >> 5) * kSteps) * 64 + (lane & 31), s_key[1] + ((lane >> 5) * kSteps) * 64 + (lane & 31)};
+  const int key_to = (lane >> 5) * kSteps * 64 + (lane & 31);
   const int turn = 2 * (lane & 3) + (lane >> 2 & 1);  // see value_at
   auto put_key = [&](int b, int i, const u32x4& h) {
     const int d8 = wave * C::kPieces + i;
-    key_to[b][(d8 >> 1) * 64 + 32 * (d8 & 1)] = h;
+    s_key[b][key_to + (d8 >> 1) * 64 + 32 * (d8 & 1)] = h;
   };
   auto put_value = [&](int b, int i, const u32x4& h) {
     *reinterpret_cast<u32x4*>(s_value[b] + lane * (2 * D) + ((wave * C::kPieces + i) ^ turn) * 16) = h;
@@ -305,9 +305,9 @@ __global__ __launch_bounds__(256, (D == 256 || FINE ? 1 : 2)) void tree_kernel(K
       const i32x6 w = __builtin_amdgcn_cvt_scalef32_pk32_fp6_f16(left, 1.0f);
       // 24 bytes for lane 32 (part & 1) + n of S = part / 2, half = key / 32; the first 16 of each lane before the last 8
       const int l = 32 * (part & 1) + (lane & 31);
-      uint32_t* const dst = s_rest[b] + ((part >> 1) * 2 + (lane >> 5)) * 384;
-      *reinterpret_cast<u32x4*>(dst + 4 * l) = (u32x4){(uint32_t)w[0], (uint32_t)w[1], (uint32_t)w[2], (uint32_t)w[3]};
-      *reinterpret_cast<u32x2*>(dst + 256 + 2 * l) = (u32x2){(uint32_t)w[4], (uint32_t)w[5]};
+      const int dst = ((part >> 1) * 2 + (lane >> 5)) * 384;
+      *reinterpret_cast<u32x4*>(&s_rest[b][dst + 4 * l]) = (u32x4){(uint32_t)w[0], (uint32_t)w[1], (uint32_t)w[2], (uint32_t)w[3]};
+      *reinterpret_cast<u32x2*>(&s_rest[b][dst + 256 + 2 * l]) = (u32x2){(uint32_t)w[4], (uint32_t)w[5]};
     }
   };
   // Piece i of the keys from its entries, with what rounding left of it.
