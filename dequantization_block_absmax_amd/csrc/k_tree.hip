@@ -226,7 +226,8 @@ __global__ __launch_bounds__(256, (D == 256 || FINE ? 1 : 2)) void tree_kernel(K
   };
 
   // ---- decoding
-  auto scale_tile = [&](Raw<D, KB, FINE>& x, int side, bool seen_key) {
+  float ka[C::kOwn], va[C::kOwn];  // block maxima of the d that the thread decodes, relative to the tile's (or the key's) exponent
+  auto scale_tile = [&](const Raw<D, KB, FINE>& x, int side, bool seen_key, float (&a)[C::kOwn]) {
     uint32_t top = 0;
 #pragma unroll
     for (int b = 0; b < C::kBlocks; ++b) top = max(top, f32_bits(x.all[b]) & 0x7fffffffu);
@@ -239,7 +240,7 @@ __global__ __launch_bounds__(256, (D == 256 || FINE ? 1 : 2)) void tree_kernel(K
     s.apart = low <= most && s.e - exponent(low, least) > (side == 0 ? kKeySpread : kValueSpread);
     s.own = s.apart && say ? exponent(top, least) : s.e;
 #pragma unroll
-    for (int b = 0; b < C::kOwn; ++b) x.a[b] = seen_key ? __builtin_ldexpf(x.a[b], -s.own) : 0.0f;
+    for (int b = 0; b < C::kOwn; ++b) a[b] = seen_key ? __builtin_ldexpf(x.a[b], -s.own) : 0.0f;
     return s;
   };
   auto entry_at = [&](uint32_t w, int b) {
@@ -252,8 +253,8 @@ __global__ __launch_bounds__(256, (D == 256 || FINE ? 1 : 2)) void tree_kernel(K
     for (int k = 0; k < C::kLookups; ++k) e[k] = entry_at(x.code[i * C::kPieceWords + k / 4], k & 3);
   };
   // The 8 values of piece i: rounded once to binary16, and what that left (times the tile's power of two).
-  auto products = [&](const Raw<D, KB, FINE>& x, int i, const typename C::Entry (&e)[C::kLookups], f16x8* left) {
-    const float a = x.a[C::kOwn > 1 ? i / 4 : 0];
+  auto products = [&](const float (&factor)[C::kOwn], int i, const typename C::Entry (&e)[C::kLookups], f16x8* left) {
+    const float a = factor[C::kOwn > 1 ? i / 4 : 0];
     u32x4 h;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -313,7 +314,7 @@ __global__ __launch_bounds__(256, (D == 256 || FINE ? 1 : 2)) void tree_kernel(K
   // Piece i of the keys from its entries, with what rounding left of it.
   auto finish_key = [&](int b, int i, const typename C::Entry (&e)[C::kLookups]) {
     f16x8 l;
-    put_key(b, i, products(xk, i, e, FINE ? &l : nullptr));
+    put_key(b, i, products(ka, i, e, FINE ? &l : nullptr));
     if constexpr (FINE) {
 #pragma unroll
       for (int k = 0; k < 8; ++k) left[8 * (i & 3) + k] = l[k];
@@ -509,20 +510,19 @@ __global__ __launch_bounds__(256, (D == 256 || FINE ? 1 : 2)) void tree_kernel(K
     auto keys_of = [&](int t, int page) { return (uint64_t)__ballot(counts(t, page)); };
     Info info;
     info.keys = keys_of(t_first, id_first);
-    info.k = scale_tile(xk, 0, info.keys >> lane & 1);
-    info.v = scale_tile(xv, 1, info.keys >> lane & 1);
+    info.k = scale_tile(xk, 0, info.keys >> lane & 1, ka);
+    info.v = scale_tile(xv, 1, info.keys >> lane & 1, va);
 #pragma unroll
     for (int i = 0; i < C::kPieces; ++i) {
       typename C::Entry e[C::kLookups];
       look_up(xk, i, e);
       finish_key(0, i, e);
       look_up(xv, i, e);
-      put_value(0, i, products(xv, i, e, nullptr));
+      put_value(0, i, products(va, i, e, nullptr));
       *reinterpret_cast<u32x4*>(s_value[1] + (i * 256 + tid) * 16) = (u32x4){0, 0, 0, 0};  // no weights wait at first
     }
-    int64_t row = row_of(t_first + 1, id);
-    fetch(xk, 0, row);
-    fetch(xv, 1, row);
+    fetch(xk, 0, row_of(t_first + 1, id));
+    fetch(xv, 1, row_of(t_first + 1, id));
     __syncthreads();
     sc[0] = multiply_keys(0, 0);
     for (int t = t_first; t < t_end; ++t) {
@@ -532,29 +532,36 @@ __global__ __launch_bounds__(256, (D == 256 || FINE ? 1 : 2)) void tree_kernel(K
       const bool seen_key = next.keys >> lane & 1;
       // Beside the products the next tile is decoded: its keys into the buffer last read before the previous barrier, its
       // values, past the barrier, into that of the tile before.
-      next.k = scale_tile(xk, 0, seen_key);
-      typename C::Entry e[C::kLookups];
-      half_step(std::integral_constant<int, 0>(), t, info, b, b ^ 1, [&](int k) {
-        if (k % 2 == 0 && k / 2 < C::kPieces) {
-          if (k > 0) finish_key(b ^ 1, k / 2 - 1, e);
-          look_up(xk, k / 2, e);
-        }
-      });
-      finish_key(b ^ 1, C::kPieces - 1, e);
-      id = id_next;
+      next.k = scale_tile(xk, 0, seen_key, ka);
+      // Entries are asked for two pieces ahead of their products, and the following tile's codes as soon as the last are.
+      typename C::Entry e[2][C::kLookups];
+      const int page = id_next;
+      const int64_t row = row_of(t + 2, page);
       id_next = page_of(t + 3);
-      row = row_of(t + 2, id);
-      fetch(xk, 0, row);
-      __syncthreads();
-      next.v = scale_tile(xv, 1, seen_key);
-      half_step(std::integral_constant<int, 1>(), t, info, b ^ 1, b, [&](int k) {
-        if (k % 2 == 0 && k / 2 < C::kPieces) {
-          if (k > 0) put_value(b ^ 1, k / 2 - 1, products(xv, k / 2 - 1, e, nullptr));
-          look_up(xv, k / 2, e);
-        }
+      auto keys_move = [&](int i) {  // what stands before piece i's products
+        if (i >= 2 && i < C::kPieces + 2) finish_key(b ^ 1, i - 2, e[i & 1]);
+        if (i < C::kPieces) look_up(xk, i, e[i & 1]);
+        if (i == C::kPieces) fetch(xk, 0, row);
+      };
+      auto values_move = [&](int i) {
+        if (i >= 2 && i < C::kPieces + 2) put_value(b ^ 1, i - 2, products(va, i - 2, e[i & 1], nullptr));
+        if (i < C::kPieces) look_up(xv, i, e[i & 1]);
+        if (i == C::kPieces) fetch(xv, 1, row);
+      };
+      constexpr int kMoves = D / 16, kPer = C::kPieces + 2 <= kMoves ? kMoves / (C::kPieces + 2) : 1;
+      half_step(std::integral_constant<int, 0>(), t, info, b, b ^ 1, [&](int k) {
+        if (k % kPer == 0) keys_move(k / kPer);
       });
-      put_value(b ^ 1, C::kPieces - 1, products(xv, C::kPieces - 1, e, nullptr));
-      fetch(xv, 1, row);
+#pragma unroll
+      for (int i = (kMoves + kPer - 1) / kPer; i < C::kPieces + 2; ++i) keys_move(i);
+      id = page;
+      __syncthreads();
+      next.v = scale_tile(xv, 1, seen_key, va);
+      half_step(std::integral_constant<int, 1>(), t, info, b ^ 1, b, [&](int k) {
+        if (k % kPer == 0) values_move(k / kPer);
+      });
+#pragma unroll
+      for (int i = (kMoves + kPer - 1) / kPer; i < C::kPieces + 2; ++i) values_move(i);
       info = next;
     }
     // the last half's weights
