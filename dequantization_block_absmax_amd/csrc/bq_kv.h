@@ -77,7 +77,8 @@ int launch_kv_attend(const KvAttendArgs& a, int dtype, const DequantArgs& da, vo
 constexpr int kMostNodes = 256;
 constexpr int kTreeBlockRows = 128;  // of a workgroup of k_tree.hip
 int tree_block_slots(int head_dim, int dtype);  // workgroups of that kernel the device holds at once
-int launch_tree_blocks(const KvAttendArgs& a, int dtype, int blocks, int nsplit, const DequantArgs& da, void* stream);
+// The call spread over about `workgroups` workgroups, of `grid` at most; a block of rows takes up to nsplit.
+int launch_tree_blocks(const KvAttendArgs& a, int dtype, int grid, int nsplit, int workgroups, const DequantArgs& da, void* stream);
 size_t kv_tree_workspace(const KvAttendArgs& a, int dtype);
 int launch_kv_tree(const KvAttendArgs& a, int dtype, const DequantArgs& da, void* stream);
 // Joins the partial results of splits of the keys (k_attn_merge.hip): [0] those of sequences with few

@@ -94,11 +94,12 @@ __global__ __launch_bounds__(64 * kWaves) void merge_few_kernel(KvAttendArgs aa,
   for (int s = 0; s < src.nsplit; ++s) {
     const Partial p = src.parts[s];
     const f32x4 x = *reinterpret_cast<const f32x4*>(src.sums + (int64_t)s * D + d);
-    const float f = p.m == -INFINITY ? 0.0f : exp2_hw(p.m - top);
+    const bool some = p.m != -INFINITY;  // where there is nothing the sums may not have been written
+    const float f = some ? exp2_hw(p.m - top) : 0.0f;
     l += lower(p.l, p.m, top);
     exact += lower(p.exact, p.m, top);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) v[k] = fmaf(f, x[k], v[k]);
+    for (int k = 0; k < 4; ++k) v[k] = fmaf(f, some ? x[k] : 0.0f, v[k]);
   }
   const float inv = inverse(l);
   const int64_t head = at - mine * aa.heads;
@@ -148,7 +149,7 @@ __global__ __launch_bounds__(64 * kWaves) void merge_kernel(KvAttendArgs aa, Mer
       const int s = s0 + i * kWaves;
       const float fs = s < src.nsplit ? bits_f32(__builtin_amdgcn_readlane(f32_bits(f), min(s, 63))) : 0.0f;
 #pragma unroll
-      for (int k = 0; k < kPer; ++k) v[k] = fmaf(fs, x[i][k], v[k]);
+      for (int k = 0; k < kPer; ++k) v[k] = fmaf(fs, fs != 0.0f ? x[i][k] : 0.0f, v[k]);
     }
   }
 #pragma unroll

@@ -11,6 +11,7 @@ namespace {
 
 constexpr int kTile = 64;   // keys
 constexpr int kRows = kTreeBlockRows;  // new token x query head of one key/value head
+constexpr int kLeastTiles = 4;  // of a workgroup, where the keys are split
 constexpr int kCopies = 8;  // of a table entry in LDS, for lanes l % 8
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
@@ -69,9 +70,76 @@ __device__ __forceinline__ uint32_t wave_max_bits(uint32_t v) {
 
 __device__ __forceinline__ int exponent(uint32_t bits, int least) { return min(max((int)(bits >> 23) - 126, least), 120); }
 
+// Which part of a call a workgroup takes: of one sequence and key/value head a block of rows and one of n_splits runs of `per` tiles.
+struct Part {
+  int seq, kvh, block, split, per, n_splits;
+};
+
+__device__ __forceinline__ int from_lane(int v, int lane) { return __builtin_amdgcn_readlane(v, lane); }
+
+// The parts are as long as the device can hold at once (`workgroups`); what is left over of each sequence is a part too.  They
+// are numbered in a row, since workgroups without one between the others would leave compute units without work: the
+// hardware deals them out in turn.  The lengths are known on the device only, so every workgroup works this out, a lane to a
+// sequence.  False: there is no such part.
+__device__ __forceinline__ bool find_part(const KvAttendArgs& aa, int group, int nsplit, int workgroups, Part& part) {
+  const int lane = threadIdx.x & 63;
+  int blocks = 0, tiles = 0;  // of the lane's sequence; of all heads
+  auto load = [&](int s) {
+    blocks = tiles = 0;
+    if (s >= aa.num_seqs) return;
+    const int q0 = row_number(aa, aa.q_start[s]), nq = max(row_number(aa, aa.q_start[s + 1]) - q0, 0);
+    const int kv = max(min(aa.kv_len[s], aa.max_kv_len), 0);
+    blocks = (int)((min(nq, aa.max_q_len) * (int64_t)group + kRows - 1) / kRows) * aa.cache.kv_heads;
+    tiles = max((kv + kTile - 1) / kTile - node_first(aa, kv - nq, 0) / kTile, 0);
+  };
+  const int rounds = (aa.num_seqs + 63) / 64;
+  int64_t work = 0;
+  for (int i = 0; i < rounds; ++i) {
+    load(64 * i + lane);
+    work += (int64_t)blocks * tiles;
+  }
+#pragma unroll
+  for (int x = 1; x < 64; x <<= 1) work += __shfl_xor(work, x);
+  int per = __builtin_amdgcn_readfirstlane((int)max((work + workgroups - 1) / workgroups, (int64_t)kLeastTiles));
+  auto per_of = [&]() { return max(per, (tiles + nsplit - 1) / nsplit); };
+  auto splits_of = [&]() { return max((tiles + per_of() - 1) / per_of(), 1); };
+  auto up_to = [&]() {  // parts of this lane's sequence and those before it
+    int n = blocks * splits_of();
+#pragma unroll
+    for (int x = 1; x < 64; x <<= 1) {
+      const int before = __shfl_up(n, x);
+      n += lane >= x ? before : 0;
+    }
+    return n;
+  };
+  if (rounds == 1) {
+    for (int i = 0; i < 12 && from_lane(up_to(), 63) > workgroups; ++i) per += max(per / 16, 1);
+  }
+  int at = blockIdx.x;
+  for (int i = 0; i < rounds; ++i) {
+    if (rounds > 1) load(64 * i + lane);
+    const int n = up_to(), all = from_lane(n, 63);
+    if (at < all) {
+      const int who = __builtin_ctzll(__ballot(at < n));
+      const int mine = from_lane(blocks, who);
+      part.seq = 64 * i + who;
+      part.per = from_lane(per_of(), who);
+      part.n_splits = from_lane(splits_of(), who);
+      at -= from_lane(n, who) - mine * part.n_splits;
+      part.split = at / mine;
+      at -= part.split * mine;
+      part.kvh = at % aa.cache.kv_heads;
+      part.block = at / aa.cache.kv_heads;
+      return true;
+    }
+    at -= all;
+  }
+  return false;
+}
+
 template <int D, int KB, bool FINE>
 __global__ __launch_bounds__(256, (D == 256 || FINE ? 1 : 2)) void tree_kernel(KvAttendArgs aa, DequantArgs da, int nsplit,
-                                                                            float* partial) {
+                                                                            int workgroups, float* partial) {
   using C = Decode<D, KB, FINE>;
   constexpr bool bf16 = !FINE;
   constexpr int kSteps = D / 16, kBlocks = D / 32;
@@ -86,22 +154,27 @@ __global__ __launch_bounds__(256, (D == 256 || FINE ? 1 : 2)) void tree_kernel(K
   const int n = lane & 31, g = lane >> 5;
   const float entry_lo = da.c[KB == 4 ? tid & 15 : tid], entry_hi = da.c[KB == 4 ? tid >> 4 : tid];
   load_fence();
-  const int kvh = blockIdx.x % aa.cache.kv_heads, rest_x = blockIdx.x / aa.cache.kv_heads;
-  const int split = rest_x % nsplit, block = rest_x / nsplit;
-  const int seq = blockIdx.z;
   const int group = aa.heads / aa.cache.kv_heads;
+  Part part;
+  if (!find_part(aa, group, nsplit, workgroups, part)) return;
+  const int kvh = part.kvh, block = part.block, seq = part.seq, split = part.split;
   const Sequence sq = sequence(aa, seq);
   const int nrows = min(sq.nq, aa.max_q_len) * group;
-  if (block * kRows >= nrows) return;
-
   const int last_row = min(block * kRows + kRows, nrows) - 1;
   const int i_first = block * kRows / group, i_last = last_row / group;
   const int context = sq.kv - sq.nq;
   const int first = node_first(aa, context, 0);
   int last = max(min(sq.kv, context + i_last + 1), 0);  // end of the keys that some row may see
   const int begin = first / kTile, end = (last + kTile - 1) / kTile;
-  const int count = max(end - begin, 0), per = (count + nsplit - 1) / nsplit;
-  const int t_first = begin + split * per, t_end = min(t_first + per, end);
+  const int t_first = begin + split * part.per, t_end = min(t_first + part.per, end);
+  // splits without a part: the join passes over them
+  for (int x = part.n_splits + (tid >> 7); split == 0 && x < nsplit; x += 2) {
+    const int r = block * kRows + (tid & 127);
+    if (r < nrows) {
+      const int64_t row = (int64_t)(sq.q0 + r / group) * aa.heads + kvh * group + r % group;
+      reinterpret_cast<Partial*>(partial + aa.tokens * aa.heads * nsplit * D)[row * nsplit + x] = {-INFINITY, 0.0f, 0.0f};
+    }
+  }
   const int lo_all = node_first(aa, context, i_last);
   int hi_all = context;
 
@@ -582,7 +655,7 @@ __global__ __launch_bounds__(256, (D == 256 || FINE ? 1 : 2)) void tree_kernel(K
   const bool sees = depth >= 0;  // a row that sees nothing went along through the context
   const float l = sees ? bits_f32(o2.x) + bits_f32(o2.y) : 0.0f;
   if (!live) return;
-  const int64_t part = (token * aa.heads + head) * nsplit + split;
+  const int64_t to = (token * aa.heads + head) * nsplit + split;
   const float inv = nsplit > 1 ? unit : (l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l)) * unit;
 #pragma unroll
   for (int k = 0; k < kBlocks; ++k)
@@ -593,7 +666,7 @@ __global__ __launch_bounds__(256, (D == 256 || FINE ? 1 : 2)) void tree_kernel(K
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[e] = sees ? acc[k][v + e] * inv : 0.0f;
       if (nsplit > 1) {
-        *reinterpret_cast<f32x4*>(partial + part * D + d) = o;
+        *reinterpret_cast<f32x4*>(partial + to * D + d) = o;
       } else {
         const u32x2 o16 = {pack16(o[0], o[1], bf16), pack16(o[2], o[3], bf16)};
         *reinterpret_cast<u32x2*>(static_cast<char*>(aa.out) + (token * aa.out_stride + (int64_t)head * D + d) * 2) = o16;
@@ -601,30 +674,32 @@ __global__ __launch_bounds__(256, (D == 256 || FINE ? 1 : 2)) void tree_kernel(K
     }
   if (g == 0) {
     const float m = sees ? ref - kHead : -INFINITY;
-    if (nsplit > 1) reinterpret_cast<Partial*>(partial + aa.tokens * aa.heads * nsplit * D)[part] = {m, l, l};
+    if (nsplit > 1) reinterpret_cast<Partial*>(partial + aa.tokens * aa.heads * nsplit * D)[to] = {m, l, l};
     else if (aa.lse != nullptr) aa.lse[token * aa.heads + head] = log_sum(m, l);
   }
 }
 
 template <int D, int KB>
-hipError_t launch_bits(const KvAttendArgs& a, int blocks, int nsplit, bool fine, const DequantArgs& da, hipStream_t s) {
-  const dim3 grid((unsigned)(a.cache.kv_heads * nsplit * blocks), 1u, (unsigned)a.num_seqs);
+hipError_t launch_bits(const KvAttendArgs& a, int grid, int nsplit, int workgroups, bool fine, const DequantArgs& da, hipStream_t s) {
+  float* const partial = static_cast<float*>(a.workspace);
   if constexpr (D == 128) {
-    if (fine) return launch_kernel(tree_kernel<D, KB, true>, grid, dim3(256), s, a, da, nsplit, static_cast<float*>(a.workspace));
+    if (fine) return launch_kernel(tree_kernel<D, KB, true>, dim3((unsigned)grid), dim3(256), s, a, da, nsplit, workgroups, partial);
   }
-  return launch_kernel(tree_kernel<D, KB, false>, grid, dim3(256), s, a, da, nsplit, static_cast<float*>(a.workspace));
+  return launch_kernel(tree_kernel<D, KB, false>, dim3((unsigned)grid), dim3(256), s, a, da, nsplit, workgroups, partial);
 }
 
 }  // namespace
 
 int tree_block_slots(int head_dim, int dtype) { return cu_count() * (head_dim == 256 || dtype == F16 ? 1 : 2); }
 
-int launch_tree_blocks(const KvAttendArgs& a, int dtype, int blocks, int nsplit, const DequantArgs& da, void* stream) {
+int launch_tree_blocks(const KvAttendArgs& a, int dtype, int grid, int nsplit, int workgroups, const DequantArgs& da, void* stream) {
   const hipStream_t s = static_cast<hipStream_t>(stream);
   const bool fine = dtype == F16;
   if (a.cache.head_dim == 128)
-    return (int)(da.K == 16 ? launch_bits<128, 4>(a, blocks, nsplit, fine, da, s) : launch_bits<128, 8>(a, blocks, nsplit, fine, da, s));
-  return (int)(da.K == 16 ? launch_bits<256, 4>(a, blocks, nsplit, fine, da, s) : launch_bits<256, 8>(a, blocks, nsplit, fine, da, s));
+    return (int)(da.K == 16 ? launch_bits<128, 4>(a, grid, nsplit, workgroups, fine, da, s)
+                            : launch_bits<128, 8>(a, grid, nsplit, workgroups, fine, da, s));
+  return (int)(da.K == 16 ? launch_bits<256, 4>(a, grid, nsplit, workgroups, fine, da, s)
+                          : launch_bits<256, 8>(a, grid, nsplit, workgroups, fine, da, s));
 }
 
 }  // namespace bq

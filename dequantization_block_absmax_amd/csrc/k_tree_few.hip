@@ -13,16 +13,19 @@ namespace {
 struct TreePlan {
   bool blocks;      // k_tree.hip
   int rt, tiles, nsplit;
+  int64_t workgroups, grid;
   size_t bytes;
 };
 
-// The splits of the keys whose rounds of resident workgroups take the least time, a workgroup costing its steps and
-// `more` of them for its start, its end and its part of the join.
-int64_t choose_splits(int64_t base, int64_t slots, int64_t steps, int64_t most_steps, int64_t more) {
+// Splits of the keys: those whose rounds of resident workgroups (`slots`; `base` without splits) take the least time, a
+// workgroup costing its steps of 256 keys and about 3 more.  With several sequences, whose lengths may differ, a workgroup
+// takes 8192 keys at most.
+int64_t choose_splits(int64_t base, int64_t slots, int64_t keys, int num_seqs) {
+  const int64_t steps = (keys + 255) / 256;
+  const int64_t least = num_seqs > 1 ? std::max((steps + 31) / 32, (int64_t)1) : 1;
   int64_t best = INT64_MAX, n = 1;
-  const int64_t least = std::max((steps + most_steps - 1) / most_steps, (int64_t)1);
   for (int64_t k = std::min(least, (int64_t)kMaxSplits); k <= kMaxSplits && (k <= steps || k <= 1); ++k) {
-    const int64_t cost = (base * k + slots - 1) / slots * ((steps + k - 1) / k + more);
+    const int64_t cost = (base * k + slots - 1) / slots * ((steps + k - 1) / k + 3);
     if (cost < best) {
       best = cost;
       n = k;
@@ -37,27 +40,35 @@ TreePlan make_plan(const KvAttendArgs& a, int dtype) {
   TreePlan p = {};
   const int64_t group = a.heads / a.cache.kv_heads, D = a.cache.head_dim, cus = cu_count();
   const int64_t rows = a.max_q_len * group;
-  p.blocks = rows > kFewRowsOfTree && (D == 128 || (D == 256 && dtype != F16));
-  int64_t per, slots;  // rows of a workgroup
+  p.blocks = rows > kFewRowsOfTree && a.num_seqs <= 1024 && (D == 128 || (D == 256 && dtype != F16));
+  int64_t n;
   if (p.blocks) {
-    per = kTreeBlockRows;
-    slots = tree_block_slots(a.cache.head_dim, dtype);
+    p.tiles = (int)((rows + kTreeBlockRows - 1) / kTreeBlockRows);
+    const int64_t tiles = ((int64_t)a.max_kv_len + 63) / 64;
+    const int64_t base = a.cache.kv_heads * std::min((int64_t)p.tiles * a.num_seqs, a.tokens * group / kTreeBlockRows + a.num_seqs);
+    // as many workgroups as the device holds at once, or a multiple
+    const int64_t slots = tree_block_slots(a.cache.head_dim, dtype);
+    p.workgroups = (base + slots - 1) / slots * slots;
+    // splits of the longest if all are as long, and room for as many more where the others are shorter
+    const int64_t per = std::max((base * tiles + p.workgroups - 1) / p.workgroups, (int64_t)4);
+    n = (tiles + per - 1) / per;
+    if (a.num_seqs > 1) n = std::min(2 * n, (tiles + 3) / 4);
+    n = std::max(std::min(n, (int64_t)kMaxSplits), (int64_t)1);
+    // what is left over of each sequence is a part of its own
+    p.grid = std::min(base * n, p.workgroups + base);
   } else {
     p.rt = D > 128 || rows <= 16 ? 1 : rows <= 32 || D == 128 ? 2 : 4;
-    per = 16 * p.rt;
+    const int64_t per = 16 * p.rt;
     const int nb = a.cache.head_dim >> a.cache.log2b;
-    slots = cus * (D == 256 || nb == 4 || p.rt * D > 128 || wide_form((int)D, nb, a.bits, p.rt) ? 1 : 2);
+    const int64_t slots = cus * (D == 256 || nb == 4 || p.rt * D > 128 || wide_form((int)D, nb, a.bits, p.rt) ? 1 : 2);
+    p.tiles = (int)((rows + per - 1) / per);
+    // tiles with rows in them: sequences may bring fewer tokens than the longest
+    const int64_t base = a.cache.kv_heads * std::min((int64_t)p.tiles * a.num_seqs, a.tokens * group / per + a.num_seqs);
+    // the workspace is asked for without a window, and holds for any
+    n = choose_splits(base, slots, a.max_kv_len, a.num_seqs);
+    if (a.window > 0 && (int64_t)a.window + a.max_q_len < a.max_kv_len)
+      n = std::min(n, choose_splits(base, slots, (int64_t)a.window + a.max_q_len, a.num_seqs));
   }
-  p.tiles = (int)((rows + per - 1) / per);
-  // tiles with rows in them: sequences may bring fewer tokens than the longest
-  const int64_t base = a.cache.kv_heads * std::min((int64_t)p.tiles * a.num_seqs, a.tokens * group / per + a.num_seqs);
-  const int64_t step = p.blocks ? 64 : 256;
-  auto splits = [&](int64_t keys) {
-    return choose_splits(base, slots, (keys + step - 1) / step, a.num_seqs > 1 ? 8192 / step : INT64_MAX / 2, p.blocks ? 8 : 3);
-  };
-  // the workspace is asked for without a window, and holds for any
-  int64_t n = splits(a.max_kv_len);
-  if (a.window > 0 && (int64_t)a.window + a.max_q_len < a.max_kv_len) n = std::min(n, splits((int64_t)a.window + a.max_q_len));
   p.nsplit = (int)n;
   if (n > 1) p.bytes = (size_t)a.tokens * a.heads * n * (D + 3) * 4;
   return p;
@@ -108,11 +119,11 @@ size_t kv_tree_workspace(const KvAttendArgs& a, int dtype) { return make_plan(a,
 int launch_kv_tree(const KvAttendArgs& a, int dtype, const DequantArgs& da, void* stream) {
   const TreePlan p = make_plan(a, dtype);
   if ((int64_t)p.tiles * p.nsplit > UINT32_MAX / 512 || a.cache.kv_heads > 32767 || (p.nsplit > 1 && !kv_merge_fits(a)) ||
-      (p.blocks && (int64_t)a.cache.kv_heads * p.tiles * p.nsplit > UINT32_MAX / 256)) {
+      (p.blocks && p.grid > UINT32_MAX / 256)) {
     g_launch_refused_for_size = true;
     return (int)hipErrorInvalidConfiguration;
   }
-  const int e = p.blocks ? launch_tree_blocks(a, dtype, p.tiles, p.nsplit, da, stream)
+  const int e = p.blocks ? launch_tree_blocks(a, dtype, (int)p.grid, p.nsplit, (int)p.workgroups, da, stream)
                          : (int)launch_few(a, p, dtype, da, static_cast<hipStream_t>(stream));
   if (e != 0 || p.nsplit <= 1) return e;
   const MergeArgs m = {{static_cast<float*>(a.workspace), nullptr}, {p.nsplit, 0}, 0, 0};
