@@ -76,7 +76,7 @@ int launch_kv_attend(const KvAttendArgs& a, int dtype, const DequantArgs& da, vo
 // Attention of a tree of new tokens (k_tree_few.hip, k_tree.hip), at most kMostNodes to a sequence.
 constexpr int kMostNodes = 256;
 constexpr int kTreeBlockRows = 128;  // of a workgroup of k_tree.hip
-int tree_block_slots(int head_dim, int dtype);  // workgroups of that kernel the device holds at once
+int tree_block_slots();  // workgroups of that kernel the device holds at once
 // The call spread over about `workgroups` workgroups, of `grid` at most; a block of rows takes up to nsplit.
 int launch_tree_blocks(const KvAttendArgs& a, int dtype, int grid, int nsplit, int workgroups, const DequantArgs& da, void* stream);
 size_t kv_tree_workspace(const KvAttendArgs& a, int dtype);

@@ -12,7 +12,7 @@ namespace {
 constexpr int kTile = 64;   // keys
 constexpr int kRows = kTreeBlockRows;  // new token x query head of one key/value head
 constexpr int kLeastTiles = 4;  // of a workgroup, where the keys are split
-constexpr int kCopies = 8;  // of a table entry in LDS, for lanes l % 8
+constexpr int kThreads = 512;  // four waves with 32 rows each, and four that decode
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
@@ -26,7 +26,7 @@ constexpr int kKeySpread = 12, kValueSpread = 4;
 constexpr int kLeastKey = -100, kLeastValue = -80;
 constexpr float kHead = 3.0f;
 
-// A thread decodes D / 4 consecutive d of one key: lane = key, wave = quarter of the head.
+// A decoding thread takes D / 4 consecutive d of one key: lane = key, wave = quarter of the head.
 template <int D, int KB, bool FINE>
 struct Decode {
   static constexpr int kPart = D / 4;
@@ -34,10 +34,8 @@ struct Decode {
   static constexpr int kRow = D * KB / 8;            // bytes of a key's codes
   static constexpr int kWords = kPart * KB / 32;     // of a thread's codes
   static constexpr int kPieceWords = KB / 4;
-  static constexpr int kOwn = D == 256 ? 2 : 1;      // blocks that a thread's d may belong to
   static constexpr int kBlocks = D / 32;             // most blocks of a head
   static constexpr int kEntry = FINE && KB == 4 ? 8 : 4;  // bytes of a table entry
-  static constexpr int kTable = 256 * kCopies * kEntry;
   static constexpr int kLookups = KB == 4 ? 4 : 8;   // of a piece
   typedef std::conditional_t<FINE && KB == 4, f32x2, uint32_t> Entry;
 };
@@ -46,16 +44,18 @@ struct Decode {
 template <int D, int KB, bool FINE>
 struct Raw {
   uint32_t code[Decode<D, KB, FINE>::kWords];
-  float a[Decode<D, KB, FINE>::kOwn];     // of its own d
+  float a;                                  // of its own d
   float all[Decode<D, KB, FINE>::kBlocks];  // of the whole head
 };
 
-// What there is to know of a tile of one side: 2^e above its largest maximum; its keys' own exponents (of the lane's key)
-// where they are apart.
-struct Scale {
-  int e, own;
-  bool apart;
+// What there is to know of a tile, left in LDS for the waves that multiply: of its keys and of its values 2^e above the largest
+// maximum and, where they are apart, every key's own exponents; which keys some row sees.
+struct Info {
+  int e[2], apart;
+  uint64_t keys;
+  int8_t own[2][kTile];
 };
+constexpr int kInfos = 4;  // a tile's is read until two tiles later, while the next but one's is written
 
 __device__ __forceinline__ uint32_t wave_max_bits(uint32_t v) {
   v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, false));
@@ -138,8 +138,7 @@ __device__ __forceinline__ bool find_part(const KvAttendArgs& aa, int group, int
 }
 
 template <int D, int KB, bool FINE>
-__global__ __launch_bounds__(256, (D == 256 || FINE ? 1 : 2)) void tree_kernel(KvAttendArgs aa, DequantArgs da, int nsplit,
-                                                                            int workgroups, float* partial) {
+__global__ __launch_bounds__(kThreads, 2) void tree_kernel(KvAttendArgs aa, DequantArgs da, int nsplit, int workgroups, float* partial) {
   using C = Decode<D, KB, FINE>;
   constexpr bool bf16 = !FINE;
   constexpr int kSteps = D / 16, kBlocks = D / 32;
@@ -147,12 +146,18 @@ __global__ __launch_bounds__(256, (D == 256 || FINE ? 1 : 2)) void tree_kernel(K
   __shared__ u32x4 s_key[2][kTilePieces];
   __shared__ __attribute__((aligned(16))) char s_value[2][kTilePieces * 16];
   __shared__ __attribute__((aligned(16))) uint32_t s_rest[2][FINE ? 12 * D : 4];
-  __shared__ __attribute__((aligned(16))) char s_table[C::kTable];
+  __shared__ __attribute__((aligned(16))) char s_table[256 * kEntryBytes];
+  __shared__ Info s_info[kInfos];
   __shared__ TreeShared<kRows> s_tree;
   const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6) & 3;
+  const bool decodes = __builtin_amdgcn_readfirstlane(tid >> 8);
   const int n = lane & 31, g = lane >> 5;
-  const float entry_lo = da.c[KB == 4 ? tid & 15 : tid], entry_hi = da.c[KB == 4 ? tid >> 4 : tid];
+  float entry_lo = 0.0f, entry_hi = 0.0f;
+  if (decodes) {
+    entry_lo = da.c[KB == 4 ? tid & 15 : tid & 255];
+    entry_hi = da.c[KB == 4 ? tid >> 4 & 15 : tid & 255];
+  }
   load_fence();
   const int group = aa.heads / aa.cache.kv_heads;
   Part part;
@@ -168,7 +173,7 @@ __global__ __launch_bounds__(256, (D == 256 || FINE ? 1 : 2)) void tree_kernel(K
   const int begin = first / kTile, end = (last + kTile - 1) / kTile;
   const int t_first = begin + split * part.per, t_end = min(t_first + part.per, end);
   // splits without a part: the join passes over them
-  for (int x = part.n_splits + (tid >> 7); split == 0 && x < nsplit; x += 2) {
+  for (int x = part.n_splits + (tid >> 7); split == 0 && x < nsplit; x += kThreads / 128) {
     const int r = block * kRows + (tid & 127);
     if (r < nrows) {
       const int64_t row = (int64_t)(sq.q0 + r / group) * aa.heads + kvh * group + r % group;
@@ -198,32 +203,35 @@ __global__ __launch_bounds__(256, (D == 256 || FINE ? 1 : 2)) void tree_kernel(K
       for (int e = 0; e < 4; ++e) x.code[k + e] = v[e];
     }
     const float* a = aa.cache.absmax[side] + row * nb;
-#pragma unroll
-    for (int b = 0; b < C::kOwn; ++b) x.a[b] = a[(wave * C::kPart + 32 * b) >> log2b];
+    x.a = a[wave * C::kPart >> log2b];
 #pragma unroll
     for (int b = 0; b < C::kBlocks; ++b) x.all[b] = a[min(b, nb - 1)];
   };
-  Raw<D, KB, FINE> xk, xv;
-  int id_first = 0, id = 0, id_next = 0;  // pages of the lane's keys of tiles t, t + 1, t + 2
-  if (t_first < t_end) {
-    id_first = page_of(t_first);
+  Raw<D, KB, FINE> xk, xv;  // of tiles t + 1 and t
+  int id_now = 0, id = 0, id_next = 0;  // pages of the lane's keys of tiles t, t + 1, t + 2
+  if (decodes && t_first < t_end) {
+    id_now = page_of(t_first);
     id = page_of(t_first + 1);
     id_next = page_of(t_first + 2);
-    const int64_t row = row_of(t_first, id_first);
-    fetch(xk, 0, row);
-    fetch(xv, 1, row);
+    fetch(xk, 0, row_of(t_first, id_now));
+    fetch(xv, 1, row_of(t_first, id_now));
   }
 
-  {  // table
+  if (decodes) {  // table
     const float x0 = __builtin_ldexpf(entry_lo, kTopBit), x1 = __builtin_ldexpf(entry_hi, kTopBit);
     const uint32_t w = pack_f16(x1, x0);
     const u32x4 e = FINE && KB == 4 ? (u32x4){f32_bits(x1), f32_bits(x0), f32_bits(x1), f32_bits(x0)}
                     : FINE          ? (u32x4){f32_bits(x0), f32_bits(x0), f32_bits(x0), f32_bits(x0)}
                                     : (u32x4){w, w, w, w};
+    const int to = tid & 255;
 #pragma unroll
-    for (int i = 0; i < kCopies * C::kEntry / 16; ++i) *reinterpret_cast<u32x4*>(s_table + (tid * kCopies * C::kEntry / 16 + i) * 16) = e;
+    for (int i = 0; i < kEntryBytes / 16; ++i)  // in turn over the banks
+      *reinterpret_cast<u32x4*>(s_table + to * kEntryBytes + ((i + to) & (kEntryBytes / 16 - 1)) * 16) = e;
+#pragma unroll
+    for (int i = 0; i < kTilePieces / 256; ++i)  // no weights wait at first
+      *reinterpret_cast<u32x4*>(s_value[1] + (i * 256 + to) * 16) = (u32x4){0, 0, 0, 0};
   }
-  const uint32_t copy = (lane & (kCopies - 1)) * C::kEntry;
+  const uint32_t copy = (lane * C::kEntry) & (kEntryBytes - 1);
 
   // Queries as operands: binary16 relative to a power of two of the row, the scale's sign included.
   const int r = block * kRows + wave * 32 + n;
@@ -231,10 +239,10 @@ __global__ __launch_bounds__(256, (D == 256 || FINE ? 1 : 2)) void tree_kernel(K
   const int row_i = live ? r / group : i_first;
   const int head = kvh * group + (live ? r - row_i * group : 0);
   const int64_t token = sq.q0 + row_i;
-  float scale;
+  float scale = 0.0f;
   f16x8 q[kSteps];
   i32x8 q_rest[FINE ? D / 64 : 1];  // four times q, in 6 bits
-  {
+  if (!decodes) {
     // d = 8 (2 s + g) .. + 7 for step s
     const char* src = static_cast<const char*>(aa.q) + (token * aa.q_stride + (int64_t)head * D + 8 * g) * 2;
     u32x4 w[kSteps];
@@ -284,7 +292,7 @@ __global__ __launch_bounds__(256, (D == 256 || FINE ? 1 : 2)) void tree_kernel(K
     }
     scale = __builtin_ldexpf(fabsf(aa.scale) * 1.44269504088896341f, ex);
   }
-  read_tree<256, kRows>(aa, s_tree, parent, tid, i_first, i_last);
+  read_tree<kThreads, kRows>(aa, s_tree, parent, tid, i_first, i_last);
   __syncthreads();  // table and tree are in place
   if (!any_node(s_tree, i_first, i_last)) last = hi_all = 0;  // no row of the block sees any key: theirs may hold anything
   const int depth = s_tree.depth[row_i - i_first];
@@ -299,8 +307,9 @@ __global__ __launch_bounds__(256, (D == 256 || FINE ? 1 : 2)) void tree_kernel(K
   };
 
   // ---- decoding
-  float ka[C::kOwn], va[C::kOwn];  // block maxima of the d that the thread decodes, relative to the tile's (or the key's) exponent
-  auto scale_tile = [&](const Raw<D, KB, FINE>& x, int side, bool seen_key, float (&a)[C::kOwn]) {
+  // The exponent of a tile's side and whether its keys are apart, into the tile's Info; returns the block maximum of the d that the
+  // thread decodes, relative to the tile's exponent or the key's own.
+  auto scale_tile = [&](const Raw<D, KB, FINE>& x, int side, bool seen_key, Info& info) {
     uint32_t top = 0;
 #pragma unroll
     for (int b = 0; b < C::kBlocks; ++b) top = max(top, f32_bits(x.all[b]) & 0x7fffffffu);
@@ -308,26 +317,25 @@ __global__ __launch_bounds__(256, (D == 256 || FINE ? 1 : 2)) void tree_kernel(K
     const bool say = seen_key && (side == 1 || top != 0);  // zero keys, whose scores are zero at any scale, have none
     const int least = side == 0 ? kLeastKey : kLeastValue;
     const uint32_t most = wave_max_bits(say ? top : 0u), low = ~wave_max_bits(say ? ~top : 0u);
-    Scale s;
-    s.e = exponent(most, least);
-    s.apart = low <= most && s.e - exponent(low, least) > (side == 0 ? kKeySpread : kValueSpread);
-    s.own = s.apart && say ? exponent(top, least) : s.e;
-#pragma unroll
-    for (int b = 0; b < C::kOwn; ++b) a[b] = seen_key ? __builtin_ldexpf(x.a[b], -s.own) : 0.0f;
-    return s;
+    const int e = exponent(most, least);
+    const bool apart = low <= most && e - exponent(low, least) > (side == 0 ? kKeySpread : kValueSpread);
+    const int own = apart && say ? exponent(top, least) : e;
+    if (wave == 0) {
+      info.own[side][lane] = (int8_t)own;
+      if (lane == 0) {
+        info.e[side] = e;
+        info.apart = side == 0 ? (int)apart : info.apart | (int)apart << 1;
+      }
+    }
+    return seen_key ? __builtin_ldexpf(x.a, -own) : 0.0f;
   };
-  auto entry_at = [&](uint32_t w, int b) {
-    constexpr int shift = __builtin_ctz(kCopies * C::kEntry);
-    const uint32_t at = ((b == 0 ? w & 255u : b == 3 ? w >> 24 : __builtin_amdgcn_ubfe(w, 8 * b, 8)) << shift) | copy;
-    return *reinterpret_cast<const typename C::Entry*>(s_table + at);
-  };
-  auto look_up = [&](const Raw<D, KB, FINE>& x, int i, typename C::Entry (&e)[C::kLookups]) {
+  auto entry_at = [&](uint32_t w, int b) { return *reinterpret_cast<const typename C::Entry*>(s_table + entry_of(w, b, copy)); };
+  auto look_up = [&](const uint32_t (&code)[C::kWords], int i, typename C::Entry (&e)[C::kLookups]) {
 #pragma unroll
-    for (int k = 0; k < C::kLookups; ++k) e[k] = entry_at(x.code[i * C::kPieceWords + k / 4], k & 3);
+    for (int k = 0; k < C::kLookups; ++k) e[k] = entry_at(code[i * C::kPieceWords + k / 4], k & 3);
   };
   // The 8 values of piece i: rounded once to binary16, and what that left (times the tile's power of two).
-  auto products = [&](const float (&factor)[C::kOwn], int i, const typename C::Entry (&e)[C::kLookups], f16x8* left) {
-    const float a = factor[C::kOwn > 1 ? i / 4 : 0];
+  auto products = [&](float a, const typename C::Entry (&e)[C::kLookups], f16x8* left) {
     u32x4 h;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -385,9 +393,9 @@ __global__ __launch_bounds__(256, (D == 256 || FINE ? 1 : 2)) void tree_kernel(K
     }
   };
   // Piece i of the keys from its entries, with what rounding left of it.
-  auto finish_key = [&](int b, int i, const typename C::Entry (&e)[C::kLookups]) {
+  auto finish_key = [&](int b, int i, float a, const typename C::Entry (&e)[C::kLookups]) {
     f16x8 l;
-    put_key(b, i, products(ka, i, e, FINE ? &l : nullptr));
+    put_key(b, i, products(a, e, FINE ? &l : nullptr));
     if constexpr (FINE) {
 #pragma unroll
       for (int k = 0; k < 8; ++k) left[8 * (i & 3) + k] = l[k];
@@ -443,15 +451,22 @@ __global__ __launch_bounds__(256, (D == 256 || FINE ? 1 : 2)) void tree_kernel(K
     return z;
   };
 
-  struct Info {
-    Scale k, v;
-    uint64_t keys;  // that some row sees
+  // A tile's Info as the waves that multiply hold it.
+  struct Known {
+    int ek, ev, apart;
+    uint64_t keys;
+  };
+  auto known = [&](int t) {
+    const Info& x = s_info[t & (kInfos - 1)];
+    return Known{__builtin_amdgcn_readfirstlane(x.e[0]), __builtin_amdgcn_readfirstlane(x.e[1]), __builtin_amdgcn_readfirstlane(x.apart),
+                 (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)x.keys) |
+                     (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(x.keys >> 32)) << 32};
   };
   // The half step of half `half` of tile t: next_b, prev_b: the buffers of the keys whose scores follow and of the values that
-  // the other half's weights belong to; beside every second product, move(k) decodes a piece.
-  auto half_step = [&](auto half_c, int t, const Info& info, int next_b, int prev_b, auto move) {
+  // the other half's weights belong to.
+  auto half_step = [&](auto half_c, int t, const Known& info, int next_b, int prev_b) {
     constexpr int half = half_c.value;
-    const float ev = (float)info.v.e;
+    const float ev = (float)info.ev;
     const int j0 = t * kTile + 32 * half;
     const uint32_t keys = half ? (uint32_t)(info.keys >> 32) : (uint32_t)info.keys;
     f32x16& s = sc[half];
@@ -465,14 +480,14 @@ __global__ __launch_bounds__(256, (D == 256 || FINE ? 1 : 2)) void tree_kernel(K
     for (int z = 0; z < kAhead; ++z) a[z] = operand(z);
     __builtin_amdgcn_sched_barrier(0);
     asm volatile("s_nop 15");  // max3_hw is no instruction that the compiler waits for a matrix product before
-    float f = fmaxf(__builtin_ldexpf(scale, info.k.e - kTopBit), 0x1p-100f);
+    float f = fmaxf(__builtin_ldexpf(scale, info.ek - kTopBit), 0x1p-100f);
     // of the lane's keys 8 i + 4 g + e, element 4 i + e
-    auto own_of = [&](const Scale& x, int v) { return __shfl(x.own, 32 * half + 8 * (v >> 2) + 4 * g + (v & 3)); };
-    if (info.k.apart || info.v.apart) {  // rare: the scores to the tile's units, the values' exponents beside them
+    auto own_of = [&](int side, int v) { return (int)s_info[t & (kInfos - 1)].own[side][32 * half + 8 * (v >> 2) + 4 * g + (v & 3)]; };
+    if (info.apart) {  // rare: the scores to the tile's units, the values' exponents beside them
       const float inv = 1.0f / f;
 #pragma unroll
       for (int v = 0; v < 16; ++v)
-        s[v] = fmaf((float)(own_of(info.v, v) - info.v.e), inv, __builtin_ldexpf(s[v], own_of(info.k, v) - info.k.e));
+        s[v] = fmaf((float)(own_of(1, v) - info.ev), inv, __builtin_ldexpf(s[v], own_of(0, v) - info.ek));
     }
     if (!(j0 >= lo_all && j0 + 32 <= hi_all && keys == ~0u)) {  // some key hidden from some row
       const int from = j0 - context;
@@ -526,7 +541,6 @@ __global__ __launch_bounds__(256, (D == 256 || FINE ? 1 : 2)) void tree_kernel(K
         if (z % 8 == 7) z_next = add_rest(half ^ 1, z / 8, s_rest[next_b], z_next);
       }
       if (z + kAhead < kMul) a[z + kAhead] = operand(z + kAhead);
-      if (z & 1) move(z >> 1);
 #pragma unroll
       for (int v = z * 16 / kMul; v < (z + 1) * 16 / kMul; ++v) {
         weigh(v, c);
@@ -568,74 +582,72 @@ __global__ __launch_bounds__(256, (D == 256 || FINE ? 1 : 2)) void tree_kernel(K
       if constexpr (FINE) wl[half][ks] = y[ks];
     }
     // The denominator, in weights that do not hold the exponent.
-    most_ev = max(most_ev, info.v.e);
-    if (info.v.apart || info.v.e < most_ev - 60) {
+    most_ev = max(most_ev, info.ev);
+    if (info.apart >> 1 || info.ev < most_ev - 60) {
       float more = 0.0f;
 #pragma unroll
-      for (int v = 0; v < 16; ++v) more += exp2_hw(fmaf(s[v], f, c) - (float)own_of(info.v, v));
+      for (int v = 0; v < 16; ++v) more += exp2_hw(fmaf(s[v], f, c) - (float)own_of(1, v));
       sum += more;
     } else {
-      sum += __builtin_ldexpf(part, -info.v.e);
+      sum += __builtin_ldexpf(part, -info.ev);
     }
   };
 
   if (t_first < t_end) {
-    auto keys_of = [&](int t, int page) { return (uint64_t)__ballot(counts(t, page)); };
-    Info info;
-    info.keys = keys_of(t_first, id_first);
-    info.k = scale_tile(xk, 0, info.keys >> lane & 1, ka);
-    info.v = scale_tile(xv, 1, info.keys >> lane & 1, va);
+    // The decoding waves are a tile ahead: while tile t is multiplied, they find out what there is to know of tile t + 1,
+    // decode its keys and the values of tile t, whose codes and factor they have held since.  A tile's codes are asked for
+    // an interval before that.
+    uint32_t held[C::kWords];
+    float held_a = 0.0f;
+    auto decode = [&](int t, int page, int64_t row_after, bool values) {  // t: the tile whose keys it is
+      const Raw<D, KB, FINE> k = xk, v = xv;
+      fetch(xk, 0, row_after);
+      fetch(xv, 1, row_after);
+      Info& info = s_info[t & (kInfos - 1)];
+      const uint64_t keys = __ballot(counts(min(t, t_end - 1), page));
+      const bool seen_key = keys >> lane & 1;
+      if (wave == 0 && lane == 0) info.keys = keys;
+      const float ka = scale_tile(k, 0, seen_key, info), va = scale_tile(v, 1, seen_key, info);
+      const int b = (t - t_first) & 1;
 #pragma unroll
-    for (int i = 0; i < C::kPieces; ++i) {
-      typename C::Entry e[C::kLookups];
-      look_up(xk, i, e);
-      finish_key(0, i, e);
-      look_up(xv, i, e);
-      put_value(0, i, products(va, i, e, nullptr));
-      *reinterpret_cast<u32x4*>(s_value[1] + (i * 256 + tid) * 16) = (u32x4){0, 0, 0, 0};  // no weights wait at first
+      for (int i = 0; i < C::kPieces; ++i) {
+        typename C::Entry e[C::kLookups];
+        look_up(k.code, i, e);
+        finish_key(b, i, ka, e);
+      }
+      if (values) {
+#pragma unroll
+        for (int i = 0; i < C::kPieces; ++i) {
+          typename C::Entry e[C::kLookups];
+          look_up(held, i, e);
+          put_value(b ^ 1, i, products(held_a, e, nullptr));
+        }
+      }
+#pragma unroll
+      for (int x = 0; x < C::kWords; ++x) held[x] = v.code[x];
+      held_a = va;
+    };
+    // Both kinds of wave pass as many barriers.
+    if (decodes) {
+      decode(t_first, id_now, row_of(t_first + 1, id), false);
+      __syncthreads();
+      for (int t = t_first; t < t_end; ++t) {
+        const int page = id;
+        id = id_next;
+        id_next = page_of(t + 3);
+        decode(t + 1, page, row_of(t + 2, id), true);
+        __syncthreads();
+      }
+      return;
     }
-    fetch(xk, 0, row_of(t_first + 1, id));
-    fetch(xv, 1, row_of(t_first + 1, id));
     __syncthreads();
     sc[0] = multiply_keys(0, 0);
     for (int t = t_first; t < t_end; ++t) {
       const int b = (t - t_first) & 1;
-      Info next;
-      next.keys = keys_of(min(t + 1, t_end - 1), id);
-      const bool seen_key = next.keys >> lane & 1;
-      // Beside the products the next tile is decoded: its keys into the buffer last read before the previous barrier, its
-      // values, past the barrier, into that of the tile before.
-      next.k = scale_tile(xk, 0, seen_key, ka);
-      // Entries are asked for two pieces ahead of their products, and the following tile's codes as soon as the last are.
-      typename C::Entry e[2][C::kLookups];
-      const int page = id_next;
-      const int64_t row = row_of(t + 2, page);
-      id_next = page_of(t + 3);
-      auto keys_move = [&](int i) {  // what stands before piece i's products
-        if (i >= 2 && i < C::kPieces + 2) finish_key(b ^ 1, i - 2, e[i & 1]);
-        if (i < C::kPieces) look_up(xk, i, e[i & 1]);
-        if (i == C::kPieces) fetch(xk, 0, row);
-      };
-      auto values_move = [&](int i) {
-        if (i >= 2 && i < C::kPieces + 2) put_value(b ^ 1, i - 2, products(va, i - 2, e[i & 1], nullptr));
-        if (i < C::kPieces) look_up(xv, i, e[i & 1]);
-        if (i == C::kPieces) fetch(xv, 1, row);
-      };
-      constexpr int kMoves = D / 16, kPer = C::kPieces + 2 <= kMoves ? kMoves / (C::kPieces + 2) : 1;
-      half_step(std::integral_constant<int, 0>(), t, info, b, b ^ 1, [&](int k) {
-        if (k % kPer == 0) keys_move(k / kPer);
-      });
-#pragma unroll
-      for (int i = (kMoves + kPer - 1) / kPer; i < C::kPieces + 2; ++i) keys_move(i);
-      id = page;
-      __syncthreads();
-      next.v = scale_tile(xv, 1, seen_key, va);
-      half_step(std::integral_constant<int, 1>(), t, info, b ^ 1, b, [&](int k) {
-        if (k % kPer == 0) values_move(k / kPer);
-      });
-#pragma unroll
-      for (int i = (kMoves + kPer - 1) / kPer; i < C::kPieces + 2; ++i) values_move(i);
-      info = next;
+      const Known info = known(t);
+      half_step(std::integral_constant<int, 0>(), t, info, b, b ^ 1);
+      __syncthreads();  // the next tile's keys and this one's values are there; their buffers' last tiles are done with
+      half_step(std::integral_constant<int, 1>(), t, info, b ^ 1, b);
     }
     // the last half's weights
     const int b = (t_end - 1 - t_first) & 1;
@@ -649,6 +661,7 @@ __global__ __launch_bounds__(256, (D == 256 || FINE ? 1 : 2)) void tree_kernel(K
           acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, __builtin_bit_cast(f16x8, wl[1][ks]), acc[i], 0, 0, 0);
       }
   }
+  if (decodes) return;
 
   const u32x2 o2 = __builtin_amdgcn_permlane32_swap(f32_bits(sum), f32_bits(sum), false, false);
   const float unit = __builtin_ldexpf(1.0f, -kTopBit);  // of the sums beside those of the weights
@@ -679,27 +692,20 @@ __global__ __launch_bounds__(256, (D == 256 || FINE ? 1 : 2)) void tree_kernel(K
   }
 }
 
-template <int D, int KB>
+template <int KB>
 hipError_t launch_bits(const KvAttendArgs& a, int grid, int nsplit, int workgroups, bool fine, const DequantArgs& da, hipStream_t s) {
-  float* const partial = static_cast<float*>(a.workspace);
-  if constexpr (D == 128) {
-    if (fine) return launch_kernel(tree_kernel<D, KB, true>, dim3((unsigned)grid), dim3(256), s, a, da, nsplit, workgroups, partial);
-  }
-  return launch_kernel(tree_kernel<D, KB, false>, dim3((unsigned)grid), dim3(256), s, a, da, nsplit, workgroups, partial);
+  return launch_kernel(fine ? tree_kernel<128, KB, true> : tree_kernel<128, KB, false>, dim3((unsigned)grid), dim3(kThreads), s, a, da,
+                       nsplit, workgroups, static_cast<float*>(a.workspace));
 }
 
 }  // namespace
 
-int tree_block_slots(int head_dim, int dtype) { return cu_count() * (head_dim == 256 || dtype == F16 ? 1 : 2); }
+int tree_block_slots() { return cu_count(); }
 
 int launch_tree_blocks(const KvAttendArgs& a, int dtype, int grid, int nsplit, int workgroups, const DequantArgs& da, void* stream) {
   const hipStream_t s = static_cast<hipStream_t>(stream);
-  const bool fine = dtype == F16;
-  if (a.cache.head_dim == 128)
-    return (int)(da.K == 16 ? launch_bits<128, 4>(a, grid, nsplit, workgroups, fine, da, s)
-                            : launch_bits<128, 8>(a, grid, nsplit, workgroups, fine, da, s));
-  return (int)(da.K == 16 ? launch_bits<256, 4>(a, grid, nsplit, workgroups, fine, da, s)
-                          : launch_bits<256, 8>(a, grid, nsplit, workgroups, fine, da, s));
+  return (int)(da.K == 16 ? launch_bits<4>(a, grid, nsplit, workgroups, dtype == F16, da, s)
+                          : launch_bits<8>(a, grid, nsplit, workgroups, dtype == F16, da, s));
 }
 
 }  // namespace bq

@@ -36,18 +36,18 @@ int64_t choose_splits(int64_t base, int64_t slots, int64_t keys, int num_seqs) {
 
 constexpr int64_t kFewRowsOfTree = 32;
 
-TreePlan make_plan(const KvAttendArgs& a, int dtype) {
+TreePlan make_plan(const KvAttendArgs& a) {
   TreePlan p = {};
   const int64_t group = a.heads / a.cache.kv_heads, D = a.cache.head_dim, cus = cu_count();
   const int64_t rows = a.max_q_len * group;
-  p.blocks = rows > kFewRowsOfTree && a.num_seqs <= 1024 && (D == 128 || (D == 256 && dtype != F16));
+  p.blocks = rows > kFewRowsOfTree && a.num_seqs <= 1024 && D == 128;
   int64_t n;
   if (p.blocks) {
     p.tiles = (int)((rows + kTreeBlockRows - 1) / kTreeBlockRows);
     const int64_t tiles = ((int64_t)a.max_kv_len + 63) / 64;
     const int64_t base = a.cache.kv_heads * std::min((int64_t)p.tiles * a.num_seqs, a.tokens * group / kTreeBlockRows + a.num_seqs);
     // as many workgroups as the device holds at once, or a multiple
-    const int64_t slots = tree_block_slots(a.cache.head_dim, dtype);
+    const int64_t slots = tree_block_slots();
     p.workgroups = (base + slots - 1) / slots * slots;
     // splits of the longest if all are as long, and room for as many more where the others are shorter
     const int64_t per = std::max((base * tiles + p.workgroups - 1) / p.workgroups, (int64_t)4);
@@ -114,12 +114,12 @@ hipError_t launch_few(const KvAttendArgs& a, const TreePlan& p, int dtype, const
 
 }  // namespace
 
-size_t kv_tree_workspace(const KvAttendArgs& a, int dtype) { return make_plan(a, dtype).bytes; }
+size_t kv_tree_workspace(const KvAttendArgs& a, int dtype) { return make_plan(a).bytes; }
 
 int launch_kv_tree(const KvAttendArgs& a, int dtype, const DequantArgs& da, void* stream) {
-  const TreePlan p = make_plan(a, dtype);
+  const TreePlan p = make_plan(a);
   if ((int64_t)p.tiles * p.nsplit > UINT32_MAX / 512 || a.cache.kv_heads > 32767 || (p.nsplit > 1 && !kv_merge_fits(a)) ||
-      (p.blocks && p.grid > UINT32_MAX / 256)) {
+      (p.blocks && p.grid > UINT32_MAX / 512)) {
     g_launch_refused_for_size = true;
     return (int)hipErrorInvalidConfiguration;
   }
