@@ -40,22 +40,22 @@ struct Decode {
   typedef std::conditional_t<FINE && KB == 4, f32x2, uint32_t> Entry;
 };
 
-// Codes and block maxima of a thread's key, of one side.
+// What a decoding thread loads of its key for one interval: codes of a tile's keys and of the values of the tile before, and the
+// block maxima of its own d; and, ahead of that, the maxima of the whole head for what there is to know of a later tile.
 template <int D, int KB, bool FINE>
 struct Raw {
-  uint32_t code[Decode<D, KB, FINE>::kWords];
-  float a;                                  // of its own d
-  float all[Decode<D, KB, FINE>::kBlocks];  // of the whole head
+  uint32_t code[2][Decode<D, KB, FINE>::kWords];
+  float own[2], all[Decode<D, KB, FINE>::kBlocks];
 };
 
 // What there is to know of a tile, left in LDS for the waves that multiply: of its keys and of its values 2^e above the largest
 // maximum and, where they are apart, every key's own exponents; which keys some row sees.
 struct Info {
-  int e[2], apart;
+  int e[2], apart[2];
   uint64_t keys;
   int8_t own[2][kTile];
 };
-constexpr int kInfos = 4;  // a tile's is read until two tiles later, while the next but one's is written
+constexpr int kInfos = 4;  // while one is written, those of the three tiles before may be read
 
 __device__ __forceinline__ uint32_t wave_max_bits(uint32_t v) {
   v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, false));
@@ -194,27 +194,42 @@ __global__ __launch_bounds__(kThreads, 2) void tree_kernel(KvAttendArgs aa, Dequ
     const int j = min(t, t_end - 1) * kTile + lane;
     return (((int64_t)(listed(id) ? id : 0) * aa.cache.kv_heads + kvh) << lps) + (j & ((1 << lps) - 1));
   };
-  auto fetch = [&](Raw<D, KB, FINE>& x, int side, int64_t row) {
-    const uint8_t* src = aa.cache.packed[side] + row * C::kRow + wave * (C::kPart * KB / 8);
+  auto fetch = [&](Raw<D, KB, FINE>& x, int64_t row, int64_t row_before) {
 #pragma unroll
-    for (int k = 0; k < C::kWords; k += 4) {
-      const u32x4 v = *reinterpret_cast<const u32x4*>(src + 4 * k);
+    for (int side = 0; side < 2; ++side) {
+      const int64_t from = side == 0 ? row : row_before;
+      const uint8_t* src = aa.cache.packed[side] + from * C::kRow + wave * (C::kPart * KB / 8);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) x.code[k + e] = v[e];
+      for (int k = 0; k < C::kWords; k += 4) {
+        const u32x4 v = *reinterpret_cast<const u32x4*>(src + 4 * k);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x.code[side][k + e] = v[e];
+      }
+      x.own[side] = aa.cache.absmax[side][from * nb + (wave * C::kPart >> log2b)];
     }
-    const float* a = aa.cache.absmax[side] + row * nb;
-    x.a = a[wave * C::kPart >> log2b];
-#pragma unroll
-    for (int b = 0; b < C::kBlocks; ++b) x.all[b] = a[min(b, nb - 1)];
   };
-  Raw<D, KB, FINE> xk, xv;  // of tiles t + 1 and t
-  int id_now = 0, id = 0, id_next = 0;  // pages of the lane's keys of tiles t, t + 1, t + 2
+  auto fetch_all = [&](Raw<D, KB, FINE>& x, int64_t row) {
+    if (wave < 2) {
+      const float* a = aa.cache.absmax[wave] + row * nb;
+#pragma unroll
+      for (int b = 0; b < C::kBlocks; ++b) x.all[b] = a[min(b, nb - 1)];
+    }
+  };
+  // Interval t takes the codes in raw[k] and the maxima there, those of tile t + 1; k takes turns.
+  Raw<D, KB, FINE> raw[2];
+  int id[2] = {0, 0};               // page of the lane's key of tile t + 2, in id[k]
+  int64_t row0 = 0, row1 = 0;       // its rows of tiles t and t + 1
+  bool listed0 = false, listed1 = false;
   if (decodes && t_first < t_end) {
-    id_now = page_of(t_first);
-    id = page_of(t_first + 1);
-    id_next = page_of(t_first + 2);
-    fetch(xk, 0, row_of(t_first, id_now));
-    fetch(xv, 1, row_of(t_first, id_now));
+    const int id0 = page_of(t_first), id1 = page_of(t_first + 1);
+    id[0] = page_of(t_first + 2);
+    listed0 = listed(id0);
+    row0 = row_of(t_first, id0);
+    fetch_all(raw[1], row0);
+    fetch(raw[0], row0, row0);
+    listed1 = listed(id1);
+    row1 = row_of(t_first + 1, id1);
+    fetch_all(raw[0], row1);
   }
 
   if (decodes) {  // table
@@ -227,9 +242,6 @@ __global__ __launch_bounds__(kThreads, 2) void tree_kernel(KvAttendArgs aa, Dequ
 #pragma unroll
     for (int i = 0; i < kEntryBytes / 16; ++i)  // in turn over the banks
       *reinterpret_cast<u32x4*>(s_table + to * kEntryBytes + ((i + to) & (kEntryBytes / 16 - 1)) * 16) = e;
-#pragma unroll
-    for (int i = 0; i < kTilePieces / 256; ++i)  // no weights wait at first
-      *reinterpret_cast<u32x4*>(s_value[1] + (i * 256 + to) * 16) = (u32x4){0, 0, 0, 0};
   }
   const uint32_t copy = (lane * C::kEntry) & (kEntryBytes - 1);
 
@@ -300,34 +312,40 @@ __global__ __launch_bounds__(kThreads, 2) void tree_kernel(KvAttendArgs aa, Dequ
   const int lo = node_first(aa, context, depth), hi = depth >= 0 ? context : 0;  // of the context
 
   // Whether some row sees the lane's key of tile t.
-  auto counts = [&](int t, int page) {
+  auto counts = [&](int t, bool in_pool) {
     const int j = t * kTile + lane, node = j - context;
     const bool used = node < 0 || (node < kMostNodes && (s_tree.used[(node >> 5) + 1] >> (node & 31) & 1));
-    return j >= first && j < last && listed(page) && used;
+    return j >= first && j < last && in_pool && used;
   };
 
   // ---- decoding
-  // The exponent of a tile's side and whether its keys are apart, into the tile's Info; returns the block maximum of the d that the
-  // thread decodes, relative to the tile's exponent or the key's own.
-  auto scale_tile = [&](const Raw<D, KB, FINE>& x, int side, bool seen_key, Info& info) {
+  // What there is to know of a tile: wave 0 finds out about its keys, wave 1 about its values.
+  auto learn = [&](int t, bool in_pool, const float (&all)[C::kBlocks]) {
+    if (wave > 1) return;
+    Info& info = s_info[t & (kInfos - 1)];
+    const uint64_t keys = __ballot(counts(min(t, t_end - 1), in_pool));
+    const bool seen_key = keys >> lane & 1;
     uint32_t top = 0;
 #pragma unroll
-    for (int b = 0; b < C::kBlocks; ++b) top = max(top, f32_bits(x.all[b]) & 0x7fffffffu);
+    for (int b = 0; b < C::kBlocks; ++b) top = max(top, f32_bits(all[b]) & 0x7fffffffu);
     top = seen_key ? top : 0u;
-    const bool say = seen_key && (side == 1 || top != 0);  // zero keys, whose scores are zero at any scale, have none
-    const int least = side == 0 ? kLeastKey : kLeastValue;
+    const bool say = seen_key && (wave == 1 || top != 0);  // zero keys, whose scores are zero at any scale, have none
+    const int least = wave == 0 ? kLeastKey : kLeastValue;
     const uint32_t most = wave_max_bits(say ? top : 0u), low = ~wave_max_bits(say ? ~top : 0u);
     const int e = exponent(most, least);
-    const bool apart = low <= most && e - exponent(low, least) > (side == 0 ? kKeySpread : kValueSpread);
-    const int own = apart && say ? exponent(top, least) : e;
-    if (wave == 0) {
-      info.own[side][lane] = (int8_t)own;
-      if (lane == 0) {
-        info.e[side] = e;
-        info.apart = side == 0 ? (int)apart : info.apart | (int)apart << 1;
-      }
+    const bool apart = low <= most && e - exponent(low, least) > (wave == 0 ? kKeySpread : kValueSpread);
+    info.own[wave][lane] = (int8_t)(apart && say ? exponent(top, least) : e);
+    if (lane == 0) {
+      info.e[wave] = e;
+      info.apart[wave] = apart;
+      info.keys = keys;  // the same of both
     }
-    return seen_key ? __builtin_ldexpf(x.a, -own) : 0.0f;
+  };
+  // The block maximum of the d that the thread decodes, relative to the tile's exponent or the key's own.
+  auto relative = [&](float own, int side, int t) {
+    const Info& info = s_info[t & (kInfos - 1)];
+    const float a = __builtin_ldexpf(own, -info.own[side][lane]);
+    return info.keys >> lane & 1 ? a : 0.0f;
   };
   auto entry_at = [&](uint32_t w, int b) { return *reinterpret_cast<const typename C::Entry*>(s_table + entry_of(w, b, copy)); };
   auto look_up = [&](const uint32_t (&code)[C::kWords], int i, typename C::Entry (&e)[C::kLookups]) {
@@ -458,7 +476,7 @@ __global__ __launch_bounds__(kThreads, 2) void tree_kernel(KvAttendArgs aa, Dequ
   };
   auto known = [&](int t) {
     const Info& x = s_info[t & (kInfos - 1)];
-    return Known{__builtin_amdgcn_readfirstlane(x.e[0]), __builtin_amdgcn_readfirstlane(x.e[1]), __builtin_amdgcn_readfirstlane(x.apart),
+    return Known{__builtin_amdgcn_readfirstlane(x.e[0]), __builtin_amdgcn_readfirstlane(x.e[1]), __builtin_amdgcn_readfirstlane(x.apart[0] | x.apart[1] << 1),
                  (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)x.keys) |
                      (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(x.keys >> 32)) << 32};
   };
@@ -491,17 +509,16 @@ __global__ __launch_bounds__(kThreads, 2) void tree_kernel(KvAttendArgs aa, Dequ
     }
     if (!(j0 >= lo_all && j0 + 32 <= hi_all && keys == ~0u)) {  // some key hidden from some row
       const int from = j0 - context;
-      uint32_t mine = 0;
+      uint32_t mine = 0;  // bit k: the row sees key j0 + k
       if (from > -32) {
         const int word = min((from + 32) >> 5, kTreeWords - 2);
         mine = __builtin_amdgcn_alignbit(seen[word + 1], seen[word], from & 31);
       }
+      const int above = min(max(lo - j0, 0), 31), below = min(max(hi - j0, 0), 32);
+      if (below > 0 && lo - j0 < 32) mine |= (~0u >> (32 - below)) & (~0u << above);
+      mine = (mine & keys) >> (4 * g);
 #pragma unroll
-      for (int v = 0; v < 16; ++v) {
-        const int key = 8 * (v >> 2) + (v & 3) + 4 * g, j = j0 + key;
-        const bool no = j >= context ? !(mine >> key & 1) : j < lo || j >= hi;
-        s[v] = no || !(keys >> key & 1) ? -INFINITY : s[v];
-      }
+      for (int v = 0; v < 16; ++v) s[v] = mine >> (8 * (v >> 2) + (v & 3)) & 1 ? s[v] : -INFINITY;
     }
     float top = -INFINITY, p = 0.0f;
     u32x4 x[2], y[2];
@@ -594,52 +611,53 @@ __global__ __launch_bounds__(kThreads, 2) void tree_kernel(KvAttendArgs aa, Dequ
   };
 
   if (t_first < t_end) {
-    // The decoding waves are a tile ahead: while tile t is multiplied, they find out what there is to know of tile t + 1,
-    // decode its keys and the values of tile t, whose codes and factor they have held since.  A tile's codes are asked for
-    // an interval before that.
-    uint32_t held[C::kWords];
-    float held_a = 0.0f;
-    auto decode = [&](int t, int page, int64_t row_after, bool values) {  // t: the tile whose keys it is
-      const Raw<D, KB, FINE> k = xk, v = xv;
-      fetch(xk, 0, row_after);
-      fetch(xv, 1, row_after);
-      Info& info = s_info[t & (kInfos - 1)];
-      const uint64_t keys = __ballot(counts(min(t, t_end - 1), page));
-      const bool seen_key = keys >> lane & 1;
-      if (wave == 0 && lane == 0) info.keys = keys;
-      const float ka = scale_tile(k, 0, seen_key, info), va = scale_tile(v, 1, seen_key, info);
-      const int b = (t - t_first) & 1;
-#pragma unroll
-      for (int i = 0; i < C::kPieces; ++i) {
-        typename C::Entry e[C::kLookups];
-        look_up(k.code, i, e);
-        finish_key(b, i, ka, e);
-      }
-      if (values) {
-#pragma unroll
-        for (int i = 0; i < C::kPieces; ++i) {
-          typename C::Entry e[C::kLookups];
-          look_up(held, i, e);
-          put_value(b ^ 1, i, products(held_a, e, nullptr));
-        }
-      }
-#pragma unroll
-      for (int x = 0; x < C::kWords; ++x) held[x] = v.code[x];
-      held_a = va;
-    };
-    // Both kinds of wave pass as many barriers.
+    // The decoding waves are a tile ahead: while tile t is multiplied, they decode the keys of tile t + 1 and the values of
+    // tile t, and find out what there is to know of tile t + 2.  Loads are an interval ahead of that, in registers that take turns
+    // (a copy would wait for them).  Both kinds of wave pass as many barriers.
     if (decodes) {
-      decode(t_first, id_now, row_of(t_first + 1, id), false);
+      learn(t_first, listed0, raw[1].all);
       __syncthreads();
-      for (int t = t_first; t < t_end; ++t) {
-        const int page = id;
-        id = id_next;
-        id_next = page_of(t + 3);
-        decode(t + 1, page, row_of(t + 2, id), true);
+      auto decode = [&](int t, auto set) {
+        constexpr int k = set.value;
+        const Raw<D, KB, FINE>& x = raw[k];
+        const int b = (t - t_first) & 1;
+        const float ka = relative(x.own[0], 0, t);
+        const float va = t > t_first ? relative(x.own[1], 1, t - 1) : 0.0f;  // the zeros that this makes have no weights
+        typename C::Entry ek[C::kPieces][C::kLookups], ev[C::kPieces][C::kLookups];
+#pragma unroll
+        for (int i = 0; i < C::kPieces; ++i) look_up(x.code[0], i, ek[i]);
+        if constexpr (KB == 4 && !FINE) {
+#pragma unroll
+          for (int i = 0; i < C::kPieces; ++i) look_up(x.code[1], i, ev[i]);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        const bool listed2 = listed(id[k]);
+        const int64_t row2 = row_of(t + 2, id[k]);
+        fetch(raw[k ^ 1], row1, row0);
+        fetch_all(raw[k ^ 1], row2);
+        id[k ^ 1] = page_of(t + 3);
+        learn(t + 1, listed1, x.all);
+        row0 = row1;
+        row1 = row2;
+        listed1 = listed2;
+#pragma unroll
+        for (int i = 0; i < C::kPieces; ++i) finish_key(b, i, ka, ek[i]);
+        if constexpr (!(KB == 4 && !FINE)) {
+          __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+          for (int i = 0; i < C::kPieces; ++i) look_up(x.code[1], i, ev[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < C::kPieces; ++i) put_value(b ^ 1, i, products(va, ev[i], nullptr));
         __syncthreads();
+      };
+      for (int t = t_first; t <= t_end; t += 2) {
+        decode(t, std::integral_constant<int, 0>());
+        if (t + 1 <= t_end) decode(t + 1, std::integral_constant<int, 1>());
       }
       return;
     }
+    __syncthreads();
     __syncthreads();
     sc[0] = multiply_keys(0, 0);
     for (int t = t_first; t < t_end; ++t) {
