@@ -77,8 +77,10 @@ struct Part {
 
 __device__ __forceinline__ int from_lane(int v, int lane) { return __builtin_amdgcn_readlane(v, lane); }
 
-// The parts are as long as the device can hold at once (`workgroups`); what is left over of each sequence is a part too.  They
-// are numbered in a row, since workgroups without one between the others would leave compute units without work: the
+// Every part is as long as leaves each of `workgroups`, which the device holds at once, one, or half of that where less then
+// stands idle: a part costs its tiles and about 8 more.  What is left over of each sequence is a part too.  With 24 sequences of
+// 32 drafted tokens and up to 8192 keys halves take 152 us and wholes 173, with two of 48 and up to 131072 keys 196 and 185.
+// Parts are numbered in a row, since workgroups without one between the others would leave compute units without work: the
 // hardware deals them out in turn.  The lengths are known on the device only, so every workgroup works this out, a lane to a
 // sequence.  False: there is no such part.
 __device__ __forceinline__ bool find_part(const KvAttendArgs& aa, int group, int nsplit, int workgroups, Part& part) {
@@ -100,7 +102,23 @@ __device__ __forceinline__ bool find_part(const KvAttendArgs& aa, int group, int
   }
 #pragma unroll
   for (int x = 1; x < 64; x <<= 1) work += __shfl_xor(work, x);
-  int per = __builtin_amdgcn_readfirstlane((int)max((work + workgroups - 1) / workgroups, (int64_t)kLeastTiles));
+  const int least[2] = {(int)max((work + workgroups - 1) / workgroups, (int64_t)kLeastTiles),
+                        (int)max((work + 2 * workgroups - 1) / (2 * workgroups), (int64_t)kLeastTiles)};
+  int per = __builtin_amdgcn_readfirstlane(least[0]);
+  if (rounds == 1) {
+    // lanes 0 .. 31 look for the length of a whole, the others for that of a half
+    const int32_t goal = lane < 32 ? workgroups : 2 * workgroups, from = lane < 32 ? least[0] : least[1];
+    const int mine = from + (from * (lane & 31) + 15) / 16;
+    const float inv = 1.0f / (float)mine;
+    int n = 0;
+    for (int s = 0; s < aa.num_seqs; ++s) {
+      const float t = (float)from_lane(tiles, s);
+      n += from_lane(blocks, s) * max((int)ceilf(t * inv), 1);
+    }
+    const uint64_t fits = __ballot(n <= goal) | 1ull << 31 | 1ull << 63;
+    const int whole = from_lane(mine, __builtin_ctzll(fits)), half = from_lane(mine, 32 + __builtin_ctzll(fits >> 32));
+    per = 2 * (half + 8) < whole + 8 ? half : whole;
+  }
   auto per_of = [&]() { return max(per, (tiles + nsplit - 1) / nsplit); };
   auto splits_of = [&]() { return max((tiles + per_of() - 1) / per_of(), 1); };
   auto up_to = [&]() {  // parts of this lane's sequence and those before it
@@ -112,9 +130,6 @@ __device__ __forceinline__ bool find_part(const KvAttendArgs& aa, int group, int
     }
     return n;
   };
-  if (rounds == 1) {
-    for (int i = 0; i < 12 && from_lane(up_to(), 63) > workgroups; ++i) per += max(per / 16, 1);
-  }
   int at = blockIdx.x;
   for (int i = 0; i < rounds; ++i) {
     if (rounds > 1) load(64 * i + lane);

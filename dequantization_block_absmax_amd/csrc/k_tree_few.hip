@@ -34,13 +34,31 @@ int64_t choose_splits(int64_t base, int64_t slots, int64_t keys, int num_seqs) {
   return n;
 }
 
-constexpr int64_t kFewRowsOfTree = 32;
+// Whether the kernel for many rows takes the call: it decodes a tile of keys once for 128 rows where the other does for 32, but
+// begins more slowly and with longer pieces.  `keys`: the longest sequence's that a row can see.  In us, this kernel / that of
+// k_tree.hip, with 32 heads over 8 in bfloat16 on 4-bit codes: one draft of 26 tokens over 1024 keys 15.0 / 21.2, over 16384
+// 31.2 / 37.6, over 65536 82.0 / 77.8; one of 256 over 4096 43.0 / 51.1, over 16384 136 / 122; 4 of 64 over 2048 25.9 / 32.9,
+// over 16384 93.7 / 77.2; 16 of 64 over 512 48.5 / 38.8.  With 64 rows (16 tokens) it is the faster one up to 65536 keys (48.7 /
+// 73.5), and with 16 sequences of 16384 too (124 / 158).
+constexpr int64_t kFewRowsOfTree = 64;
 
-TreePlan make_plan(const KvAttendArgs& a) {
+bool many_rows(const KvAttendArgs& a, int64_t keys) {
+  const int64_t rows = a.max_q_len * (int64_t)(a.heads / a.cache.kv_heads);
+  if (a.cache.head_dim != 128 || rows <= kFewRowsOfTree || a.num_seqs > 1024) return false;
+  const int64_t work = (rows + 31) / 32 * a.cache.kv_heads * a.num_seqs * keys;
+  return a.num_seqs > 1 ? work >= 1 << 19 : work > 1 << 20;
+}
+
+// The most keys that a row sees, where a window can leave some out.
+int64_t keys_in_window(const KvAttendArgs& a) {
+  return a.window > 0 ? std::min((int64_t)a.max_kv_len, (int64_t)a.window + a.max_q_len) : a.max_kv_len;
+}
+
+TreePlan make_plan(const KvAttendArgs& a, bool blocks) {
   TreePlan p = {};
   const int64_t group = a.heads / a.cache.kv_heads, D = a.cache.head_dim, cus = cu_count();
   const int64_t rows = a.max_q_len * group;
-  p.blocks = rows > kFewRowsOfTree && a.num_seqs <= 1024 && D == 128;
+  p.blocks = blocks;
   int64_t n;
   if (p.blocks) {
     p.tiles = (int)((rows + kTreeBlockRows - 1) / kTreeBlockRows);
@@ -49,13 +67,13 @@ TreePlan make_plan(const KvAttendArgs& a) {
     // as many workgroups as the device holds at once, or a multiple
     const int64_t slots = tree_block_slots();
     p.workgroups = (base + slots - 1) / slots * slots;
-    // splits of the longest if all are as long, and room for as many more where the others are shorter
-    const int64_t per = std::max((base * tiles + p.workgroups - 1) / p.workgroups, (int64_t)4);
+    // splits of the longest if all are as long and parts half as long, and room for as many more where the others are shorter
+    const int64_t per = std::max((base * tiles + 2 * p.workgroups - 1) / (2 * p.workgroups), (int64_t)4);
     n = (tiles + per - 1) / per;
     if (a.num_seqs > 1) n = std::min(2 * n, (tiles + 3) / 4);
     n = std::max(std::min(n, (int64_t)kMaxSplits), (int64_t)1);
     // what is left over of each sequence is a part of its own
-    p.grid = std::min(base * n, p.workgroups + base);
+    p.grid = std::min(base * n, 2 * p.workgroups + base);
   } else {
     p.rt = D > 128 || rows <= 16 ? 1 : rows <= 32 || D == 128 ? 2 : 4;
     const int64_t per = 16 * p.rt;
@@ -64,10 +82,9 @@ TreePlan make_plan(const KvAttendArgs& a) {
     p.tiles = (int)((rows + per - 1) / per);
     // tiles with rows in them: sequences may bring fewer tokens than the longest
     const int64_t base = a.cache.kv_heads * std::min((int64_t)p.tiles * a.num_seqs, a.tokens * group / per + a.num_seqs);
-    // the workspace is asked for without a window, and holds for any
+    // never more than without a window
     n = choose_splits(base, slots, a.max_kv_len, a.num_seqs);
-    if (a.window > 0 && (int64_t)a.window + a.max_q_len < a.max_kv_len)
-      n = std::min(n, choose_splits(base, slots, (int64_t)a.window + a.max_q_len, a.num_seqs));
+    if (keys_in_window(a) < a.max_kv_len) n = std::min(n, choose_splits(base, slots, keys_in_window(a), a.num_seqs));
   }
   p.nsplit = (int)n;
   if (n > 1) p.bytes = (size_t)a.tokens * a.heads * n * (D + 3) * 4;
@@ -114,10 +131,14 @@ hipError_t launch_few(const KvAttendArgs& a, const TreePlan& p, int dtype, const
 
 }  // namespace
 
-size_t kv_tree_workspace(const KvAttendArgs& a, int dtype) { return make_plan(a).bytes; }
+// The workspace is asked for without a window and holds for any, in which either kernel may be the one.
+size_t kv_tree_workspace(const KvAttendArgs& a, int dtype) {
+  const size_t few = make_plan(a, false).bytes;
+  return many_rows(a, a.max_kv_len) ? std::max(few, make_plan(a, true).bytes) : few;
+}
 
 int launch_kv_tree(const KvAttendArgs& a, int dtype, const DequantArgs& da, void* stream) {
-  const TreePlan p = make_plan(a);
+  const TreePlan p = make_plan(a, many_rows(a, keys_in_window(a)));
   if ((int64_t)p.tiles * p.nsplit > UINT32_MAX / 512 || a.cache.kv_heads > 32767 || (p.nsplit > 1 && !kv_merge_fits(a)) ||
       (p.blocks && p.grid > UINT32_MAX / 512)) {
     g_launch_refused_for_size = true;
