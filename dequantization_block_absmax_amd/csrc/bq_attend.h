@@ -385,10 +385,104 @@ __device__ __forceinline__ bool any_node(const TreeShared<ROWS>& tree, int i_fir
   return __builtin_amdgcn_readfirstlane(any) != 0;
 }
 
+// Which part of a call a workgroup takes: of one sequence and key/value head a block of rows and one of n_splits runs of `per` units of
+// keys.
+struct Part {
+  int seq, kvh, block, split, per, n_splits;
+};
+
+__device__ __forceinline__ int from_lane(int v, int lane) { return __builtin_amdgcn_readlane(v, lane); }
+
+// Divides sequences of different lengths into parts of ROWS rows by a number of units of UNIT keys, from the ALIGN-th key that they
+// begin at.  Every part is as long as leaves each of `workgroups`, which the device holds at once, one, or half of that where
+// less then stands idle: a part costs its units and about `extra` more.  What is left over of each sequence is a part too.
+// With the kernel of k_tree.hip 24 sequences of 32 drafted tokens and up to 8192 keys take 152 us in halves and 173 in wholes, two
+// of 48 and up to 131072 keys 196 and 185.  Parts are numbered in a row, since workgroups without one between the others would
+// leave compute units without work: the hardware deals them out in turn.  The lengths are known on the device only, so every
+// workgroup works this out, a lane to a sequence.  False: there is no such part.
+template <int ROWS, int UNIT, int ALIGN>
+__device__ __forceinline__ bool find_part(const KvAttendArgs& aa, int group, int nsplit, int workgroups, int least, int extra, Part& part) {
+  const int lane = threadIdx.x & 63;
+  int blocks = 0, units = 0;  // of the lane's sequence; of all heads
+  auto load = [&](int s) {
+    blocks = units = 0;
+    if (s >= aa.num_seqs) return;
+    const int q0 = row_number(aa, aa.q_start[s]), nq = max(row_number(aa, aa.q_start[s + 1]) - q0, 0);
+    const int kv = max(min(aa.kv_len[s], aa.max_kv_len), 0);
+    blocks = (int)((min(nq, aa.max_q_len) * (int64_t)group + ROWS - 1) / ROWS) * aa.cache.kv_heads;
+    units = max((int)((kv - (node_first(aa, kv - nq, 0) & ~(ALIGN - 1)) + (int64_t)UNIT - 1) / UNIT), 0);
+  };
+  const int rounds = (aa.num_seqs + 63) / 64, lanes = min(aa.num_seqs, 64);
+  int64_t work = 0;
+  for (int i = 0; i < rounds; ++i) {
+    load(64 * i + lane);
+    work += (int64_t)blocks * units;
+  }
+  for (int x = 1; x < lanes; x <<= 1) work += __shfl_xor(work, x);
+  work = (int64_t)(uint32_t)from_lane((int)work, 0) | (int64_t)from_lane((int)(work >> 32), 0) << 32;
+  const int of_whole = max((int)((work + workgroups - 1) / workgroups), least);
+  const int of_half = max((int)((work + 2 * workgroups - 1) / (2 * workgroups)), least);
+  int per = of_whole;
+  if (rounds == 1) {
+    // lanes 0 .. 31 look for the length of a whole, the others for that of a half
+    const int goal = lane < 32 ? workgroups : 2 * workgroups, from = lane < 32 ? of_whole : of_half;
+    const int mine = from + (from * (lane & 31) + 15) / 16;
+    const float inv = 1.0f / (float)mine;
+    int n = 0;
+    for (int s = 0; s < aa.num_seqs; ++s)
+      n += from_lane(blocks, s) * max((int)ceilf((float)from_lane(units, s) * inv), 1);
+    const uint64_t fits = __ballot(n <= goal) | 1ull << 31 | 1ull << 63;
+    const int whole = from_lane(mine, __builtin_ctzll(fits)), half = from_lane(mine, 32 + __builtin_ctzll(fits >> 32));
+    per = 2 * (half + extra) < whole + extra ? half : whole;
+  }
+  auto per_of = [&]() { return max(per, (units + nsplit - 1) / nsplit); };
+  auto splits_of = [&]() { return max((units + per_of() - 1) / per_of(), 1); };
+  auto up_to = [&]() {  // parts of this lane's sequence and those before it
+    int n = blocks * splits_of();
+    for (int x = 1; x < lanes; x <<= 1) {
+      const int before = __shfl_up(n, x);
+      n += lane >= x ? before : 0;
+    }
+    return n;
+  };
+  int at = blockIdx.x;
+  for (int i = 0; i < rounds; ++i) {
+    if (rounds > 1) load(64 * i + lane);
+    const int n = up_to(), all = from_lane(n, lanes - 1);
+    if (at < all) {
+      const int who = __builtin_ctzll(__ballot(at < n));
+      const int mine = from_lane(blocks, who);
+      part.seq = 64 * i + who;
+      part.per = from_lane(per_of(), who);
+      part.n_splits = from_lane(splits_of(), who);
+      at -= from_lane(n, who) - mine * part.n_splits;
+      part.split = at / mine;
+      at -= part.split * mine;
+      part.kvh = at % aa.cache.kv_heads;
+      part.block = at / aa.cache.kv_heads;
+      return true;
+    }
+    at -= all;
+  }
+  return false;
+}
+
+// Splits of row r that no part takes: the join passes over them.
+template <int D>
+__device__ __forceinline__ void no_parts(const KvAttendArgs& aa, const Part& part, const Sequence& sq, int nrows, int nsplit, int r,
+                                         float* partial) {
+  if (r >= nrows) return;
+  const int group = aa.heads / aa.cache.kv_heads;
+  const int64_t row = (int64_t)(sq.q0 + r / group) * aa.heads + part.kvh * group + r % group;
+  for (int x = part.n_splits; x < nsplit; ++x)
+    reinterpret_cast<Partial*>(partial + aa.tokens * aa.heads * nsplit * D)[row * nsplit + x] = {-INFINITY, 0.0f, 0.0f};
+}
+
 // TREE: the new tokens are a tree (aa.parents).  Token i sees the context (the keys before the new tokens), itself and
 // the tokens on its path from the root, by its depth within the window.  The words are worked out once for a tile, beside
 // the first loads, each token's path by a lane of its own; they are looked at for the groups that reach past the
-// context only.
+// context only.  `rows`: what takes() goes by or, of a tree, the workgroups that the device holds at once where the
+// parts are found from the lengths (find_part), and else 0.
 template <int D, int NB, int KB, int RT, bool HL, bool TREE>
 __global__ __launch_bounds__((64 * Occupancy<D, NB, KB, RT>::kWaves), (Occupancy<D, NB, KB, RT>::kPerSimd)) void attend_kernel(
     KvAttendArgs aa, DequantArgs da, int nsplit, float* partial, int rows) {
@@ -420,13 +514,19 @@ __global__ __launch_bounds__((64 * Occupancy<D, NB, KB, RT>::kWaves), (Occupancy
     entry_hi = da.c[KB == 4 ? tid >> 4 : tid];
   }
   load_fence();
-  const int split = blockIdx.x % nsplit, tile = blockIdx.x / nsplit;
-  const int kvh = blockIdx.y;
-  const int seq = blockIdx.z;
   const int group = aa.heads / aa.cache.kv_heads;
+  Part part = {(int)blockIdx.z, (int)blockIdx.y, (int)blockIdx.x / nsplit, (int)blockIdx.x % nsplit, 0, nsplit};
+  if constexpr (TREE) {
+    constexpr int kPartUnits = 3;  // that a part costs besides its own
+    if (rows != 0 && !find_part<kRows, kGroup * W, kGroup>(aa, group, nsplit, rows, 1, kPartUnits, part)) return;
+  }
+  const int split = part.split, tile = part.block, kvh = part.kvh, seq = part.seq;
   const Sequence sq = sequence(aa, seq);
   const int nrows = min(sq.nq, aa.max_q_len) * group;  // rows of the sequence for this key/value head
-  if (tile * kRows >= nrows || !takes(rows, min(sq.nq, aa.max_q_len), group, aa.num_seqs)) return;
+  if (tile * kRows >= nrows || (!TREE && !takes(rows, min(sq.nq, aa.max_q_len), group, aa.num_seqs))) return;
+  if constexpr (TREE) {
+    if (split == 0 && tid < kRows) no_parts<D>(aa, part, sq, nrows, nsplit, tile * kRows + tid, partial);
+  }
 
   // Keys of the tile's rows together, this split's groups of 32 of them, and this wave's: groups
   // wave, wave + W, ... of the split.
@@ -439,7 +539,7 @@ __global__ __launch_bounds__((64 * Occupancy<D, NB, KB, RT>::kWaves), (Occupancy
   const int lo_all = TREE ? node_first(aa, context, i_last) : first_key(aa, sq, i_last);  // seen by every row
   int hi_all = TREE ? context : end_key(aa, sq, i_first);
   const int groups = end > begin ? (end - begin + kGroup - 1) / kGroup : 0;
-  const int per = (groups + nsplit - 1) / nsplit;
+  const int per = TREE && rows != 0 ? part.per * W : (groups + nsplit - 1) / nsplit;
   const int g_end = min((split + 1) * per, groups);
   int gi = split * per + wave;
 

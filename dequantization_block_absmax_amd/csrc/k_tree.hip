@@ -12,6 +12,7 @@ namespace {
 constexpr int kTile = 64;   // keys
 constexpr int kRows = kTreeBlockRows;  // new token x query head of one key/value head
 constexpr int kLeastTiles = 4;  // of a workgroup, where the keys are split
+constexpr int kPartTiles = 8;   // that a part costs besides its own
 constexpr int kThreads = 512;  // four waves with 32 rows each, and four that decode
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
@@ -70,88 +71,6 @@ __device__ __forceinline__ uint32_t wave_max_bits(uint32_t v) {
 
 __device__ __forceinline__ int exponent(uint32_t bits, int least) { return min(max((int)(bits >> 23) - 126, least), 120); }
 
-// Which part of a call a workgroup takes: of one sequence and key/value head a block of rows and one of n_splits runs of `per` tiles.
-struct Part {
-  int seq, kvh, block, split, per, n_splits;
-};
-
-__device__ __forceinline__ int from_lane(int v, int lane) { return __builtin_amdgcn_readlane(v, lane); }
-
-// Every part is as long as leaves each of `workgroups`, which the device holds at once, one, or half of that where less then
-// stands idle: a part costs its tiles and about 8 more.  What is left over of each sequence is a part too.  With 24 sequences of
-// 32 drafted tokens and up to 8192 keys halves take 152 us and wholes 173, with two of 48 and up to 131072 keys 196 and 185.
-// Parts are numbered in a row, since workgroups without one between the others would leave compute units without work: the
-// hardware deals them out in turn.  The lengths are known on the device only, so every workgroup works this out, a lane to a
-// sequence.  False: there is no such part.
-__device__ __forceinline__ bool find_part(const KvAttendArgs& aa, int group, int nsplit, int workgroups, Part& part) {
-  const int lane = threadIdx.x & 63;
-  int blocks = 0, tiles = 0;  // of the lane's sequence; of all heads
-  auto load = [&](int s) {
-    blocks = tiles = 0;
-    if (s >= aa.num_seqs) return;
-    const int q0 = row_number(aa, aa.q_start[s]), nq = max(row_number(aa, aa.q_start[s + 1]) - q0, 0);
-    const int kv = max(min(aa.kv_len[s], aa.max_kv_len), 0);
-    blocks = (int)((min(nq, aa.max_q_len) * (int64_t)group + kRows - 1) / kRows) * aa.cache.kv_heads;
-    tiles = max((kv + kTile - 1) / kTile - node_first(aa, kv - nq, 0) / kTile, 0);
-  };
-  const int rounds = (aa.num_seqs + 63) / 64;
-  int64_t work = 0;
-  for (int i = 0; i < rounds; ++i) {
-    load(64 * i + lane);
-    work += (int64_t)blocks * tiles;
-  }
-#pragma unroll
-  for (int x = 1; x < 64; x <<= 1) work += __shfl_xor(work, x);
-  const int least[2] = {(int)max((work + workgroups - 1) / workgroups, (int64_t)kLeastTiles),
-                        (int)max((work + 2 * workgroups - 1) / (2 * workgroups), (int64_t)kLeastTiles)};
-  int per = __builtin_amdgcn_readfirstlane(least[0]);
-  if (rounds == 1) {
-    // lanes 0 .. 31 look for the length of a whole, the others for that of a half
-    const int32_t goal = lane < 32 ? workgroups : 2 * workgroups, from = lane < 32 ? least[0] : least[1];
-    const int mine = from + (from * (lane & 31) + 15) / 16;
-    const float inv = 1.0f / (float)mine;
-    int n = 0;
-    for (int s = 0; s < aa.num_seqs; ++s) {
-      const float t = (float)from_lane(tiles, s);
-      n += from_lane(blocks, s) * max((int)ceilf(t * inv), 1);
-    }
-    const uint64_t fits = __ballot(n <= goal) | 1ull << 31 | 1ull << 63;
-    const int whole = from_lane(mine, __builtin_ctzll(fits)), half = from_lane(mine, 32 + __builtin_ctzll(fits >> 32));
-    per = 2 * (half + 8) < whole + 8 ? half : whole;
-  }
-  auto per_of = [&]() { return max(per, (tiles + nsplit - 1) / nsplit); };
-  auto splits_of = [&]() { return max((tiles + per_of() - 1) / per_of(), 1); };
-  auto up_to = [&]() {  // parts of this lane's sequence and those before it
-    int n = blocks * splits_of();
-#pragma unroll
-    for (int x = 1; x < 64; x <<= 1) {
-      const int before = __shfl_up(n, x);
-      n += lane >= x ? before : 0;
-    }
-    return n;
-  };
-  int at = blockIdx.x;
-  for (int i = 0; i < rounds; ++i) {
-    if (rounds > 1) load(64 * i + lane);
-    const int n = up_to(), all = from_lane(n, 63);
-    if (at < all) {
-      const int who = __builtin_ctzll(__ballot(at < n));
-      const int mine = from_lane(blocks, who);
-      part.seq = 64 * i + who;
-      part.per = from_lane(per_of(), who);
-      part.n_splits = from_lane(splits_of(), who);
-      at -= from_lane(n, who) - mine * part.n_splits;
-      part.split = at / mine;
-      at -= part.split * mine;
-      part.kvh = at % aa.cache.kv_heads;
-      part.block = at / aa.cache.kv_heads;
-      return true;
-    }
-    at -= all;
-  }
-  return false;
-}
-
 template <int D, int KB, bool FINE>
 __global__ __launch_bounds__(kThreads, 2) void tree_kernel(KvAttendArgs aa, DequantArgs da, int nsplit, int workgroups, float* partial) {
   using C = Decode<D, KB, FINE>;
@@ -176,7 +95,7 @@ __global__ __launch_bounds__(kThreads, 2) void tree_kernel(KvAttendArgs aa, Dequ
   load_fence();
   const int group = aa.heads / aa.cache.kv_heads;
   Part part;
-  if (!find_part(aa, group, nsplit, workgroups, part)) return;
+  if (!find_part<kRows, kTile, kTile>(aa, group, nsplit, workgroups, kLeastTiles, kPartTiles, part)) return;
   const int kvh = part.kvh, block = part.block, seq = part.seq, split = part.split;
   const Sequence sq = sequence(aa, seq);
   const int nrows = min(sq.nq, aa.max_q_len) * group;
@@ -187,14 +106,8 @@ __global__ __launch_bounds__(kThreads, 2) void tree_kernel(KvAttendArgs aa, Dequ
   int last = max(min(sq.kv, context + i_last + 1), 0);  // end of the keys that some row may see
   const int begin = first / kTile, end = (last + kTile - 1) / kTile;
   const int t_first = begin + split * part.per, t_end = min(t_first + part.per, end);
-  // splits without a part: the join passes over them
-  for (int x = part.n_splits + (tid >> 7); split == 0 && x < nsplit; x += kThreads / 128) {
-    const int r = block * kRows + (tid & 127);
-    if (r < nrows) {
-      const int64_t row = (int64_t)(sq.q0 + r / group) * aa.heads + kvh * group + r % group;
-      reinterpret_cast<Partial*>(partial + aa.tokens * aa.heads * nsplit * D)[row * nsplit + x] = {-INFINITY, 0.0f, 0.0f};
-    }
-  }
+  if (split == 0)
+    for (int r = tid; r < kRows; r += kThreads) no_parts<D>(aa, part, sq, nrows, nsplit, block * kRows + r, partial);
   const int lo_all = node_first(aa, context, i_last);
   int hi_all = context;
 

@@ -34,6 +34,15 @@ int64_t choose_splits(int64_t base, int64_t slots, int64_t keys, int num_seqs) {
   return n;
 }
 
+// Splits for parts that are found on the device, of at least `least` units of keys: those of the longest sequence if all are as
+// long and parts half as long as they can be, and room for as many more where the others are shorter.
+int64_t most_splits(int64_t base, int64_t workgroups, int64_t units, int64_t least, int num_seqs) {
+  const int64_t per = std::max((base * units + 2 * workgroups - 1) / (2 * workgroups), least);
+  int64_t n = (units + per - 1) / per;
+  if (num_seqs > 1) n = std::min(2 * n, (units + least - 1) / least);
+  return std::max(std::min(n, (int64_t)kMaxSplits), (int64_t)1);
+}
+
 // Whether the kernel for many rows takes the call: it decodes a tile of keys once for 128 rows where the other does for 32, but
 // begins more slowly and with longer pieces.  `keys`: the longest sequence's that a row can see.  In us, this kernel / that of
 // k_tree.hip, with 32 heads over 8 in bfloat16 on 4-bit codes: one draft of 26 tokens over 1024 keys 15.0 / 21.2, over 16384
@@ -42,7 +51,7 @@ int64_t choose_splits(int64_t base, int64_t slots, int64_t keys, int num_seqs) {
 // 73.5), and with 16 sequences of 16384 too (124 / 158).
 constexpr int64_t kFewRowsOfTree = 64;
 
-bool many_rows(const KvAttendArgs& a, int64_t keys) {
+bool blocks_take(const KvAttendArgs& a, int64_t keys) {
   const int64_t rows = a.max_q_len * (int64_t)(a.heads / a.cache.kv_heads);
   if (a.cache.head_dim != 128 || rows <= kFewRowsOfTree || a.num_seqs > 1024) return false;
   const int64_t work = (rows + 31) / 32 * a.cache.kv_heads * a.num_seqs * keys;
@@ -54,11 +63,25 @@ int64_t keys_in_window(const KvAttendArgs& a) {
   return a.window > 0 ? std::min((int64_t)a.max_kv_len, (int64_t)a.window + a.max_q_len) : a.max_kv_len;
 }
 
-TreePlan make_plan(const KvAttendArgs& a, bool blocks) {
+constexpr int kBlocks = 0;  // in place of a number of rows / 16: the kernel of k_tree.hip
+
+// Rows / 16 of a workgroup of the kernel for few rows: as many as hold a short draft, where decoding the keys again for more
+// of them costs more than the tiles' number gives, and 1 for small calls, whose time is the chain from arguments to result.
+// With 16 rows, and with more, in us: 128 wide, 32 heads over 8, 4-bit codes, bfloat16: one draft of 26 tokens over 1000 keys 12.7 and
+// 15.2, over 4000 19.4 and 18.3, 8 of 6 over 1000 14.0 and 16.7, 8 of 13 over 8000 36.9 and 34.6; 64 wide, 20 heads over 5, 8-bit
+// codes, binary16: one of 13 over 1000 11.4 and 19.4, 20 of 13 over a window of 4000 56 and 61, 4 of 64 over 8000 60 and 52.
+int few_rows(const KvAttendArgs& a, int64_t keys) {
+  const int64_t D = a.cache.head_dim, rows = a.max_q_len * (int64_t)(a.heads / a.cache.kv_heads);
+  const int64_t work = (rows + 15) / 16 * a.cache.kv_heads * a.num_seqs * keys;
+  if (D > 128 || rows <= 16 || work <= (D == 64 ? 1 << 21 : 1 << 17)) return 1;
+  return rows <= 32 || D == 128 ? 2 : 4;
+}
+
+TreePlan make_plan(const KvAttendArgs& a, int rt) {
   TreePlan p = {};
   const int64_t group = a.heads / a.cache.kv_heads, D = a.cache.head_dim, cus = cu_count();
   const int64_t rows = a.max_q_len * group;
-  p.blocks = blocks;
+  p.blocks = rt == kBlocks;
   int64_t n;
   if (p.blocks) {
     p.tiles = (int)((rows + kTreeBlockRows - 1) / kTreeBlockRows);
@@ -67,16 +90,12 @@ TreePlan make_plan(const KvAttendArgs& a, bool blocks) {
     // as many workgroups as the device holds at once, or a multiple
     const int64_t slots = tree_block_slots();
     p.workgroups = (base + slots - 1) / slots * slots;
-    // splits of the longest if all are as long and parts half as long, and room for as many more where the others are shorter
-    const int64_t per = std::max((base * tiles + 2 * p.workgroups - 1) / (2 * p.workgroups), (int64_t)4);
-    n = (tiles + per - 1) / per;
-    if (a.num_seqs > 1) n = std::min(2 * n, (tiles + 3) / 4);
-    n = std::max(std::min(n, (int64_t)kMaxSplits), (int64_t)1);
+    n = most_splits(base, p.workgroups, tiles, 4, a.num_seqs);
     // what is left over of each sequence is a part of its own
     p.grid = std::min(base * n, 2 * p.workgroups + base);
   } else {
-    p.rt = D > 128 || rows <= 16 ? 1 : rows <= 32 || D == 128 ? 2 : 4;
-    const int64_t per = 16 * p.rt;
+    p.rt = rt;
+    const int64_t per = 16 * p.rt, unit = D == 256 && a.cache.head_dim >> a.cache.log2b == 8 ? 128 : 256;
     const int nb = a.cache.head_dim >> a.cache.log2b;
     const int64_t slots = cus * (D == 256 || nb == 4 || p.rt * D > 128 || wide_form((int)D, nb, a.bits, p.rt) ? 1 : 2);
     p.tiles = (int)((rows + per - 1) / per);
@@ -85,6 +104,12 @@ TreePlan make_plan(const KvAttendArgs& a, bool blocks) {
     // never more than without a window
     n = choose_splits(base, slots, a.max_kv_len, a.num_seqs);
     if (keys_in_window(a) < a.max_kv_len) n = std::min(n, choose_splits(base, slots, keys_in_window(a), a.num_seqs));
+    if (n > 1 && a.num_seqs > 1 && a.num_seqs <= 64) {
+      p.workgroups = (base + slots - 1) / slots * slots;
+      auto most = [&](int64_t keys) { return most_splits(base, p.workgroups, (keys + unit - 1) / unit, 1, a.num_seqs); };
+      n = std::min(most(a.max_kv_len), most(keys_in_window(a)));
+      p.grid = std::min(base * n, 2 * p.workgroups + base);
+    }
   }
   p.nsplit = (int)n;
   if (n > 1) p.bytes = (size_t)a.tokens * a.heads * n * (D + 3) * 4;
@@ -93,10 +118,11 @@ TreePlan make_plan(const KvAttendArgs& a, bool blocks) {
 
 template <int D, int NB, int KB, int RT>
 hipError_t launch_rows(const KvAttendArgs& a, const TreePlan& p, int dtype, const DequantArgs& da, hipStream_t s) {
-  const dim3 grid((unsigned)(p.tiles * p.nsplit), (unsigned)a.cache.kv_heads, (unsigned)a.num_seqs);
+  const dim3 grid = p.workgroups != 0 ? dim3((unsigned)p.grid)
+                                      : dim3((unsigned)(p.tiles * p.nsplit), (unsigned)a.cache.kv_heads, (unsigned)a.num_seqs);
   const auto kernel = dtype == F16 ? attend_kernel<D, NB, KB, RT, true, true> : attend_kernel<D, NB, KB, RT, false, true>;
   return launch_kernel(kernel, grid, dim3(64 * Occupancy<D, NB, KB, RT>::kWaves), s, a, da, p.nsplit,
-                       static_cast<float*>(a.workspace), (int)kAllRows);
+                       static_cast<float*>(a.workspace), (int)p.workgroups);
 }
 
 template <int D, int NB, int KB>
@@ -131,16 +157,16 @@ hipError_t launch_few(const KvAttendArgs& a, const TreePlan& p, int dtype, const
 
 }  // namespace
 
-// The workspace is asked for without a window and holds for any, in which either kernel may be the one.
+// The workspace is asked for without a window and holds for any, whichever form is the one with it.
 size_t kv_tree_workspace(const KvAttendArgs& a, int dtype) {
-  const size_t few = make_plan(a, false).bytes;
-  return many_rows(a, a.max_kv_len) ? std::max(few, make_plan(a, true).bytes) : few;
+  const size_t few = std::max(make_plan(a, 1).bytes, make_plan(a, few_rows(a, a.max_kv_len)).bytes);
+  return blocks_take(a, a.max_kv_len) ? std::max(few, make_plan(a, kBlocks).bytes) : few;
 }
 
 int launch_kv_tree(const KvAttendArgs& a, int dtype, const DequantArgs& da, void* stream) {
-  const TreePlan p = make_plan(a, many_rows(a, keys_in_window(a)));
+  const TreePlan p = make_plan(a, blocks_take(a, keys_in_window(a)) ? kBlocks : few_rows(a, keys_in_window(a)));
   if ((int64_t)p.tiles * p.nsplit > UINT32_MAX / 512 || a.cache.kv_heads > 32767 || (p.nsplit > 1 && !kv_merge_fits(a)) ||
-      (p.blocks && p.grid > UINT32_MAX / 512)) {
+      p.grid > UINT32_MAX / 512) {
     g_launch_refused_for_size = true;
     return (int)hipErrorInvalidConfiguration;
   }
