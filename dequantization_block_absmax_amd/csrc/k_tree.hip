@@ -1,4 +1,30 @@
 // k_tree.hip -- attention of a tree of drafted tokens over the cache, for drafts with many rows to a key/value head.
+//
+//   o_i = sum_j p_ij v_j,   p_ij = exp(s_ij) / sum_j exp(s_ij),   s_ij = scale * (q_i . k_j)
+// over the keys j that row i sees: the context within its window, its ancestors and itself; one pass with the running maximum
+// and sum of the softmax.
+//
+// Work decomposition.  A workgroup takes 128 rows (new token x query head of one key/value head) and a run of tiles of 64 keys
+// (find_part).  Waves 0 to 3 multiply, 32 rows each, on v_mfma_f32_32x32x16_f16; waves 4 to 7 decode: a lane takes a quarter of a
+// key's head, looks its codes up in a table in LDS, multiplies by the block maximum and rounds once to binary16, relative to a power
+// of two of the tile (of the key, where keys differ too much).  So each code is decoded once for 128 rows, where the kernel of
+// bq_attend.h decodes it once for 16 to 64.  Keys go to LDS in the order of the first product's operands, values by rows,
+// their 16-byte chunks permuted so that neither the stores nor the transposed loads (ds_read_b64_tr_b16) of the second product's
+// operands meet in a bank.  Both have two buffers, so that one barrier a tile is enough: while tile t is multiplied, the keys of
+// t + 1 and the values of t are decoded and the exponents of t + 2 found.  A multiplying wave takes half a tile at a time: the
+// products of the next half's scores, those of the last half's weights with their values, and this half's exponentials
+// stand in turn, in an order that is kept.  With q in binary16 what rounding left of the keys follows in 6 bits through
+// v_mfma_scale_f32_32x32x64_f8f6f4, and what it left of the weights as second products; values are rounded once.
+//
+// What bounds it.  Nothing alone: in the steady state a tile takes about 3900 cycles of a compute unit, of which the matrix cores have
+// work for 1024, LDS for about 1800 and the vector units for about 2200; decoding alone, without the products, took 129 us of 188 in
+// the first case below and 179 of 266 in the third (before two of its waves looked a tile ahead).  On MI355X, a call's time:
+//   24 drafts of up to 32 tokens over up to 8192 keys, 32 heads over 8, 4-bit, B = 64, bf16: 153 us with its join, 358 TFLOP/s
+//   2 of 48 over up to 131072, 16 over 2, 8-bit, B = 128, f16: 180 us, 379 TFLOP/s
+//   2 of 256 over up to 18432, 32 over 4, 4-bit, B = 64, bf16: 216 us, 492 TFLOP/s
+// Other forms, same cases: four waves that decode between their own products, two workgroups to a compute unit, 155, 272 and 232 us;
+// all eight waves in both roles with keys held in registers spilled; loads four tiles ahead instead of one 189, 194 and 268 against
+// 188, 188 and 266; one workgroup to each run of a fixed length, without numbering, 169, 354 and 210.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
@@ -22,7 +48,10 @@ typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
 typedef int i32x6 __attribute__((ext_vector_type(6)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 
-// As in k_attn_chunk.hip.
+// A tile's keys are apart where their largest block maxima differ by more than 2^kKeySpread: then binary16 would lose bits of the
+// small ones relative to the largest.  The same of values by 2^kValueSpread, whose weights have to stay in binary16's range too.
+// Exponents end at the least that the sums' scale allows.  kHead: log2 of the room above a weight of 1 that the reference may
+// fall short by, kSlack of it before it moves.
 constexpr int kKeySpread = 12, kValueSpread = 4;
 constexpr int kLeastKey = -100, kLeastValue = -80;
 constexpr float kHead = 3.0f;

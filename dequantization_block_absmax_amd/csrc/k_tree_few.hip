@@ -1,5 +1,10 @@
 // k_tree_few.hip -- attention of a tree of drafted tokens over the cache: how a call is divided, and the launches for drafts with
 // few rows to a key/value head (the kernel of bq_attend.h).
+//
+// That kernel's figures for trees, on MI355X: one draft of 26 tokens over 1026 keys, 32 heads over 8 of 128, 4-bit, B = 64, bf16:
+// 12.7 us and join 3.9, the chain of loads from the arguments to the keys and two launches; 20 of up to 13 over a window of
+// 4000, 20 over 5 of 64, 8-bit, B = 32, f16: 52 us with the join, 1.0 TB/s: 16 rows are decoded for at a time, vector units;
+// 5 of up to 21 over up to 6000, 8 over 1 of 256, 8-bit, B = 128, bf16: 32 us, 93 TFLOP/s: 11 row tiles decode the same keys.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -48,12 +53,13 @@ int64_t most_splits(int64_t base, int64_t workgroups, int64_t units, int64_t lea
 // k_tree.hip, with 32 heads over 8 in bfloat16 on 4-bit codes: one draft of 26 tokens over 1024 keys 15.0 / 21.2, over 16384
 // 31.2 / 37.6, over 65536 82.0 / 77.8; one of 256 over 4096 43.0 / 51.1, over 16384 136 / 122; 4 of 64 over 2048 25.9 / 32.9,
 // over 16384 93.7 / 77.2; 16 of 64 over 512 48.5 / 38.8.  With 64 rows (16 tokens) it is the faster one up to 65536 keys (48.7 /
-// 73.5), and with 16 sequences of 16384 too (124 / 158).
+// 73.5), and with 16 sequences of 16384 too (124 / 158).  Past 256 sequences every workgroup's look at their lengths outweighs
+// what that gives: 256 of 26 over 1024 keys 399 / 401, 1024 of 20 over 300 778 / 1516.
 constexpr int64_t kFewRowsOfTree = 64;
 
 bool blocks_take(const KvAttendArgs& a, int64_t keys) {
   const int64_t rows = a.max_q_len * (int64_t)(a.heads / a.cache.kv_heads);
-  if (a.cache.head_dim != 128 || rows <= kFewRowsOfTree || a.num_seqs > 1024) return false;
+  if (a.cache.head_dim != 128 || rows <= kFewRowsOfTree || a.num_seqs > 256) return false;
   const int64_t work = (rows + 31) / 32 * a.cache.kv_heads * a.num_seqs * keys;
   return a.num_seqs > 1 ? work >= 1 << 19 : work > 1 << 20;
 }
