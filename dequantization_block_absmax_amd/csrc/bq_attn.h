@@ -1,4 +1,4 @@
-// bq_attn.h -- device helpers shared by the attention kernels (k_attn.hip, k_attn_chunk.hip, k_attn_merge.hip).
+// bq_attn.h -- device helpers shared by the attention kernels (bq_attend.h, k_attn_chunk.hip, k_attn_merge.hip, k_tree.hip).
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -125,7 +125,7 @@ constexpr int kMaxSplits = 64;
 
 // Which sequences a launch takes.  A call whose sequences may bring many rows to a key/value head goes
 // through two sets of kernels: those of k_attn_chunk.hip for sequences with more than kFewRows rows (any, if
-// it is the only one), and the splitting kernel of k_attn.hip for the others.  Its grid has room for kFewRows rows of
+// it is the only one), and the splitting kernel of bq_attend.h for the others.  Its grid has room for kFewRows rows of
 // every sequence, so more of them cost calls in which most bring one (48 single tokens beside 200 of one
 // prompt, 32 heads over 8 of 128: 139 us, 180 with 64 rows, 265 with 128) and gain little elsewhere (the ragged
 // batch of 9: 69, 71, 73).

@@ -10,7 +10,7 @@
 
 namespace bq {
 
-// A paged key/value cache as the kernels take it (k_kv.hip, k_attn.hip): index 0 the keys, 1 the
+// A paged key/value cache as the kernels take it (k_kv.hip, bq_attend.h): index 0 the keys, 1 the
 // values.
 struct KvCacheArgs {
   uint8_t* packed[2];
@@ -53,7 +53,7 @@ struct KvAcceptArgs {
 };
 int launch_kv_accept(const KvAcceptArgs& a, void* stream);
 
-// Attention over the cache (k_attn.hip).
+// Attention over the cache (k_attn.hip, bq_attend.h).
 struct KvAttendArgs {
   KvCacheArgs cache;
   const int32_t *q_start, *kv_len, *page_table;

@@ -27,7 +27,7 @@
 // What is rounded.  K', V' and the weights to binary16, each 2^-11 at most; with q in bfloat16 that is a fraction of the
 // result's own rounding.  With q in binary16 (kFine) it would be four times that rounding (8.5e-4 of the result's
 // norm against 2.1e-4), the keys most of it, and a sequence's bits would depend on whether a long piece stands
-// beside it in the call, since k_attn.hip keeps two parts of its operands.  So what rounding left of K'
+// beside it in the call, since bq_attend.h keeps two parts of its operands.  So what rounding left of K'
 // follows in 6 bits, multiplied with q in 6 bits by v_mfma_scale_f32_32x32x64_f8f6f4 (an eighth more time on the
 // matrix cores, 3/8 more key bytes), and what it left of the weights as a second binary16 product with the same V'.  V' stays
 // once rounded, as bq_kv_read in that type gives it: 3.0e-4, sqrt(2) times the result's own rounding.
