@@ -88,10 +88,14 @@ __global__ __launch_bounds__(64 * kWaves) void merge_few_kernel(KvAttendArgs aa,
   float top = -INFINITY;
 #pragma unroll 4
   for (int s = 0; s < src.nsplit; ++s) top = fmaxf(top, src.parts[s].m);
+  // The splits of a tree's rows that are there stand first, and there may be room for many more.
+  int n = src.nsplit;
+  if (aa.parents != nullptr)
+    while (n > 0 && src.parts[n - 1].m == -INFINITY) --n;
   float l = 0.0f, exact = 0.0f;
   f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 4
-  for (int s = 0; s < src.nsplit; ++s) {
+  for (int s = 0; s < n; ++s) {
     const Partial p = src.parts[s];
     const f32x4 x = *reinterpret_cast<const f32x4*>(src.sums + (int64_t)s * D + d);
     const bool some = p.m != -INFINITY;  // where there is nothing the sums may not have been written
@@ -136,18 +140,23 @@ __global__ __launch_bounds__(64 * kWaves) void merge_kernel(KvAttendArgs aa, Mer
   for (int k = 0; k < kPer; ++k) v[k] = 0.0f;
   // splits past the last repeat it with weight zero, so that no load sits under a condition
   constexpr int kFlight = D <= 128 ? 8 : 4;
-  for (int s0 = wave; s0 < src.nsplit; s0 += kFlight * kWaves) {
+  int n = src.nsplit;
+  if (aa.parents != nullptr) {  // as above
+    const uint64_t there = __ballot(mine.m != -INFINITY);
+    n = there != 0 ? 64 - __builtin_clzll(there) : 0;
+  }
+  for (int s0 = wave; s0 < n; s0 += kFlight * kWaves) {
     float x[kFlight][kPer];
 #pragma unroll
     for (int i = 0; i < kFlight; ++i) {
-      const float* at_split = src.sums + (int64_t)min(s0 + i * kWaves, src.nsplit - 1) * D + lane * kPer;
+      const float* at_split = src.sums + (int64_t)min(s0 + i * kWaves, n - 1) * D + lane * kPer;
 #pragma unroll
       for (int k = 0; k < kPer; ++k) x[i][k] = at_split[k];
     }
 #pragma unroll
     for (int i = 0; i < kFlight; ++i) {
       const int s = s0 + i * kWaves;
-      const float fs = s < src.nsplit ? bits_f32(__builtin_amdgcn_readlane(f32_bits(f), min(s, 63))) : 0.0f;
+      const float fs = s < n ? bits_f32(__builtin_amdgcn_readlane(f32_bits(f), min(s, 63))) : 0.0f;
 #pragma unroll
       for (int k = 0; k < kPer; ++k) v[k] = fmaf(fs, fs != 0.0f ? x[i][k] : 0.0f, v[k]);
     }
