@@ -19,9 +19,9 @@
 // What bounds it.  Nothing alone: in the steady state a tile takes about 3900 cycles of a compute unit, of which the matrix cores have
 // work for 1024, LDS for about 1800 and the vector units for about 2200; decoding alone, without the products, took 129 us of 188 in
 // the first case below and 179 of 266 in the third (before two of its waves looked a tile ahead).  On MI355X, a call's time:
-//   24 drafts of up to 32 tokens over up to 8192 keys, 32 heads over 8, 4-bit, B = 64, bf16: 153 us with its join, 358 TFLOP/s
-//   2 of 48 over up to 131072, 16 over 2, 8-bit, B = 128, f16: 180 us, 379 TFLOP/s
-//   2 of 256 over up to 18432, 32 over 4, 4-bit, B = 64, bf16: 216 us, 492 TFLOP/s
+//   24 drafts of up to 32 tokens over up to 8192 keys, 32 heads over 8, 4-bit, B = 64, bf16: 148 us with its join, 369 TFLOP/s
+//   2 of 48 over up to 131072, 16 over 2, 8-bit, B = 128, f16: 175 us, 390 TFLOP/s
+//   2 of 256 over up to 18432, 32 over 4, 4-bit, B = 64, bf16: 210 us, 505 TFLOP/s
 // Other forms, same cases: four waves that decode between their own products, two workgroups to a compute unit, 155, 272 and 232 us;
 // all eight waves in both roles with keys held in registers spilled; loads four tiles ahead instead of one 189, 194 and 268 against
 // 188, 188 and 266; one workgroup to each run of a fixed length, without numbering, 169, 354 and 210.
