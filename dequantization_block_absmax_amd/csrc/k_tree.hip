@@ -24,7 +24,9 @@
 //   2 of 256 over up to 18432, 32 over 4, 4-bit, B = 64, bf16: 210 us, 505 TFLOP/s
 // Other forms, same cases: four waves that decode between their own products, two workgroups to a compute unit, 155, 272 and 232 us;
 // all eight waves in both roles with keys held in registers spilled; loads four tiles ahead instead of one 189, 194 and 268 against
-// 188, 188 and 266; one workgroup to each run of a fixed length, without numbering, 169, 354 and 210.
+// 188, 188 and 266; one workgroup to each run of a fixed length, without numbering, 169, 354 and 210.  Against today's
+// 148, 175 and 210: the decoding waves at a higher priority 158, 181 and 228, the others at one no change; a half's first operands asked for
+// at the end of the half before 148, 259 (registers spilled) and 210.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
@@ -44,7 +46,6 @@ constexpr int kThreads = 512;  // four waves with 32 rows each, and four that de
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef _Float16 f16x32 __attribute__((ext_vector_type(32)));
-typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
 typedef int i32x6 __attribute__((ext_vector_type(6)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 

@@ -214,3 +214,36 @@ def test_replays_and_streams(dev):
         torch.cuda.synchronize()
         assert torch.equal(outs[0], eager) and torch.equal(outs[1], other)
         compare(eager, eager_lse, *reference(pool, batch, now, q, "bfloat16", 0.088), k)
+
+
+@pytest.mark.parametrize("bound", [None, BOUND])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_no_keys_and_rows_elsewhere(dev, dim, bound):
+    """Drafts of sequences without a key; rows before the first sequence and between its rows of out stay as they were."""
+    rng = np.random.default_rng(dim)
+    lens = [(5, 0), (70, 0), (0, 0), (33, 20), (40, 40), (12, 500)]
+    pool, batch, parents, q = make(dev, rng, lens, 8, 2, dim, 64, 4, 16, "bfloat16", unused=0.1, bound=bound)
+    check_tree(dev, pool, batch, parents, q, "bfloat16", 0.1)
+    want, _ = run_tree(dev, pool, batch, parents, q, "bfloat16", 0.1)
+    shift = 7
+    wide_q = torch.zeros(batch.tokens + shift, 10, dim, dtype=q.dtype, device=dev)
+    wide_q[shift:, 1:9] = q
+    wide = torch.full((batch.tokens + shift, 11, dim), 77.0, dtype=q.dtype, device=dev)
+    lse = torch.full((batch.tokens + shift, 8), 77.0, device=dev)
+    starts = batch.dev[0] + shift
+    moved = bq.kv_batch(starts, batch.dev[1], batch.dev[2], batch.tokens + shift, batch.max_q, batch.max_kv)
+    size = bq.bq_kv_tree_attention_workspace_bytes(pool.cache, moved, bq.BQ_BF16, 8)
+    ws = torch.full((max(size, 16),), 0xFF, dtype=torch.uint8, device=dev)
+    par = torch.tensor([0] * shift + parents, dtype=torch.int64).to(torch.int32).to(dev)
+    bq.check(bq.bq_kv_tree_attention(pool.cache, moved, par, bq.BQ_BF16, wide_q[:, 1:9], wide_q.stride(0), 8, 0.1, 0, wide[:, 2:10],
+                                     wide.stride(0), lse, ws, size))
+    torch.cuda.synchronize()
+    assert torch.equal(wide[shift:, 2:10], want)
+    assert (wide[:shift] == 77.0).all() and (wide[:, :2] == 77.0).all() and (wide[:, 10] == 77.0).all() and (lse[:shift] == 77.0).all()
+
+
+@pytest.mark.parametrize("heads,kv_heads,dim", [(128, 1, 128), (64, 64, 128), (128, 1, 64), (96, 3, 256)])
+def test_many_heads(dev, heads, kv_heads, dim):
+    rng = np.random.default_rng(heads)
+    pool, batch, parents, q = make(dev, rng, [(256, 300), (3, 77)], heads, kv_heads, dim, 64, 4, 32, "bfloat16", unused=0.02)
+    check_tree(dev, pool, batch, parents, q, "bfloat16", dim ** -0.5)
