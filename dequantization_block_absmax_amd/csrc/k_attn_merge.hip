@@ -88,10 +88,11 @@ __global__ __launch_bounds__(64 * kWaves) void merge_few_kernel(KvAttendArgs aa,
   float top = -INFINITY;
 #pragma unroll 4
   for (int s = 0; s < src.nsplit; ++s) top = fmaxf(top, src.parts[s].m);
-  // The splits of a tree's rows that are there stand first, and there may be room for many more.
+  // The splits of a tree's rows that are there stand first, and there may be room for many more.  A split without a reference
+  // whose sum is not zero is there: the row's query was NaN.
   int n = src.nsplit;
   if (aa.parents != nullptr)
-    while (n > 0 && src.parts[n - 1].m == -INFINITY) --n;
+    while (n > 0 && src.parts[n - 1].m == -INFINITY && src.parts[n - 1].l == 0.0f) --n;
   float l = 0.0f, exact = 0.0f;
   f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 4
@@ -141,7 +142,7 @@ __global__ __launch_bounds__(64 * kWaves) void merge_kernel(KvAttendArgs aa, Mer
   // splits past the last repeat it with weight zero, so that no load sits under a condition
   constexpr int kFlight = D <= 128 ? 8 : 4;
   int n = src.nsplit;
-  if (aa.parents != nullptr) {  // as above
+  if (aa.parents != nullptr) {  // as above; a NaN among the weights' sums is in l already
     const uint64_t there = __ballot(mine.m != -INFINITY);
     n = there != 0 ? 64 - __builtin_clzll(there) : 0;
   }
