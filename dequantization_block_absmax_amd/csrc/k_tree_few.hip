@@ -49,19 +49,30 @@ int64_t most_splits(int64_t base, int64_t workgroups, int64_t units, int64_t lea
 }
 
 // Whether the kernel for many rows takes the call: it decodes a tile of keys once for 128 rows where the other does for 32, but
-// begins more slowly and with longer pieces.  `keys`: the longest sequence's that a row can see.  In us, this kernel / that of
-// k_tree.hip, with 32 heads over 8 in bfloat16 on 4-bit codes: one draft of 26 tokens over 1024 keys 15.0 / 21.2, over 16384
-// 31.2 / 37.6, over 65536 82.0 / 77.8; one of 256 over 4096 43.0 / 51.1, over 16384 136 / 122; 4 of 64 over 2048 25.9 / 32.9,
-// over 16384 93.7 / 77.2; 16 of 64 over 512 48.5 / 38.8.  With 64 rows (16 tokens) it is the faster one up to 65536 keys (48.7 /
-// 73.5), and with 16 sequences of 16384 too (124 / 158).  Past 256 sequences every workgroup's look at their lengths outweighs
-// what that gives: 256 of 26 over 1024 keys 399 / 401, 1024 of 20 over 300 778 / 1516.
+// begins more slowly and with longer pieces.  `keys`: the longest sequence's that a row can see.  What the other decodes (tiles of 32
+// rows x keys, twice as dear for 8-bit codes, whose lookups are one each, and for binary16, whose entries have two parts) is held against the
+// blocks of 128 rows: where they do not fill the device the keys of each are split further, and the longer pieces show.  In us, the
+// other kernel / that of k_tree.hip, 32 heads over 8, bfloat16 and 4-bit codes if not said otherwise, drafts of equal length:
+//   up to 64 blocks    1 of 64 tokens over 16384 keys 46 / 49, over 32768 77 / 70; 4 of 64 over 2048 28 / 39, over 16384 143 / 122;
+//                      binary16 4 of 64 over 2048 37 / 43, over 8192 117 / 94; 8-bit 4 of 64 over 2048 34 / 39, over 8192 101 / 83;
+//                      both, 16 heads over 2, 8 of 32 over 8192 82 / 64
+//   up to 128          12 of 32 over 1024 36 / 36, over 2048 61 / 46; 8 of 64 over 1024 37 / 40, over 4096 82 / 76
+//   more               16 of 64 over 512 54 / 44; 64 of 32 over 128 81 / 37; 8-bit 16 of 64 over 256 53 / 22
+// Blocks that 96 rows or fewer leave a quarter empty gain only until there are two for each compute unit (drafts and contexts of
+// up to and from a half and a quarter of these on): 128 of 17 tokens over 1024 134 / 178, over 8192 478 / 767, where 26 tokens take
+// 232 / 188 and 807 / 745.  With up to 64 rows (16 tokens) it is the other one up to 65536 keys (48.7 / 73.5), and with 16 sequences
+// of 16384 too (124 / 158).  Past 400 sequences every workgroup's look at their lengths outweighs the rest: 300 of 64 over 4096
+// 2063 / 1936, 400 2792 / 2849, 1000 of 64 over 1024 4225 / 6065.
 constexpr int64_t kFewRowsOfTree = 64;
 
-bool blocks_take(const KvAttendArgs& a, int64_t keys) {
-  const int64_t rows = a.max_q_len * (int64_t)(a.heads / a.cache.kv_heads);
-  if (a.cache.head_dim != 128 || rows <= kFewRowsOfTree || a.num_seqs > 256) return false;
-  const int64_t work = (rows + 31) / 32 * a.cache.kv_heads * a.num_seqs * keys;
-  return a.num_seqs > 1 ? work >= 1 << 19 : work > 1 << 20;
+bool blocks_take(const KvAttendArgs& a, int dtype, int64_t keys) {
+  const int64_t rows = a.max_q_len * (int64_t)(a.heads / a.cache.kv_heads), cus = cu_count();
+  if (a.cache.head_dim != 128 || rows <= kFewRowsOfTree || a.num_seqs > 400) return false;
+  const int64_t heads = (int64_t)a.cache.kv_heads * a.num_seqs;
+  const int64_t blocks = (rows + kTreeBlockRows - 1) / kTreeBlockRows * heads;
+  if (rows <= kTreeBlockRows * 3 / 4 && blocks > 2 * cus) return false;
+  const int64_t work = (rows + 31) / 32 * heads * keys * (dtype == F16 ? 2 : 1) * (a.bits == 8 ? 2 : 1);
+  return work >= (blocks > cus / 2 ? 1 << 17 : blocks > cus / 4 ? 3 << 18 : 3 << 19);
 }
 
 // The most keys that a row sees, where a window can leave some out.
@@ -166,11 +177,11 @@ hipError_t launch_few(const KvAttendArgs& a, const TreePlan& p, int dtype, const
 // The workspace is asked for without a window and holds for any, whichever form is the one with it.
 size_t kv_tree_workspace(const KvAttendArgs& a, int dtype) {
   const size_t few = std::max(make_plan(a, 1).bytes, make_plan(a, few_rows(a, a.max_kv_len)).bytes);
-  return blocks_take(a, a.max_kv_len) ? std::max(few, make_plan(a, kBlocks).bytes) : few;
+  return blocks_take(a, dtype, a.max_kv_len) ? std::max(few, make_plan(a, kBlocks).bytes) : few;
 }
 
 int launch_kv_tree(const KvAttendArgs& a, int dtype, const DequantArgs& da, void* stream) {
-  const TreePlan p = make_plan(a, blocks_take(a, keys_in_window(a)) ? kBlocks : few_rows(a, keys_in_window(a)));
+  const TreePlan p = make_plan(a, blocks_take(a, dtype, keys_in_window(a)) ? kBlocks : few_rows(a, keys_in_window(a)));
   if ((int64_t)p.tiles * p.nsplit > UINT32_MAX / 512 || a.cache.kv_heads > 32767 || (p.nsplit > 1 && !kv_merge_fits(a)) ||
       p.grid > UINT32_MAX / 512) {
     g_launch_refused_for_size = true;

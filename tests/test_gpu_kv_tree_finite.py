@@ -18,7 +18,7 @@ PLANS = {
     "few rows, several sequences": ([(12, 4000), (3, 90), (9, 2500)], 8, 2, None, (2, 16)),
     "few rows, many splits": ([(12, 30000)], 8, 2, None, (17, 64)),
     "many rows, whole": ([(250, 256), (256, 256)] + [(2, 40)] * 14, 64, 16, None, (1, 1)),
-    "many rows, few splits": ([(256, 5000)], 32, 8, None, (2, 16)),
+    "many rows, few splits": ([(256, 6200)], 32, 8, None, (2, 16)),
     "many rows, several sequences": ([(64, 1500), (40, 700)] + [(2, 50)] * 14, 64, 16, 2048, (2, 16)),
     "many rows, many splits": ([(40, 900), (33, 300)], 8, 2, BOUND, (17, 64)),
 }
