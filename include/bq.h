@@ -445,7 +445,8 @@ typedef struct {
  *              token whose slot is outside the pool has its queries rotated all the same.
  * q_out overlaps none of the inputs but q, and that not in part.
  * Errors: as bq_kv_write, and BQ_ERR_FORMAT (rotary_dim), BQ_ERR_SIZE (max_positions below 1, a stride too
- * short, heads, q_out == q with another stride). */
+ * short, heads, q_out == q with another stride, or a launch of more than 2^32 - 1 threads, each with
+ * 8 elements of the keys or values, or 8 to 64 of the queries). */
 bq_status bq_kv_append(const bq_kv_cache* cache, const bq_rotation* rotation, bq_dtype dtype, const void* k,
                        const void* v, int64_t tokens, int64_t k_stride, int64_t v_stride, const int64_t* positions,
                        const int64_t* slots, const void* q, int64_t q_stride, int32_t heads, void* q_out,
