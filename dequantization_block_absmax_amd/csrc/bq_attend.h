@@ -311,7 +311,9 @@ __device__ __forceinline__ void load_fence() {
 // workgroup: among the forms at the limit 64 wide with 32 rows and two blocks (24 x 6 tokens, 8-bit, windows of 4000, buffers
 // in turn: 38.1 us at four with 12 to 15 registers spilled, 35.9 at two with the weights' rests besides; bf16
 // 33.5 and 29.4) and 128 wide in 8 bits with two blocks (64 single tokens over up to 4096 keys, bf16: 100 us with 7
-// spilled, 90).  Of the others <128, 4, 8, 2> with q in binary16 spills one register.
+// spilled, 90).  Of the others <128, 4, 8, 2> and <64, 1, 8, 2> with q in binary16 spill one register.  What a
+// tree adds costs more: with q in binary16 <64, 1, 8, 2> spills 18, <64, 1, 4, 2> 14, <128, 4, 8, 2> 7 (in bfloat16 6), <64, 2, 4, 4> 6
+// and <128, 1, 8, 1> 4.
 constexpr bool wide_form(int head_dim, int nb, int bits, int rt) {
   return nb == 2 && rt * head_dim == 128 && (head_dim == 64 || bits == 8);
 }
@@ -339,7 +341,9 @@ struct TreeShared {
 struct NoTree {};
 
 // Fills the shared tree of a tile with the new tokens i_first .. i_last; `parent` is token tid's.  The last 256 threads, each
-// with a token of its own, follow its path to the root.  Every thread takes part; a barrier has to follow.
+// with a token of its own, follow its path to the root, a load from LDS for each ancestor: drafts level by level are a few deep, a chain of
+// 256 tokens takes some 20 us more in each workgroup (one over 1024 keys 41 us, a shallow tree of as many 19).  Every thread
+// takes part; a barrier has to follow.
 template <int THREADS, int ROWS>
 __device__ __forceinline__ void read_tree(const KvAttendArgs& aa, TreeShared<ROWS>& tree, int parent, int tid, int i_first,
                                           int i_last) {
@@ -396,7 +400,7 @@ __device__ __forceinline__ int from_lane(int v, int lane) { return __builtin_amd
 // Divides sequences of different lengths into parts of ROWS rows by a number of units of UNIT keys, from the ALIGN-th key that they
 // begin at.  Every part is as long as leaves each of `workgroups`, which the device holds at once, one, or half of that where
 // less then stands idle: a part costs its units and about `extra` more.  What is left over of each sequence is a part too.
-// With the kernel of k_tree.hip 24 sequences of 32 drafted tokens and up to 8192 keys take 152 us in halves and 173 in wholes, two
+// With the kernel of k_tree.hip 24 sequences of 32 drafted tokens and up to 8192 keys took 152 us in halves and 173 in wholes, two
 // of 48 and up to 131072 keys 196 and 185.  Parts are numbered in a row, since workgroups without one between the others would
 // leave compute units without work: the hardware deals them out in turn.  The lengths are known on the device only, so every
 // workgroup works this out, a lane to a sequence.  False: there is no such part.

@@ -5,7 +5,7 @@
 // places, then the wave loads all their bytes before it stores any.  The path ascends, so path[i] >= i, and what a
 // later piece reads (places from path[i + 1] on) no earlier one has written (places up to i).  A few KB to a
 // sequence: bound by the chain of loads, path to page to codes.  One sequence of 8 heads of 128, 4-bit: 3.9 us; 512 sequences, paths
-// of up to 9, 8-bit: 8.5 us.
+// of up to 9, 8-bit: 9.0 us.
 #include <hip/hip_runtime.h>
 
 #include "bq_attn.h"

@@ -12,9 +12,9 @@
 // and sines.
 //
 // What bounds it.  Few tokens: the launch (48 tokens, 32 heads over 8 of 128, bf16, 4-bit: 3.8 us).  Many: memory, beside the places
-// and searches of 8 elements that each lane works out: 16384 tokens, 32 over 8 of 128, bf16, 8-bit, B = 128: 91 us, 4.6 TB/s of
-// the projections read, queries and codes written (a large copy reaches 5.0); 4099, 15 over 5 of 64, fp32, 4-bit, half of each
-// head in neighbouring pairs: 13.0 us, 3.9 TB/s.
+// and searches of 8 elements that each lane works out: 16384 tokens, 32 over 8 of 128, bf16, 8-bit, B = 128: 91.6 us for 379 MB (projections
+// and angles read, queries and codes written), 4.1 TB/s where a large copy reaches 5.0; 4099, 15 over 5 of 64, fp32, 4-bit, half of each
+// head in neighbouring pairs: 12.5 us, 44 MB, 3.5 TB/s.
 #include <hip/hip_runtime.h>
 
 #include "bq_kv_device.h"

@@ -18,13 +18,15 @@
 //
 // What bounds it.  Nothing alone: in the steady state a tile takes about 3900 cycles of a compute unit, of which the matrix cores have
 // work for 1024, LDS for about 1800 and the vector units for about 2200; decoding alone, without the products, took 129 us of 188 in
-// the first case below and 179 of 266 in the third (before two of its waves looked a tile ahead).  On MI355X, a call's time:
-//   24 drafts of up to 32 tokens over up to 8192 keys, 32 heads over 8, 4-bit, B = 64, bf16: 148 us with its join, 369 TFLOP/s
-//   2 of 48 over up to 131072, 16 over 2, 8-bit, B = 128, f16: 175 us, 390 TFLOP/s
-//   2 of 256 over up to 18432, 32 over 4, 4-bit, B = 64, bf16: 210 us, 505 TFLOP/s
+// the first case below and 179 of 266 in the third (before two of its waves looked a tile ahead).  On MI355X, a call's time with its join
+// after some 30 ms of such calls (12% more in the first few, until the clock has risen), and the kernel's own:
+//   24 drafts of up to 32 tokens over up to 8192 keys, 32 heads over 8, 4-bit, B = 64, bf16: 150 us, 366 TFLOP/s; 138, 396
+//   2 of 48 over up to 131072, 16 over 2, 8-bit, B = 128, f16: 178 us, 383 TFLOP/s; 170, 402
+//   2 of 256 over up to 18432, 32 over 4, 4-bit, B = 64, bf16: 213 us, 499 TFLOP/s; 202, 526
+// With q in binary16 <128, 8> spills 16 registers and <128, 4> 10, in the loop.
 // Other forms, same cases: four waves that decode between their own products, two workgroups to a compute unit, 155, 272 and 232 us;
 // all eight waves in both roles with keys held in registers spilled; loads four tiles ahead instead of one 189, 194 and 268 against
-// 188, 188 and 266; one workgroup to each run of a fixed length, without numbering, 169, 354 and 210.  Against today's
+// 188, 188 and 266; one workgroup to each run of a fixed length, without numbering, 169, 354 and 210.  Against
 // 148, 175 and 210: the decoding waves at a higher priority 158, 181 and 228, the others at one no change; a half's first operands asked for
 // at the end of the half before 148, 259 (registers spilled) and 210.
 #include <hip/hip_runtime.h>

@@ -2,9 +2,9 @@
 // few rows to a key/value head (the kernel of bq_attend.h).
 //
 // That kernel's figures for trees, on MI355X: one draft of 26 tokens over 1026 keys, 32 heads over 8 of 128, 4-bit, B = 64, bf16:
-// 12.7 us and join 3.9, the chain of loads from the arguments to the keys and two launches; 20 of up to 13 over a window of
-// 4000, 20 over 5 of 64, 8-bit, B = 32, f16: 52 us with the join, 1.0 TB/s: 16 rows are decoded for at a time, vector units;
-// 5 of up to 21 over up to 6000, 8 over 1 of 256, 8-bit, B = 128, bf16: 32 us, 93 TFLOP/s: 11 row tiles decode the same keys.
+// 12.4 us and join 3.9, the chain of loads from the arguments to the keys and two launches; 20 of up to 13 over a window of
+// 4000, 20 over 5 of 64, 8-bit, B = 32, f16: 47 us and join 5.6, 1.0 TB/s: 16 rows are decoded for at a time, vector units;
+// 5 of up to 21 over up to 6000, 8 over 1 of 256, 8-bit, B = 128, bf16: 28 us and join 5.6, 88 TFLOP/s: 11 row tiles decode the same keys.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -62,7 +62,8 @@ int64_t most_splits(int64_t base, int64_t workgroups, int64_t units, int64_t lea
 // up to and from a half and a quarter of these on): 128 of 17 tokens over 1024 134 / 178, over 8192 478 / 767, where 26 tokens take
 // 232 / 188 and 807 / 745.  With up to 64 rows (16 tokens) it is the other one up to 65536 keys (48.7 / 73.5), and with 16 sequences
 // of 16384 too (124 / 158).  Past 400 sequences every workgroup's look at their lengths outweighs the rest: 300 of 64 over 4096
-// 2063 / 1936, 400 2792 / 2849, 1000 of 64 over 1024 4225 / 6065.
+// 2063 / 1936, 400 2792 / 2849, 1000 of 64 over 1024 4225 / 6065.  Where the rule is most wrong: 128 of 17 over 128 keys 115 / 57, and many
+// drafts over contexts of one length, whose parts just miss a round: 300 of 64 over 8192 5506 / 7963.
 constexpr int64_t kFewRowsOfTree = 64;
 
 bool blocks_take(const KvAttendArgs& a, int dtype, int64_t keys) {
@@ -86,7 +87,10 @@ constexpr int kBlocks = 0;  // in place of a number of rows / 16: the kernel of 
 // of them costs more than the tiles' number gives, and 1 for small calls, whose time is the chain from arguments to result.
 // With 16 rows, and with more, in us: 128 wide, 32 heads over 8, 4-bit codes, bfloat16: one draft of 26 tokens over 1000 keys 12.7 and
 // 15.2, over 4000 19.4 and 18.3, 8 of 6 over 1000 14.0 and 16.7, 8 of 13 over 8000 36.9 and 34.6; 64 wide, 20 heads over 5, 8-bit
-// codes, binary16: one of 13 over 1000 11.4 and 19.4, 20 of 13 over a window of 4000 56 and 61, 4 of 64 over 8000 60 and 52.
+// codes, binary16: one of 13 over 1000 11.4 and 19.4, 20 of 13 over a window of 4000 56 and 61, 4 of 64 over 8000 60 and 52.  Held
+// against 935 points of both types, 4 and 8 bits, 64 and 128 wide, 1 to 48 drafts of 5 to 64 tokens over 256 to 32768 keys, it loses 1.4 to 6.2% on
+// the mean of a form to the best number of rows; most where the workgroups just miss a round: 48 of 8 over 2048, 64 wide, 32 over 8, 4-bit,
+// bfloat16 64 where 32 rows take 31; 16 of 64 over 2048, 20 over 5, 8-bit, binary16 108 where 16 take 74.
 int few_rows(const KvAttendArgs& a, int64_t keys) {
   const int64_t D = a.cache.head_dim, rows = a.max_q_len * (int64_t)(a.heads / a.cache.kv_heads);
   const int64_t work = (rows + 15) / 16 * a.cache.kv_heads * a.num_seqs * keys;
