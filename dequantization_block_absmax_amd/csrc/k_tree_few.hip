@@ -49,31 +49,37 @@ int64_t most_splits(int64_t base, int64_t workgroups, int64_t units, int64_t lea
 }
 
 // Whether the kernel for many rows takes the call: it decodes a tile of keys once for 128 rows where the other does for 32, but
-// begins more slowly and with longer pieces.  `keys`: the longest sequence's that a row can see.  What the other decodes (tiles of 32
-// rows x keys, twice as dear for 8-bit codes, whose lookups are one each, and for binary16, whose entries have two parts) is held against the
-// blocks of 128 rows: where they do not fill the device the keys of each are split further, and the longer pieces show.  In us, the
-// other kernel / that of k_tree.hip, 32 heads over 8, bfloat16 and 4-bit codes if not said otherwise, drafts of equal length:
-//   up to 64 blocks    1 of 64 tokens over 16384 keys 46 / 49, over 32768 77 / 70; 4 of 64 over 2048 28 / 39, over 16384 143 / 122;
-//                      binary16 4 of 64 over 2048 37 / 43, over 8192 117 / 94; 8-bit 4 of 64 over 2048 34 / 39, over 8192 101 / 83;
-//                      both, 16 heads over 2, 8 of 32 over 8192 82 / 64
-//   up to 128          12 of 32 over 1024 36 / 36, over 2048 61 / 46; 8 of 64 over 1024 37 / 40, over 4096 82 / 76
-//   more               16 of 64 over 512 54 / 44; 64 of 32 over 128 81 / 37; 8-bit 16 of 64 over 256 53 / 22
-// Blocks that 96 rows or fewer leave a quarter empty gain only until there are two for each compute unit (drafts and contexts of
-// up to and from a half and a quarter of these on): 128 of 17 tokens over 1024 134 / 178, over 8192 478 / 767, where 26 tokens take
-// 232 / 188 and 807 / 745.  With up to 64 rows (16 tokens) it is the other one up to 65536 keys (48.7 / 73.5), and with 16 sequences
-// of 16384 too (124 / 158).  Past 400 sequences every workgroup's look at their lengths outweighs the rest: 300 of 64 over 4096
-// 2063 / 1936, 400 2792 / 2849, 1000 of 64 over 1024 4225 / 6065.  Where the rule is most wrong: 128 of 17 over 128 keys 115 / 57, and many
-// drafts over contexts of one length, whose parts just miss a round: 300 of 64 over 8192 5506 / 7963.
+// begins more slowly and with longer pieces, and rounds more in binary16.  `keys`: the longest sequence's that a row can see; never true
+// for fewer keys than it is false for (the workspace is asked for without a window).  It has to be a large call (`work`: tiles of 32 rows x
+// keys).  Where its blocks of 128 rows leave compute units over, the keys of each are split further and its longer pieces show, all the
+// more where the other kernel just fills the device; the other's lookups are dearer for 8-bit codes and for binary16, whose
+// entries have two parts.  In us, the other kernel / that of k_tree.hip, 32 heads over 8, bfloat16 and 4-bit codes if not said otherwise, drafts of
+// equal length on 256 compute units:
+//   one sequence       64 tokens over 16384 keys 46 / 49, over 32768 77 / 70; 256 over 4096 42 / 50, over 16384 133 / 118
+//   49 to 64 blocks    4 of 64 over 2048 28 / 39, over 4096 42 / 53, over 8192 73 / 76, over 16384 143 / 122; 8 of 32 over 2048 28 / 38;
+//                      binary16 4 of 64 over 2048 37 / 43, over 4096 63 / 60; 8-bit over 2048 34 / 39, over 4096 55 / 57, over 8192 101 / 83
+//   65 to 128          8 of 64 over 1024 37 / 40, over 2048 52 / 52, over 4096 82 / 76; 12 of 17 over 2048 58 / 43; 4 of 128 over 1024 36 / 40;
+//                      binary16 8 of 64 over 1024 47 / 44
+//   others             2 of 64 over 16384 80 / 75; 16 of 64 over 512 54 / 44; 24 of 32 over 2048 77 / 74
+// Blocks that 96 rows or fewer leave a quarter empty, two or more to each compute unit (drafts and contexts of up to these, from a half and
+// a quarter of them on): 65 of 17 tokens over 1024 73 / 101, 128 of 17 over 8192 478 / 767, binary16 and 8-bit 128 over 4096 464 / 563,
+// but over 300 97 / 101 and, of equal lengths, over 256 126 / 70; with 26 tokens 232 / 188 and 807 / 745.
+// With up to 64 rows (16 tokens) it is the other one up to 65536 keys (48.7 / 73.5), and with 16 sequences of 16384 too (124 /
+// 158).  Below its least work k_tree.hip is often the faster one too, most for 8-bit codes and short contexts in many
+// blocks (16 of 64 over 256 53 / 22), and past 256 sequences up to about 400 (300 of 64 over 4096 2063 / 1936; 1000 of 64 over 1024
+// 4225 / 6065): left to the kernel that rounds less.
 constexpr int64_t kFewRowsOfTree = 64;
 
 bool blocks_take(const KvAttendArgs& a, int dtype, int64_t keys) {
   const int64_t rows = a.max_q_len * (int64_t)(a.heads / a.cache.kv_heads), cus = cu_count();
-  if (a.cache.head_dim != 128 || rows <= kFewRowsOfTree || a.num_seqs > 400) return false;
+  if (a.cache.head_dim != 128 || rows <= kFewRowsOfTree || a.num_seqs > 256) return false;
   const int64_t heads = (int64_t)a.cache.kv_heads * a.num_seqs;
   const int64_t blocks = (rows + kTreeBlockRows - 1) / kTreeBlockRows * heads;
-  if (rows <= kTreeBlockRows * 3 / 4 && blocks > 2 * cus) return false;
-  const int64_t work = (rows + 31) / 32 * heads * keys * (dtype == F16 ? 2 : 1) * (a.bits == 8 ? 2 : 1);
-  return work >= (blocks > cus / 2 ? 1 << 17 : blocks > cus / 4 ? 3 << 18 : 3 << 19);
+  if (rows <= kTreeBlockRows * 3 / 4 && blocks > 2 * cus && a.max_kv_len > 512) return false;
+  const int64_t work = (rows + 31) / 32 * heads * keys;
+  if (a.num_seqs > 1 ? work < 1 << 19 : work <= 1 << 20) return false;
+  const int64_t dear = work * (dtype == F16 ? 2 : 1) * (a.bits == 8 ? 2 : 1);
+  return blocks > cus / 2 || blocks <= cus * 3 / 16 || dear > (blocks > cus / 4 ? 1 << 19 : 1 << 20);
 }
 
 // The most keys that a row sees, where a window can leave some out.

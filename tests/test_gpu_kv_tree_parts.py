@@ -52,3 +52,16 @@ def test_one_sequence_with_all_the_keys(dev, seqs):
         lens[at] = (16, 9000)
         pool, batch, parents, q = make(dev, rng, lens, 8, 2, 128, 64, 4, 16, "bfloat16", bound=None)
         check_tree(dev, pool, batch, parents, q, "bfloat16", 0.088, tag=at)
+
+
+@pytest.mark.parametrize("bound", [None, 300])
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
+def test_a_short_window_in_a_large_batch(dev, dtype, bound):
+    """Which kernel a call takes may depend on its window: the workspace that is asked for without one is enough."""
+    rng = np.random.default_rng(70)
+    most = bound or 700
+    lens = [(int(rng.integers(12, 21)), int(rng.integers(40, most))) for _ in range(70)]
+    lens[3] = (20, most)
+    pool, batch, parents, q = make(dev, rng, lens, 32, 8, 128, 64, 4, 16, dtype, unused=0.05, bound=None)
+    for window in (0, 9, 120):
+        check_tree(dev, pool, batch, parents, q, dtype, 0.088, window=window, tag=window)

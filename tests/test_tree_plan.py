@@ -26,3 +26,9 @@ def test_few_blocks_take_the_kernel_for_few_rows(seqs, nodes, keys):
 def test_many_blocks_take_the_kernel_for_many_rows(seqs, nodes, keys):
     assert splits(seqs, nodes, keys) == 2
 
+
+
+def test_blocks_that_few_rows_leave_part_empty():
+    """128 drafts of 17 tokens are 1024 blocks of 68 rows: the kernel for few rows, without splits.  128 of 26 are the other's."""
+    assert splits(128, 17, 8192) == 0
+    assert splits(128, 26, 8192) > 0
